@@ -446,6 +446,159 @@ linrec_status linrec_delta_bwd_seq(linrec_ctx* ctx, const linrec_desc* d, int32_
                                    linrec_tensor dbeta, float* dS_in, void* workspace,
                                    void* stream);
 
+/* ------------------------------------------------ elementwise recurrence
+ * Per batch b and channel c (one sub-sequence of T tokens):
+ *
+ *     h_0 = h_in,  h_t = a_t h_{t-1} + b_t,  a_t = exp(g_t),  h_out = h_T
+ *     LINREC_DIAG_PLAIN: b_t = x_t;   LINREC_DIAG_MIX: b_t = (1 - a_t) x_t
+ *
+ * the gated recurrence with a vector state, one gate per token and channel
+ * (the layer above has one gate per token and head and a matrix state).  The
+ * gate is given as its logarithm g <= 0, which keeps 1 - a exact to the
+ * storage type's relative precision when a is close to 1; g = -inf forgets
+ * everything before the token.  Pieces chain through h_out -> h_in and,
+ * backward, dh_in -> dh_out, as for the layer.
+ *
+ * Layouts: g, x, h, dh, dg, dx are [B, T, C] with element strides (sb, st)
+ * of a linrec_tensor (sh ignored), the channel index contiguous, every token
+ * row 16-byte aligned (strides of dimensions of size 1 are not looked at).
+ * h_in, h_out, dh_out, dh_in: contiguous fp32 [B, C].  Inputs share `dtype`,
+ * outputs `out_dtype` (LINREC_F32 when dtype is); the recurrence runs in fp32.
+ * 1 <= B <= 32767, 1 <= C <= 2^20, 0 <= T <= LINREC_MAX_T.  Rows of an output
+ * must not overlap (LINREC_E_LAYOUT).  T == 0 copies h_in to h_out (dh_out to
+ * dh_in) and does nothing else. */
+typedef enum { LINREC_DIAG_PLAIN = 0, LINREC_DIAG_MIX = 1 } linrec_diag_form;
+
+typedef struct {
+    int32_t B, T, C;
+    int32_t form;             /* linrec_diag_form */
+    int32_t dtype;            /* linrec_dtype of g, x, dh */
+    int32_t out_dtype;        /* linrec_dtype of h, dg, dx */
+} linrec_diag_desc;
+
+/* Bytes of the state store (0 if `d` is invalid or T == 0): the state
+ * entering every 256 tokens, fp32 [B, ceil(T/256), C], written by the forward
+ * and read by the backward of the same piece. */
+size_t linrec_diag_states_bytes(const linrec_diag_desc* d);
+
+/* Bytes of workspace linrec_diag_fwd and linrec_diag_bwd need (0 if `d` is
+ * invalid or T <= 256: then workspace may be NULL): per 256 tokens and channel
+ * the product of the gates and the sum of what the tokens add. */
+size_t linrec_diag_workspace_bytes(const linrec_diag_desc* d);
+
+/* Forward.  h_in: NULL means zeros.  h_out: required, may alias h_in.  states:
+ * linrec_diag_states_bytes(d) bytes.  Errors and ownership as linrec_fwd. */
+linrec_status linrec_diag_fwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec_tensor g,
+                              linrec_tensor x, const float* h_in, linrec_tensor h, float* h_out,
+                              void* states, void* workspace, void* stream);
+
+/* Backward, for L = <dh, h> + <dh_out, h_out>, from the forward's states:
+ *     G_t = dh_t + a_{t+1} G_{t+1}   (dh_out enters at t = T),
+ *     dx_t = G_t (plain) or (1 - a_t) G_t (mix),
+ *     dg_t = a_t G_t (h_{t-1} - [mix] x_t),   dh_in = a_1 G_1.
+ * dh_out: NULL means zeros.  dh_in: required, may alias dh_out.  dg may alias
+ * g and dx may alias x or dh (the same view: every element is read before it is
+ * written).  The states h_{t-1} are formed again in fp32 from the stored ones,
+ * not read from a rounded h. */
+linrec_status linrec_diag_bwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec_tensor g,
+                              linrec_tensor x, const void* states, linrec_tensor dh,
+                              const float* dh_out, linrec_tensor dg, linrec_tensor dx,
+                              float* dh_in, void* workspace, void* stream);
+
+/* ------------------------------------------------------------ token step
+ * The layer's recurrence and the delta rule, token by token, for generation:
+ *
+ *     beta.ptr == NULL:  S <- a_t S + k_t^T v_t
+ *     else:              S <- a_t (I - beta_t k_t^T k_t) S + beta_t k_t^T v_t
+ *     o_t = q_t S
+ *
+ * in fp32, with S updated in place in a pool of states, fp32 contiguous
+ * [nslots, H, d_k, d_v].  The state is read and written once per call; the T
+ * tokens run one after another on it (meant for one or a few tokens: a long
+ * piece is linrec_fwd's or linrec_delta_fwd's).  Layouts, dtypes and shapes as
+ * linrec_fwd (d_k, d_v in {64, 128} each; beta: fp32 [B,H,T] with strides).
+ *   slots: int32 [B] in device memory, or NULL (entry b uses state b; nslots
+ *   >= B).  Entry b uses the states slots[b]; an entry whose slot lies
+ *   outside [0, nslots), or occurs at an earlier entry, is skipped: its o is
+ *   zeros and no state changes.
+ * T == 0 does nothing.  Nothing is allocated and no workspace is needed, so
+ * the call can be captured into a graph. */
+linrec_status linrec_step(linrec_ctx* ctx, const linrec_desc* d, linrec_tensor q, linrec_tensor k,
+                          linrec_tensor v, linrec_tensor beta, linrec_tensor decay, float* S,
+                          const int32_t* slots, int32_t nslots, linrec_tensor o, void* stream);
+
+/* ------------------------------------------------- paged 8-bit key/value cache
+ * The softmax-attention layers of a hybrid model carry, from piece to piece
+ * and token to token, the keys and values of all earlier tokens.  The cache
+ * holds them as e4m3 codes with one scale per page and head:
+ *   k: [pages, H, page, D] bytes, v: [pages, H, D, page] bytes (a head's
+ *   tokens run along the row, so that a product over tokens reads 16 of them
+ *   at once); k_scale, v_scale: fp32 [pages, H]; all contiguous, k and v
+ *   16-byte aligned.  Value = code * scale.
+ *   table: int32 [B, max_pages] with row stride table_stride: token t of
+ *   sequence b lies in page table[b][t / page] at t % page.  An entry outside
+ *   [0, pages) is no page: its tokens are not written and not attended to.
+ * page in {16, 32, 64, 128}; D in {64, 128}; 1 <= H <= 65535.
+ * A call adds or attends from T new tokens per sequence, which follow past[b]
+ * tokens (int32 [B], device memory; negative counts as 0 tokens and no new
+ * ones); n_new: int32 [B], the first n_new[b] of the T (clamped to [0, T]) are
+ * there, or NULL: all.  Rows behind them are neither read nor written.
+ * Activations are LINREC_BF16, [B, H, T, D] linrec_tensors as above.
+ * Pages may be shared between sequences for reading. */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* table;
+    int64_t table_stride;
+    int32_t pages, page, max_pages;
+    int32_t H, D;             /* key/value heads, head width */
+} linrec_kv_cache;
+
+/* Append k, v [B,H,T,D] at positions past[b] + t, rotating keys (and, when q is
+ * given, queries q [B,Hq,T,D] into q_out) by their position on the way:
+ *   features (i, i + rot/2) of a head (interleaved: (2i, 2i+1)), i < rot/2,
+ *   turn by the angle (past[b] + t) * inv_freq[i]; inv_freq: fp64 [rot/2] in
+ *   device memory.  Angles are formed and reduced in fp64.  rot == 0: no
+ *   rotation (inv_freq ignored); else a multiple of 16, at most D.
+ * Scales: the least power of two s >= 2^-100 with max|x| <= 448 s over the
+ * page's new tokens, and no less than the scale the page has when it holds
+ * earlier tokens of the sequence (past[b] inside the page); those are then
+ * rescaled to s, exactly but for codes that become subnormal.  A page that is
+ * begun takes a new scale.  Values that are not finite do not enter the scale:
+ * infinities are stored as +-448 s, NaN as NaN.
+ * A page named more than once among the pages that the call writes is written
+ * for the first (lowest b, then lowest token) alone.  Tokens at or past
+ * max_pages * page are dropped.
+ *   q.ptr == NULL: no queries (Hq, q_out ignored).  q_out may be q. */
+linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache* cache, int32_t B, int32_t T,
+                               linrec_tensor k, linrec_tensor v, const int32_t* past,
+                               const int32_t* n_new, const double* inv_freq, int32_t rot,
+                               int32_t interleaved, int32_t Hq, linrec_tensor q,
+                               linrec_tensor q_out, void* stream);
+
+/* Bytes of workspace linrec_kv_attn needs (0 if the arguments are invalid or
+ * none is needed: then workspace may be NULL). */
+size_t linrec_kv_attn_workspace_bytes(const linrec_kv_cache* cache, int32_t B, int32_t T,
+                                      int32_t Hq);
+
+/* Attention of the T tokens over the cache, which holds them already
+ * (linrec_kv_append).  Query head h reads key/value head h / (Hq / H):
+ *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j - lse_i),
+ * over the cached tokens j with past[b] + i - window < j <= past[b] + i
+ * (window <= 0: no lower bound).  lse: fp32 contiguous [B,Hq,T], the natural
+ * logarithm of the sum, or NULL.  A row that sees no token gets o = 0 and
+ * lse = -inf.  Cached values that a row does not see never reach it, whatever
+ * they are.  Hq: a multiple of cache->H.  scale: finite.
+ * The result does not depend on what else is in the batch beyond the choice of
+ * the split (a function of B, T, Hq and the cache's sizes), and repeats bit for
+ * bit. */
+linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int32_t B, int32_t T,
+                             int32_t Hq, linrec_tensor q, const int32_t* past,
+                             const int32_t* n_new, float scale, int32_t window, linrec_tensor o,
+                             float* lse, void* workspace, void* stream);
+
 /* Kernel kinds for linrec_ctx_kernel_times(). */
 enum {
     LINREC_KERNEL_FWD_SUM = 0,    /* forward segment sums (parallel)           */
@@ -457,7 +610,12 @@ enum {
     LINREC_KERNEL_DA_FINISH = 6,  /* decay gradient, last step                 */
     LINREC_KERNEL_DELTA_FWD = 7,  /* delta rule forward (each launch of a piece's kernels) */
     LINREC_KERNEL_DELTA_BWD = 8,  /* delta rule backward (each launch of a piece's kernels) */
-    LINREC_KERNEL_KINDS = 9
+    LINREC_KERNEL_DIAG_FWD = 9,   /* elementwise recurrence forward (each call's kernels)  */
+    LINREC_KERNEL_DIAG_BWD = 10,  /* elementwise recurrence backward (each call's kernels) */
+    LINREC_KERNEL_STEP = 11,      /* token step                                */
+    LINREC_KERNEL_KV_APPEND = 12, /* append to the paged cache                 */
+    LINREC_KERNEL_KV_ATTN = 13,   /* attention over the paged cache (each call's kernels) */
+    LINREC_KERNEL_KINDS = 14
 };
 
 /* Per-kernel timing (instrumentation, off by default).  While enabled, every

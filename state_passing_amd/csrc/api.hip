@@ -12,35 +12,25 @@
 #include <new>
 #include <vector>
 
+#include "ctx.hpp"
 #include "launch.hpp"
 #include "linrec.h"
 
+using linrec::aligned;
 using linrec::BwdIntraLaunch;
+using linrec::check_act;
+using linrec::check_buffer;
+using linrec::check_ctx;
+using linrec::check_decay;
+using linrec::check_desc;
+using linrec::check_state_ptr;
 using linrec::DaFinishLaunch;
+using linrec::elem_size;
 using linrec::FwdIntraLaunch;
+using linrec::hip_fail;
 using linrec::ScanLaunch;
 using linrec::TensorArg;
-
-struct TimedLaunch {
-    int kind;
-    hipEvent_t begin, end;
-};
-
-struct linrec_ctx {
-    int device;
-    void* scratch;          // this device's address of the no-allocation scratch
-    hipError_t scratch_err; // result of looking that address up
-    hipStream_t aux;        // state transitions
-    hipEvent_t ev_start;    // inputs ready on the caller's stream
-    hipEvent_t ev_scan;     // a piece's scan finished (aux)
-    hipEvent_t ev_slot[2];  // a workspace slot's last reader finished (aux)
-    // opt-in per-kernel timing (linrec_ctx_set_timing)
-    int timing;
-    std::vector<TimedLaunch> pending;
-    std::vector<hipEvent_t> pool;
-    double ms[LINREC_KERNEL_KINDS];
-    int64_t count[LINREC_KERNEL_KINDS];
-};
+using linrec::timed_launch;
 
 // Scratch of linrec_bwd_noalloc: the gradient records of one piece.  Each
 // GPU the library runs on holds its own copy for the life of the process.
@@ -49,103 +39,17 @@ struct linrec_ctx {
 // hipGetSymbolAddress (ctx->scratch).
 static __device__ __align__(256) unsigned char scratch[LINREC_NOALLOC_SCRATCH_BYTES];
 
+thread_local int linrec::g_last_hip_error = 0;
+
 namespace {
 
-thread_local int g_last_hip_error = 0;
-
-constexpr int kChunk = 64;
+using linrec::kChunk;
 // Chunks per segment: the segment kernels rebuild every per-chunk state of a
 // segment in registers; only the state at each segment boundary is stored.
 constexpr int kSegChunks = 4;
 
 int64_t chunks_of(int64_t tokens) { return (tokens + kChunk - 1) / kChunk; }
 int64_t nseg_of(int64_t tokens) { return (chunks_of(tokens) + kSegChunks - 1) / kSegChunks; }
-
-linrec_status hip_fail(hipError_t e, linrec_status code)
-{
-    g_last_hip_error = (int)e;
-    return code;
-}
-
-int elem_size(int dtype) { return dtype == LINREC_BF16 ? 2 : 4; }
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-
-linrec_status check_desc(const linrec_desc* d)
-{
-    if (!d)
-        return LINREC_E_NULL;
-    if (d->dtype != LINREC_BF16 && d->dtype != LINREC_F32)
-        return LINREC_E_DTYPE;
-    // B: the sequence backward's launches carry another piece's segment sums
-    // as a second set of grid rows z, so 2 B must fit the grid's 65535
-    if (d->chunk != kChunk || d->B < 1 || d->H < 1 || d->B > 32767 || d->H > 65535 || d->T < 0 ||
-        d->T > LINREC_MAX_T)
-        return LINREC_E_SHAPE;
-    if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128))
-        return LINREC_E_SHAPE;
-    if (d->out_dtype != LINREC_BF16 && d->out_dtype != LINREC_F32)
-        return LINREC_E_DTYPE;
-    if (d->dtype == LINREC_F32 && (d->dk != 64 || d->dv != 64 || d->out_dtype != LINREC_F32))
-        return LINREC_E_DTYPE;
-    if (d->decay != LINREC_DECAY_NONE && d->decay != LINREC_DECAY_HEAD &&
-        d->decay != LINREC_DECAY_TOKEN)
-        return LINREC_E_LAYOUT;
-    return LINREC_OK;
-}
-
-// An activation view: 16-byte aligned rows, non-negative strides, rows at
-// least `width` elements apart.
-linrec_status check_act(const linrec_tensor& t, int width, int esz)
-{
-    if (!t.ptr)
-        return LINREC_E_NULL;
-    if (t.sb < 0 || t.sh < 0 || t.st < width)
-        return LINREC_E_LAYOUT;
-    if (!aligned(t.ptr, 16) || (t.st * esz) % 16 || (t.sh * esz) % 16 || (t.sb * esz) % 16)
-        return LINREC_E_ALIGN;
-    return LINREC_OK;
-}
-
-linrec_status check_decay(const linrec_desc* d, const linrec_tensor& a)
-{
-    if (d->decay == LINREC_DECAY_NONE)
-        return LINREC_OK;
-    if (!a.ptr)
-        return LINREC_E_NULL;
-    if (!aligned(a.ptr, 4))
-        return LINREC_E_ALIGN;
-    if (a.sh < 0 || (d->decay == LINREC_DECAY_TOKEN && (a.sb < 0 || a.st < 0)))
-        return LINREC_E_LAYOUT;
-    return LINREC_OK;
-}
-
-linrec_status check_state_ptr(const void* p, bool required)
-{
-    if (!p)
-        return required ? LINREC_E_NULL : LINREC_OK;
-    return aligned(p, 4) ? LINREC_OK : LINREC_E_ALIGN;
-}
-
-linrec_status check_buffer(const void* p)
-{
-    if (!p)
-        return LINREC_E_WORKSPACE;
-    return aligned(p, 16) ? LINREC_OK : LINREC_E_WORKSPACE;
-}
-
-linrec_status check_ctx(linrec_ctx* ctx)
-{
-    if (!ctx)
-        return LINREC_E_NULL;
-    int cur = -1;
-    hipError_t e = hipGetDevice(&cur);
-    if (e != hipSuccess)
-        return hip_fail(e, LINREC_E_DEVICE);
-    if (cur != ctx->device)
-        return hip_fail(hipErrorInvalidDevice, LINREC_E_DEVICE);
-    return LINREC_OK;
-}
 
 linrec_status check_pieces(const linrec_desc* d, int32_t npieces, const int32_t* lengths)
 {
@@ -369,53 +273,6 @@ linrec::SumArg sum_arg_of(const ScanLaunch& sc)
     a.nseg = (sc.N + sc.m - 1) / sc.m;
     return a;
 }
-
-hipError_t pool_event(linrec_ctx* ctx, hipEvent_t* ev)
-{
-    if (!ctx->pool.empty()) {
-        *ev = ctx->pool.back();
-        ctx->pool.pop_back();
-        return hipSuccess;
-    }
-    // no system-scope release at the event: it would write back L2 after
-    // the bracketed kernel and bill that to the kernel's duration
-    return hipEventCreateWithFlags(ev, hipEventDisableSystemFence);
-}
-
-// Launch `fn` on `stream`; with timing on, the kernels it launches carry a pair
-// of events as their own start and end stamps (launch_kernel).
-template <typename F>
-hipError_t timed_launch(linrec_ctx* ctx, int kind, hipStream_t stream, F fn)
-{
-    if (!ctx->timing)
-        return fn();
-    TimedLaunch t{kind, nullptr, nullptr};
-    hipError_t e = pool_event(ctx, &t.begin);
-    if (e == hipSuccess)
-        e = pool_event(ctx, &t.end);
-    if (e == hipSuccess) {
-        // the events become the launched kernels' own start and end stamps
-        linrec::launch_stamps() = linrec::LaunchStamps{t.begin, t.end};
-        e = fn();
-        linrec::launch_stamps() = linrec::LaunchStamps{};
-    }
-    if (e != hipSuccess) {
-        if (t.begin)
-            ctx->pool.push_back(t.begin);
-        if (t.end)
-            ctx->pool.push_back(t.end);
-        return e;
-    }
-    ctx->pending.push_back(t);
-    return hipSuccess;
-}
-
-#define LAUNCH(call)                                              \
-    do {                                                          \
-        hipError_t e_ = (call);                                   \
-        if (e_ != hipSuccess)                                     \
-            return hip_fail(e_, LINREC_E_LAUNCH);                 \
-    } while (0)
 
 // The state transition of a piece: segment sum, then fold.
 #define LAUNCH_SCAN(ctx, desc, stream)                                                       \
@@ -1179,7 +1036,7 @@ const char* linrec_status_str(linrec_status s)
     return "unknown status";
 }
 
-int linrec_last_hip_error(void) { return g_last_hip_error; }
+int linrec_last_hip_error(void) { return linrec::g_last_hip_error; }
 
 int linrec_version(void) { return 100; }
 

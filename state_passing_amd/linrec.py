@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -49,10 +49,16 @@ EXPORTS = (
     "linrec_delta_bwd_workspace_bytes", "linrec_delta_bwd", "linrec_delta_seq_saved_bytes",
     "linrec_delta_fwd_seq_workspace_bytes", "linrec_delta_bwd_seq_workspace_bytes",
     "linrec_delta_fwd_seq", "linrec_delta_bwd_seq",
+    "linrec_diag_states_bytes", "linrec_diag_workspace_bytes", "linrec_diag_fwd", "linrec_diag_bwd",
+    "linrec_step", "linrec_kv_append", "linrec_kv_attn_workspace_bytes", "linrec_kv_attn",
 )
 
 KERNEL_KINDS = {0: "fwd_sum", 1: "fwd_fold", 2: "fwd_seg", 3: "bwd_sum", 4: "bwd_fold",
-                5: "bwd_seg", 6: "da_finish", 7: "delta_fwd", 8: "delta_bwd"}
+                5: "bwd_seg", 6: "da_finish", 7: "delta_fwd", 8: "delta_bwd", 9: "diag_fwd",
+                10: "diag_bwd", 11: "step", 12: "kv_append", 13: "kv_attn"}
+
+# Forms of the elementwise recurrence (linrec_diag_form).
+DIAG_FORMS = {"plain": 0, "mix": 1}
 
 
 class LinrecError(RuntimeError):
@@ -75,6 +81,18 @@ class Desc(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32)]
 
 
+class DiagDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("form", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
 _LIB = None
 
 
@@ -87,7 +105,7 @@ def _lib():
                            "(python -m state_passing_amd.build)")
     lib = ctypes.CDLL(LIB_PATH)
     P, T, D = ctypes.c_void_p, Tensor, ctypes.POINTER(Desc)
-    I32 = ctypes.c_int32
+    I32, DD, KC = ctypes.c_int32, ctypes.POINTER(DiagDesc), ctypes.POINTER(KvCacheDesc)
     sig = {
         "linrec_ctx_create": ([ctypes.POINTER(P), ctypes.c_int], ctypes.c_int),
         "linrec_ctx_destroy": ([P], ctypes.c_int),
@@ -115,6 +133,15 @@ def _lib():
         "linrec_bwd_da": ([P, D, T, T, T, T, P, T, P, T, T, T, P, T, P, P, P, P], ctypes.c_int),
         "linrec_fwd_seq": ([P, D, I32, P, T, T, T, T, P, T, P, P, P], ctypes.c_int),
         "linrec_bwd_seq": ([P, D, I32, P, T, T, T, T, P, T, P, T, T, T, P, P, P], ctypes.c_int),
+        "linrec_diag_states_bytes": ([DD], ctypes.c_size_t),
+        "linrec_diag_workspace_bytes": ([DD], ctypes.c_size_t),
+        "linrec_diag_fwd": ([P, DD, T, T, P, T, P, P, P, P], ctypes.c_int),
+        "linrec_diag_bwd": ([P, DD, T, T, P, T, P, T, T, P, P, P], ctypes.c_int),
+        "linrec_step": ([P, D, T, T, T, T, T, P, P, I32, T, P], ctypes.c_int),
+        "linrec_kv_append": ([P, KC, I32, I32, T, T, P, P, P, I32, I32, I32, T, T, P], ctypes.c_int),
+        "linrec_kv_attn_workspace_bytes": ([KC, I32, I32, I32], ctypes.c_size_t),
+        "linrec_kv_attn": ([P, KC, I32, I32, I32, T, P, P, ctypes.c_float, I32, T, P, P, P],
+                           ctypes.c_int),
         "linrec_status_str": ([ctypes.c_int], ctypes.c_char_p),
         "linrec_last_hip_error": ([], ctypes.c_int),
         "linrec_version": ([], ctypes.c_int),
@@ -789,6 +816,297 @@ def delta_bwd_seq(q, k, v, beta, decay, lengths: Sequence[int], saved, dO, dS_ou
                                      _ptr(workspace), _stream(q.device))
     _check(rc, "linrec_delta_bwd_seq")
     return dq, dk, dv, dbeta, dS_in
+
+
+# ----------------------------------------------------------------- elementwise recurrence
+
+def diag_desc(B, T, C, form, dtype_code, out_code=None) -> DiagDesc:
+    return DiagDesc(B, T, C, form, dtype_code, dtype_code if out_code is None else out_code)
+
+
+def diag_states_bytes(d: DiagDesc) -> int:
+    return int(_lib().linrec_diag_states_bytes(ctypes.byref(d)))
+
+
+def diag_workspace_bytes(d: DiagDesc) -> int:
+    return int(_lib().linrec_diag_workspace_bytes(ctypes.byref(d)))
+
+
+def _rows(t: torch.Tensor) -> Tensor:
+    s = t.stride()
+    return Tensor(t.data_ptr(), s[0], 0, s[1])
+
+
+def _check_rows(name, t, shape, dtype):
+    if not isinstance(t, torch.Tensor):
+        _fail(f"{name}: expected a tensor", TypeError)
+    if t.shape != shape:
+        _fail(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype != dtype:
+        _fail(f"{name}: dtype {t.dtype} != {dtype}", TypeError)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        _fail(f"{name}: the channel dimension must be contiguous (stride 1)")
+
+
+def _diag_setup(g, x, form, out_dtype, outs, carries):
+    """Checks of a diag call; returns (desc, output dtype)."""
+    if not isinstance(g, torch.Tensor) or g.dim() != 3:
+        _fail("g: must be a [B,T,C] tensor")
+    if form not in DIAG_FORMS:
+        _fail(f"form: {form!r} is none of {sorted(DIAG_FORMS)}")
+    if g.dtype not in (torch.bfloat16, torch.float32):
+        _fail(f"unsupported activation dtype {g.dtype}", TypeError)
+    _check_rows("g", g, g.shape, g.dtype)
+    _check_rows("x", x, g.shape, g.dtype)
+    odts = {t.dtype for _, t in outs if isinstance(t, torch.Tensor)}
+    if len(odts) > 1:
+        _fail(f"outputs must share one dtype, got {sorted(map(str, odts))}", TypeError)
+    odt = odts.pop() if odts else (g.dtype if out_dtype is None else out_dtype)
+    if odt not in (torch.bfloat16, torch.float32):
+        _fail(f"unsupported output dtype {odt}", TypeError)
+    for name, t in outs:
+        if t is not None:
+            _check_rows(name, t, g.shape, odt)
+    B, T, C = g.shape
+    for name, t in carries:
+        _check_state(name, t, torch.Size((B, C)))
+    return diag_desc(B, T, C, DIAG_FORMS[form], BF16 if g.dtype == torch.bfloat16 else F32,
+                     BF16 if odt == torch.bfloat16 else F32), odt
+
+
+def _bytes(n, device):
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def diag_fwd(g, x, h_in=None, *, form="plain", h=None, h_out=None, states=None, workspace=None,
+             out_dtype=None):
+    """Elementwise gated recurrence over one piece (linrec_diag_fwd):
+    h_t = exp(g_t) h_{t-1} + b_t per channel, b = x ("plain") or
+    (1 - exp(g)) x ("mix"); g, x: [B,T,C], h_in, h_out: fp32 [B,C].
+    Returns (h, h_out, states); states is what diag_bwd needs."""
+    d, odt = _diag_setup(g, x, form, out_dtype, (("h", h),), (("h_in", h_in), ("h_out", h_out)))
+    need, work = diag_states_bytes(d), diag_workspace_bytes(d)
+    if states is not None:
+        _check_buffer("states", states, need)
+    if workspace is not None:
+        _check_buffer("workspace", workspace, work)
+    _check_device(g, ("x", x), ("h_in", h_in), ("h", h), ("h_out", h_out), ("states", states),
+                  ("workspace", workspace))
+    dev = g.device
+    if h is None:
+        h = torch.empty(g.shape, dtype=odt, device=dev)
+    if h_out is None:
+        h_out = torch.empty(g.shape[0], g.shape[2], dtype=torch.float32, device=dev)
+    if states is None:
+        states = _bytes(need, dev)
+    if workspace is None and work:
+        workspace = _bytes(work, dev)
+    rc = _lib().linrec_diag_fwd(context(dev.index), ctypes.byref(d), _rows(g), _rows(x), _ptr(h_in),
+                                _rows(h), _ptr(h_out), _ptr(states), _ptr(workspace), _stream(dev))
+    _check(rc, "linrec_diag_fwd")
+    return h, h_out, states
+
+
+def diag_bwd(g, x, states, dh, dh_out=None, *, form="plain", dg=None, dx=None, dh_in=None,
+             workspace=None, out_dtype=None):
+    """Backward of diag_fwd over one piece (linrec_diag_bwd), from its states,
+    for the loss <dh, h> + <dh_out, h_out>.  Returns (dg, dx, dh_in)."""
+    d, odt = _diag_setup(g, x, form, out_dtype, (("dg", dg), ("dx", dx)),
+                         (("dh_out", dh_out), ("dh_in", dh_in)))
+    _check_rows("dh", dh, g.shape, g.dtype)
+    work = diag_workspace_bytes(d)
+    _check_buffer("states", states, diag_states_bytes(d))
+    if workspace is not None:
+        _check_buffer("workspace", workspace, work)
+    _check_device(g, ("x", x), ("states", states), ("dh", dh), ("dh_out", dh_out), ("dg", dg),
+                  ("dx", dx), ("dh_in", dh_in), ("workspace", workspace))
+    dev = g.device
+    if dg is None:
+        dg = torch.empty(g.shape, dtype=odt, device=dev)
+    if dx is None:
+        dx = torch.empty(g.shape, dtype=odt, device=dev)
+    if dh_in is None:
+        dh_in = torch.empty(g.shape[0], g.shape[2], dtype=torch.float32, device=dev)
+    if workspace is None and work:
+        workspace = _bytes(work, dev)
+    rc = _lib().linrec_diag_bwd(context(dev.index), ctypes.byref(d), _rows(g), _rows(x), _ptr(states),
+                                _rows(dh), _ptr(dh_out), _rows(dg), _rows(dx), _ptr(dh_in),
+                                _ptr(workspace), _stream(dev))
+    _check(rc, "linrec_diag_bwd")
+    return dg, dx, dh_in
+
+
+# ----------------------------------------------------------------- generation
+
+def _check_int(name, t, shape, dtype=torch.int32):
+    if not isinstance(t, torch.Tensor):
+        _fail(f"{name}: expected a tensor", TypeError)
+    if t.dtype != dtype:
+        _fail(f"{name}: must be {dtype}, got {t.dtype}", TypeError)
+    if t.shape != shape:
+        _fail(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
+        _fail(f"{name}: must be contiguous")
+
+
+def step(q, k, v, decay, S, *, beta=None, slots=None, o=None, out_dtype=None):
+    """One or a few tokens of the layer (beta None) or of the gated delta rule
+    (linrec_step), S updated in place.  q, k: [B,H,T,d_k]; v: [B,H,T,d_v];
+    decay as fwd; beta: fp32 [B,H,T]; S: fp32 [n,H,d_k,d_v], entry b at slots[b]
+    (int32 [B] on the device) or at b.  An entry whose slot is outside the
+    pool, or taken by an earlier entry, is skipped (o = 0).  Returns o."""
+    odt = _out_dtype(q, out_dtype, o)
+    _validate(q, k, v, decay, outs=_outs(q, v, odt, o=o))
+    B, H, T, DK = q.shape
+    if not isinstance(S, torch.Tensor) or S.dim() != 4:
+        _fail("S: must be a float32 [n,H,d_k,d_v] tensor")
+    _check_state("S", S, torch.Size((S.shape[0], H, DK, v.shape[3])))
+    if slots is not None:
+        _check_int("slots", slots, torch.Size((B,)))
+    elif S.shape[0] < B:
+        _fail(f"S: {S.shape[0]} states for {B} entries")
+    barg = _beta_arg("beta", beta, B, H, T) if beta is not None else Tensor(None, 0, 0, 0)
+    kind, dec = _decay(decay)
+    d = _desc_of(q, v, kind, odt)
+    _check_device(q, ("k", k), ("v", v), ("decay", decay), ("S", S), ("beta", beta),
+                  ("slots", slots), ("o", o))
+    o = _new_act(q, v.shape[3], odt, o)
+    rc = _lib().linrec_step(context(q.device.index), ctypes.byref(d), _act(q), _act(k), _act(v), barg,
+                            dec, _ptr(S), _ptr(slots), S.shape[0], _act(o), _stream(q.device))
+    _check(rc, "linrec_step")
+    return o
+
+
+class KvCache(NamedTuple):
+    """A paged 8-bit key/value cache (layouts in include/linrec.h): codes as
+    float8_e4m3fn tensors k [pages,H,page,D] and v [pages,H,D,page], scales
+    fp32 [pages,H], table int32 [B,max_pages]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    table: torch.Tensor
+
+
+def kv_cache(pages, heads, page, width, table, device=None) -> KvCache:
+    """An empty cache of `pages` pages for the block table `table`."""
+    dev = table.device if device is None else device
+    codes = lambda *shape: torch.zeros(*shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)  # noqa: E731
+    scale = lambda: torch.zeros(pages, heads, dtype=torch.float32, device=dev)  # noqa: E731
+    return KvCache(codes(pages, heads, page, width), codes(pages, heads, width, page), scale(), scale(),
+                   table)
+
+
+def _kv_desc(cache: KvCache, B: int):
+    """Checks of a cache's tensors; returns the C description."""
+    k, v, ks, vs, table = cache
+    for name, t in (("cache.k", k), ("cache.v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            _fail(f"{name}: must be a 4-dimensional tensor")
+        if t.dtype != torch.float8_e4m3fn:
+            _fail(f"{name}: must be float8_e4m3fn, got {t.dtype}", TypeError)
+        if not t.is_contiguous():
+            _fail(f"{name}: must be contiguous")
+    pages, H, page, D = k.shape
+    if v.shape != (pages, H, D, page):
+        _fail(f"cache.v: shape {tuple(v.shape)} != {(pages, H, D, page)}")
+    _check_state("cache.k_scale", ks, torch.Size((pages, H)))
+    _check_state("cache.v_scale", vs, torch.Size((pages, H)))
+    if ks is None or vs is None:
+        _fail("cache: the scales are needed")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        _fail("cache.table: must be an int32 [B,max_pages] tensor")
+    if table.dtype != torch.int32:
+        _fail(f"cache.table: must be torch.int32, got {table.dtype}", TypeError)
+    if table.shape[0] != B:
+        _fail(f"cache.table: {table.shape[0]} rows for {B} sequences")
+    if table.shape[1] > 1 and table.stride(1) != 1:
+        _fail("cache.table: rows must be contiguous")
+    return KvCacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(),
+                       table.stride(0), pages, page, table.shape[1], H, D)
+
+
+def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interleaved=False, q=None,
+              q_out=None):
+    """Append k, v [B,H,T,D] (bf16) behind past[b] (int32 [B]) tokens of every
+    sequence's cache, the first n_new[b] of the T, with the rotation of
+    inv_freq (fp64 [rot/2]) applied to the keys and to q [B,Hq,T,D]
+    (linrec_kv_append).  Returns the rotated queries (None without q); rows
+    that n_new excludes are left as they were (zeros in a new q_out)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        _fail("k: must be a [B,H,T,D] tensor")
+    B, H, T, D = k.shape
+    c = _kv_desc(cache, B)
+    bf = torch.bfloat16
+    shape = torch.Size((B, c.H, T, c.D))
+    _check_act("k", k, shape, bf)
+    _check_act("v", v, shape, bf)
+    _check_int("past", past, torch.Size((B,)))
+    if n_new is not None:
+        _check_int("n_new", n_new, torch.Size((B,)))
+    rot = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            _fail("inv_freq: must be a float64 vector")
+        _check_int("inv_freq", inv_freq, inv_freq.shape, torch.float64)
+        rot = 2 * inv_freq.numel()
+    Hq = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            _fail("q: must be a [B,Hq,T,D] tensor")
+        Hq = q.shape[1]
+        _check_act("q", q, torch.Size((B, Hq, T, D)), bf)
+        if q_out is not None:
+            _check_act("q_out", q_out, q.shape, bf)
+    elif q_out is not None:
+        _fail("q_out: there is no q")
+    _check_device(k, ("v", v), ("past", past), ("n_new", n_new), ("inv_freq", inv_freq), ("q", q),
+                  ("q_out", q_out), *zip(KvCache._fields, cache))
+    if q is not None and q_out is None:
+        q_out = torch.zeros_like(q) if n_new is not None else torch.empty_like(q)
+    rc = _lib().linrec_kv_append(context(k.device.index), ctypes.byref(c), B, T, _act(k), _act(v),
+                                 _ptr(past), _ptr(n_new), _ptr(inv_freq), rot, 1 if interleaved else 0,
+                                 Hq, _act(q), _act(q_out), _stream(k.device))
+    _check(rc, "linrec_kv_append")
+    return q_out
+
+
+def kv_attn(cache: KvCache, q, past, *, n_new=None, scale=None, window=0, o=None, lse=None,
+            workspace=None):
+    """Attention of q [B,Hq,T,D] (bf16) over the cache, which already holds
+    these T tokens behind past[b] earlier ones (linrec_kv_attn).  scale:
+    1/sqrt(D) by default; window > 0: the last `window` tokens only.  lse: fp32
+    [B,Hq,T] to be filled, or None.  Returns o; rows that n_new excludes are
+    left as they were (zeros in a new o)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        _fail("q: must be a [B,Hq,T,D] tensor")
+    B, Hq, T, D = q.shape
+    c = _kv_desc(cache, B)
+    bf = torch.bfloat16
+    shape = torch.Size((B, Hq, T, c.D))
+    _check_act("q", q, shape, bf)
+    _check_int("past", past, torch.Size((B,)))
+    if n_new is not None:
+        _check_int("n_new", n_new, torch.Size((B,)))
+    if o is not None:
+        _check_act("o", o, shape, bf)
+    _check_state("lse", lse, torch.Size((B, Hq, T)))
+    if Hq % c.H:
+        _fail(f"q: {Hq} heads are no multiple of the cache's {c.H}")
+    need = int(_lib().linrec_kv_attn_workspace_bytes(ctypes.byref(c), B, T, Hq))
+    if workspace is not None:
+        _check_buffer("workspace", workspace, need)
+    _check_device(q, ("past", past), ("n_new", n_new), ("o", o), ("lse", lse), ("workspace", workspace),
+                  *zip(KvCache._fields, cache))
+    if o is None:
+        o = torch.zeros_like(q) if n_new is not None else torch.empty_like(q)
+    if workspace is None and need:
+        workspace = _bytes(need, q.device)
+    rc = _lib().linrec_kv_attn(context(q.device.index), ctypes.byref(c), B, T, Hq, _act(q), _ptr(past),
+                               _ptr(n_new), D ** -0.5 if scale is None else float(scale), int(window),
+                               _act(o), _ptr(lse), _ptr(workspace), _stream(q.device))
+    _check(rc, "linrec_kv_attn")
+    return o
 
 
 def piece_loop(q, k, v, decay, lengths: Sequence[int], S_in=None, dO=None, dS_out=None,
