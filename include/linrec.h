@@ -534,15 +534,18 @@ linrec_status linrec_step(linrec_ctx* ctx, const linrec_desc* d, linrec_tensor q
  *   k: [pages, H, page, D] bytes, v: [pages, H, D, page] bytes (a head's
  *   tokens run along the row, so that a product over tokens reads 16 of them
  *   at once); k_scale, v_scale: fp32 [pages, H]; all contiguous, k and v
- *   16-byte aligned.  Value = code * scale.
+ *   16-byte aligned.  Value = code * scale; a scale is a power of two (of a
+ *   scale that is not, the attention takes the exponent alone).
  *   table: int32 [B, max_pages] with row stride table_stride: token t of
  *   sequence b lies in page table[b][t / page] at t % page.  An entry outside
  *   [0, pages) is no page: its tokens are not written and not attended to.
- * page in {16, 32, 64, 128}; D in {64, 128}; 1 <= H <= 65535.
+ * page in {16, 32, 64, 128}; D in {64, 128}; 1 <= H <= 65535; max_pages * page
+ * <= LINREC_MAX_T.
  * A call adds or attends from T new tokens per sequence, which follow past[b]
  * tokens (int32 [B], device memory; negative counts as 0 tokens and no new
  * ones); n_new: int32 [B], the first n_new[b] of the T (clamped to [0, T]) are
- * there, or NULL: all.  Rows behind them are neither read nor written.
+ * there, or NULL: all (a token whose position would pass 2^31 - 2 is not).
+ * Rows behind them are neither read nor written.
  * Activations are LINREC_BF16, [B, H, T, D] linrec_tensors as above.
  * Pages may be shared between sequences for reading. */
 typedef struct {

@@ -21,22 +21,20 @@ struct KvCache {
 };
 
 // A sequence's new tokens in a call of T: they follow `past` tokens, n of them
-// are there.  past + n may pass 31 bits.
+// are there; positions stay below 2^31 - 1.
 struct Span {
-    int64_t past;
-    int n;
+    int past, n;
     __device__ __forceinline__ Span(const int* past_, const int* n_new, int b, int T)
     {
         const int p = past_[b];
-        past = p < 0 ? 0 : p;
+        past = max(p, 0);
         n = n_new ? min(max(n_new[b], 0), T) : T;
-        if (p < 0)
-            n = 0;
+        n = p < 0 ? 0 : min(n, 0x7fffffff - past);
     }
 };
 
 // The page of a sequence's token block, -1 if there is none.
-__device__ __forceinline__ int page_of(const KvCache& c, int b, int64_t block)
+__device__ __forceinline__ int page_of(const KvCache& c, int b, int block)
 {
     if (block < 0 || block >= c.max_pages)
         return -1;
@@ -50,7 +48,8 @@ inline linrec_status check_kv(const linrec_kv_cache* c, int32_t B, int32_t T)
         return LINREC_E_NULL;
     if (B < 1 || B > 32767 || T < 0 || T > LINREC_MAX_T || c->H < 1 || c->H > 65535 ||
         (c->D != 64 && c->D != 128) || c->pages < 1 || c->max_pages < 1 ||
-        (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128))
+        (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) ||
+        (int64_t)c->max_pages * c->page > LINREC_MAX_T)
         return LINREC_E_SHAPE;
     // sizes are known without the pointers (workspace queries stop here)
     return LINREC_OK;

@@ -73,13 +73,13 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a)
     __shared__ float red[4];
     const int P = 1 << a.c.shift, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const Span sp(a.past, a.n_new, b, a.T);
-    const int64_t blk = (sp.past >> a.c.shift) + blockIdx.x, base = blk << a.c.shift;
+    const int64_t blk = (sp.past >> a.c.shift) + (int64_t)blockIdx.x, base = blk << a.c.shift;
     // new tokens of the page: [lo, hi)
     const int lo = (int)max((int64_t)0, sp.past - base);
-    const int hi = (int)min((int64_t)P, sp.past + sp.n - base);
+    const int hi = (int)min((int64_t)P, (int64_t)sp.past + sp.n - base);
     if (lo >= hi)
         return;
-    const int page = page_of(a.c, b, blk);
+    const int page = page_of(a.c, b, (int)blk);
     if (page < 0)
         return;
     // an earlier touched block with the same page owns it
@@ -87,8 +87,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a)
     for (int64_t e = tid; e < (int64_t)b * a.nblk + blockIdx.x; e += 256) {
         const int eb = (int)(e / a.nblk), ej = (int)(e % a.nblk);
         const Span es(a.past, a.n_new, eb, a.T);
-        const int64_t first = es.past >> a.c.shift;
-        if (es.n > 0 && first + ej <= (es.past + es.n - 1) >> a.c.shift)
+        const int first = es.past >> a.c.shift;
+        if (es.n > 0 && ej <= ((es.past + es.n - 1) >> a.c.shift) - first)
             dup |= page_of(a.c, eb, first + ej) == page;
     }
     if (__syncthreads_or(dup))

@@ -3,6 +3,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 #include "kv.hpp"
 
 namespace linrec {
@@ -13,97 +15,670 @@ struct AttnArgs {
     Act<const bf16> q;
     Act<bf16> o;
     float* lse;
+    float* part;         // per split: rows of D unnormalised sums, then (max, sum) of every row
     const int* past;
     const int* n_new;
-    int B, T, Hq, group, window;
-    float scale;
+    int B, T, Hq, group, window, nsplit;
+    int rows, row_tiles; // query rows of a key/value head (T * group), tiles of them
+    float c2;            // |scale| * log2(e)
+    bool negate;         // scale < 0: the sign goes into q
 };
 
-__device__ __forceinline__ float decode(unsigned char c)
+// The query rows of one key/value head are (token, head of the group) pairs,
+// token-major: row r is token r / group, head h * group + r % group.
+
+// Keys are taken 64 at a time (a tile), scores as S^T = K Q^T: the result of a
+// 16x16 product gives lane (g, t) four keys of row t, so the softmax of a row
+// stays within the 4 lanes of a column and exp(S^T) is, unmoved, the right
+// operand of O^T = V^T P^T.  Which keys a tile's 4 products hold is free: product
+// i of lane group g holds the keys of KEYS below, chosen so that the 8 values a
+// lane contributes to a k32 step of the second product are neighbours in V's
+// rows, one 16-byte load.
+
+// What a row sees of a tile: offsets lo .. hi, in the 16-key groups (a group
+// lies in one page) whose page is there.
+struct Seen {
+    int lo, hi;
+    unsigned groups;
+    __device__ __forceinline__ bool operator()(int key) const
+    {
+        return key >= lo && key <= hi && (groups >> (key >> 4) & 1);
+    }
+};
+
+// 8 codes (two words) times 2^e as bf16, exact: e4m3 has 3 mantissa bits.  The
+// conversion takes the scale's exponent field, which is all a power of two has.
+__device__ __forceinline__ bf16x8 values8(unsigned lo, unsigned hi, float scale)
 {
-    return __builtin_amdgcn_cvt_f32_fp8((int)c, 0);
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// One workgroup per query row: 256 keys at a time, one per thread, with the
-// running maximum and sum of the softmax; then the threads take (feature, part
-// of the keys) for the weighted sum.
-template <int D>
-__global__ __launch_bounds__(256) void kv_attn_row_kernel(AttnArgs a)
+__device__ __forceinline__ Frag<bf16> frag(bf16x8 v)
 {
-    constexpr int PARTS = 256 / D;
-    __shared__ float qs[D], ps[256], red[4], acc[PARTS][D];
-    __shared__ int pg[256];
-    const int t = blockIdx.x, hq = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-    const Span sp(a.past, a.n_new, b, a.T);
-    if (t >= sp.n)
-        return;
-    const int h = hq / a.group, P = 1 << a.c.shift;
-    const int64_t pos = sp.past + t, lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
-    const int64_t end = min(pos + 1, (int64_t)a.c.max_pages << a.c.shift);
-    if (tid < D)
-        qs[tid] = (float)a.q.head(b, hq)[t * a.q.st + tid];
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    const int f = tid % D, part = tid / D;
-    for (int64_t k0 = lo; k0 < end; k0 += 256) {
-        __syncthreads();
-        const int64_t key = k0 + tid;
-        const int page = key < end ? page_of(a.c, b, key >> a.c.shift) : -1;
-        float s = -INFINITY;
-        if (page >= 0) {
-            const int64_t ph = (int64_t)page * a.c.H + h;
-            const uint8_t* kp = a.c.k + (ph * P + (key & (P - 1))) * D;
-            float x = 0.f;
-            for (int i = 0; i < D; ++i)
-                x += qs[i] * decode(kp[i]);
-            s = x * a.c.ks[ph] * a.scale;
+    Frag<bf16> f;
+    f.v = v;
+    return f;
+}
+
+// Running softmax of the 16 rows of a lane column (row t): the maximum of the
+// raw scores, this lane's share of the sum, and the sums O^T: tile dt of lane
+// (g, t) holds features 16 dt + 4 g + r of row t.
+template <int D>
+struct RowState {
+    float m = -INFINITY, l = 0.f;
+    floatx4 acc[D / 16];
+    __device__ __forceinline__ void clear()
+    {
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            acc[i] = zero4();
+    }
+};
+
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor(x, 16, 64));
+    return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+
+__device__ __forceinline__ float quad_sum(float x)
+{
+    x += __shfl_xor(x, 16, 64);
+    return x + __shfl_xor(x, 32, 64);
+}
+
+// One tile's scores x (lane (g, t): product i, element r) become the weights'
+// fragments p (k32 step s from products 2s, 2s + 1).
+template <int D>
+__device__ __forceinline__ void softmax_tile(RowState<D>& st, floatx4 (&x)[4], Frag<bf16> (&p)[2], float c2)
+{
+    float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        mx = fmaxf(mx, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
+    mx = fmaxf(st.m, quad_max(mx));
+    const float ref = mx == -INFINITY ? 0.f : mx, off = ref * c2;
+    if (__any(mx > st.m)) {   // most tiles leave every row's maximum as it is
+        const float keep = __builtin_amdgcn_exp2f((st.m - ref) * c2);
+        st.l *= keep;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            st.acc[i] *= keep;
+        st.m = mx;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            x[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r], c2, -off));
+            sum += x[i][r];
         }
-        pg[tid] = page;
-        float mx = s;
+    st.l += sum;
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1)
-            mx = fmaxf(mx, __shfl_xor(mx, off, 64));
-        if ((tid & 63) == 0)
-            red[tid >> 6] = mx;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        // a score of NaN spreads through p; the maximum passes it over
-        const float ref = mn == -INFINITY ? 0.f : mn, keep = __expf(m - ref);
-        const float p = page >= 0 ? __expf(s - ref) : 0.f;
-        ps[tid] = p;
-        l = l * keep + p;
-        o *= keep;
-        m = mn;
-        __syncthreads();
-        for (int j = part; j < 256; j += PARTS)
-            if (pg[j] >= 0) {
-                const int64_t ph = (int64_t)pg[j] * a.c.H + h;
-                o += ps[j] * a.c.vs[ph] * decode(a.c.v[(ph * D + f) * P + ((k0 + j) & (P - 1))]);
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            p[s].v[r] = (bf16)x[2 * s][r];
+            p[s].v[4 + r] = (bf16)x[2 * s + 1][r];
+        }
+}
+
+// Query fragments of 16 rows from row r0: element e of k32 step s is feature
+// feat(s) + e.  Rows that are not there read as zeros.
+template <int D, typename Feat>
+__device__ __forceinline__ void load_q(Frag<bf16> (&q)[D / 32], const AttnArgs& a, int b, int h, int row,
+                                       int rows, Feat feat)
+{
+    const bool there = row < rows;
+    const int t = there ? row / a.group : 0, hq = h * a.group + (there ? row % a.group : 0);
+    const bf16* p = a.q.head(b, hq) + (int64_t)t * a.q.st;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        u32x4 v = there ? *reinterpret_cast<const u32x4*>(p + feat(s)) : u32x4{0u, 0u, 0u, 0u};
+        if (a.negate)
+            v ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
+        q[s].v = __builtin_bit_cast(bf16x8, v);
+    }
+}
+
+// The tiles of keys that a block of rows [r0, r1) reads, and the share of them
+// that is this split's.
+struct Range {
+    int k0, end;         // first key (a multiple of 64), end of the visible keys
+    int first, last;     // this split's tiles [first, last)
+    __device__ __forceinline__ Range(const AttnArgs& a, const Span& sp, int r0, int r1, int split, int least)
+    {
+        const int lo = a.window > 0 ? max(0, sp.past + r0 / a.group - a.window + 1) : 0;
+        end = min(sp.past + (r1 - 1) / a.group + 1, a.c.max_pages << a.c.shift);
+        k0 = lo & ~63;
+        const int tiles = end > k0 ? (end - k0 + 63) / 64 : 0;
+        const int per = max((tiles + a.nsplit - 1) / a.nsplit, least);
+        first = min(tiles, split * per);
+        last = min(tiles, first + per);
+    }
+};
+
+// A tile at the border of what the rows see may hold, for some rows, values
+// they do not see.  Their weight is 0, but 0 * NaN is not 0.  Where a border
+// tile holds values that are not finite, they are taken out of V's fragments,
+// and rows that do see one get a NaN.
+
+// Per 32-bit word of two bf16: the elements that are not finite, as 1.0.
+__device__ __forceinline__ unsigned nonfinite2(unsigned w)
+{
+    return ((w & 0x7f80u) == 0x7f80u ? 0x3f80u : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0x3f800000u : 0u);
+}
+
+__device__ __forceinline__ u32x4 nonfinite(const Frag<bf16>& v)
+{
+    const u32x4 w = __builtin_bit_cast(u32x4, v.v);
+    return u32x4{nonfinite2(w[0]), nonfinite2(w[1]), nonfinite2(w[2]), nonfinite2(w[3])};
+}
+
+// Whether the tile holds any (wave-uniform).  vslow(dt, s): V's fragment, for
+// rolled loops: this is rare, and unrolled it would cost the others registers.
+template <int D, typename VSlow>
+__device__ __forceinline__ bool any_nonfinite(VSlow vslow)
+{
+    bool bad = false;
+#pragma unroll 1
+    for (int e = 0; e < D / 8; ++e) {
+        const u32x4 is = nonfinite(vslow(e >> 1, e & 1));
+        bad |= (is[0] | is[1] | is[2] | is[3]) != 0;
+    }
+    return __any(bad);
+}
+
+// Bit 4 dt + r: the row sees one in feature 16 dt + 4 g + r (a product over the
+// indicators of "not finite" and "seen").
+template <int D, typename VSlow, typename Key>
+__device__ __forceinline__ unsigned nonfinite_hits(const Seen& seen, VSlow vslow, Key key)
+{
+    unsigned hits = 0;
+#pragma unroll 1
+    for (int e = 0; e < D / 8; ++e) {
+        const int s = e & 1;
+        Frag<bf16> vis;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            vis.v[i] = (bf16)(seen(key(2 * s + i / 4, i % 4)) ? 1.f : 0.f);
+        const floatx4 hit = mma(frag(__builtin_bit_cast(bf16x8, nonfinite(vslow(e >> 1, s)))), vis, zero4());
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            hits |= (hit[r] > 0.f ? 1u : 0u) << (4 * (e >> 1) + r);
+    }
+    return hits;
+}
+
+// Weights and values of one tile, given its scores; vfrag(dt, s): V's fragment.
+// whole: every row sees all of the tile (wave-uniform).
+template <int D, int NR, typename VFrag, typename VSlow, typename Key>
+__device__ __forceinline__ void attend(RowState<D> (&st)[NR], floatx4 (&x)[NR][4], float c2, bool whole,
+                                       const Seen (&seen)[NR], VFrag vfrag, VSlow vslow, Key key)
+{
+    bool bad = false;
+    if (!whole) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    x[n][i][r] = seen[n](key(i, r)) ? x[n][i][r] : -INFINITY;
+        bad = any_nonfinite<D>(vslow);
+    }
+    Frag<bf16> p[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+        softmax_tile<D>(st[n], x[n], p[n], c2);
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            Frag<bf16> v = vfrag(dt, s);
+            if (bad) {
+                const u32x4 is = nonfinite(v);
+                u32x4 w = __builtin_bit_cast(u32x4, v.v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] &= ((is[i] & 0xffffu) ? 0xffff0000u : ~0u) & ((is[i] >> 16) ? 0xffffu : ~0u);
+                v.v = __builtin_bit_cast(bf16x8, w);
             }
-    }
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1)
-        l += __shfl_xor(l, off, 64);
-    __syncthreads();
-    if ((tid & 63) == 0)
-        red[tid >> 6] = l;
-    acc[part][f] = o;
-    __syncthreads();
-    l = red[0] + red[1] + red[2] + red[3];
-    if (tid < D) {
-        float y = 0.f;
+            for (int n = 0; n < NR; ++n)
+                st[n].acc[dt] = mma(v, p[n][s], st[n].acc[dt]);
+        }
+    if (bad) {
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-            y += acc[i][tid];
-        a.o.head(b, hq)[t * a.o.st + tid] = (bf16)(l == 0.f ? 0.f : y / l);
+        for (int n = 0; n < NR; ++n) {
+            const unsigned hits = nonfinite_hits<D>(seen[n], vslow, key);
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i)
+                if (hits >> i & 1)
+                    st[n].acc[i / 4][i % 4] = __builtin_nanf("");
+        }
     }
-    if (a.lse && tid == 0)
-        a.lse[((int64_t)b * a.Hq + hq) * a.T + t] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// A row's place in o and lse.
+template <int D>
+__device__ __forceinline__ void write_row(const AttnArgs& a, int b, int h, int row, int f, const floatx4& y, float m,
+                                          float l)
+{
+    const int tok = row / a.group, hq = h * a.group + row % a.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<bf16x4*>(a.o.head(b, hq) + (int64_t)tok * a.o.st + f) =
+        bf16x4{(bf16)(y[0] * inv), (bf16)(y[1] * inv), (bf16)(y[2] * inv), (bf16)(y[3] * inv)};
+    if (a.lse && f == 0)
+        a.lse[((int64_t)b * a.Hq + hq) * a.T + tok] =
+            l == 0.f ? -INFINITY : (m * a.c2 + __log2f(l)) * 0.6931471805599453f;
+}
+
+// A row's sums, and its maximum and total, in a split's part.
+template <int D>
+__device__ __forceinline__ float* part_row(const AttnArgs& a, int split, int b, int h, int row)
+{
+    const int64_t n = (int64_t)a.B * a.c.H * a.rows;
+    return a.part + split * n * (D + 2) + (((int64_t)b * a.c.H + h) * a.rows + row) * D;
 }
 
 template <int D>
-hipError_t launch_attn(const AttnArgs& a, hipStream_t s)
+__device__ __forceinline__ float* part_stat(const AttnArgs& a, int split, int b, int h, int row)
 {
-    launch_kernel(kv_attn_row_kernel<D>, dim3(a.T, a.Hq, a.B), dim3(256), s, a);
+    const int64_t n = (int64_t)a.B * a.c.H * a.rows;
+    return a.part + split * n * (D + 2) + n * D + (((int64_t)b * a.c.H + h) * a.rows + row) * 2;
+}
+
+// ---- few rows: generation -----------------------------------------------
+//
+// Bound by the cache's bytes (2 D per key).  Four waves take every fourth tile
+// of a split's keys each, straight from global memory to registers (no LDS, no
+// barrier: a fragment is 16 contiguous bytes of K's or V's rows), the next
+// tile's K and its page numbers loaded ahead, and join at the end.
+template <int D, int NR>
+__global__ __launch_bounds__(256, 2) void kv_attn_token_kernel(AttnArgs a)
+{
+    constexpr int KS = D / 64, DT = D / 16;
+    __shared__ float red[4][16][D + 4];
+    __shared__ float ms[4][16 * NR], ls[4][16 * NR];
+    const int tile = blockIdx.x % a.row_tiles, split = blockIdx.x / a.row_tiles, h = blockIdx.y, b = blockIdx.z;
+    const Span sp(a.past, a.n_new, b, a.T);
+    const int rows = sp.n * a.group, r0 = tile * 16 * NR;
+    if (r0 >= rows)
+        return;
+    const int r1 = min(rows, r0 + 16 * NR);
+    const Range rg(a, sp, r0, r1, split, 4);
+    const int wave = wave_id(), lane = lane_id(), t = lane & 15, g = lane >> 4;
+    const int shift = a.c.shift, P = 1 << shift, H = a.c.H;
+    // product i's rows 4 g' + r are the keys 16 g' + 4 i + r of the tile
+    auto key = [&](int i, int r) { return 16 * g + 4 * i + r; };
+
+    Frag<bf16> q[NR][D / 32];
+    RowState<D> st[NR];
+    int pos[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int row = r0 + 16 * n + t;
+        load_q<D>(q[n], a, b, h, row, rows, [&](int s) { return 64 * (s / 2) + 16 * g + 8 * (s % 2); });
+        st[n].clear();
+        pos[n] = row < rows ? sp.past + row / a.group : -1;   // -1: sees nothing
+    }
+    // pages of the 16-token groups that this lane loads K (group t / 4) and V (group g) of
+    struct Pages {
+        int k, v;
+    };
+    auto pages = [&](int tl) {
+        const int k = rg.k0 + 64 * tl;
+        const bool in = tl < rg.last;
+        return Pages{in ? page_of(a.c, b, (k + 16 * (t >> 2)) >> shift) : -1,
+                     in ? page_of(a.c, b, (k + 16 * g) >> shift) : -1};
+    };
+    u32x4 kr[4][KS], vr[DT];
+    float ks;
+    auto load_k = [&](int tl, int page) {
+        const int k = rg.k0 + 64 * tl;
+        const int64_t ph = (int64_t)max(page, 0) * H + h;
+        const int in_page = ((k + 16 * (t >> 2)) & (P - 1)) + (t & 3);
+        const uint8_t* p = a.c.k + (ph * P + in_page) * D + 16 * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+                kr[i][j] = *reinterpret_cast<const u32x4*>(p + 4 * i * D + 64 * j);
+        ks = a.c.ks[ph];
+    };
+    int tl = rg.first + wave;
+    Pages now = pages(tl), next = pages(tl + 4);
+    if (tl < rg.last)
+        load_k(tl, now.k);
+    for (; tl < rg.last; tl += 4) {
+        const int k0 = rg.k0 + 64 * tl;
+        const int64_t ph = (int64_t)max(now.v, 0) * H + h;
+        const uint8_t* vp = a.c.v + (ph * D + t) * P + ((k0 + 16 * g) & (P - 1));
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+            vr[i] = *reinterpret_cast<const u32x4*>(vp + 16 * i * P);
+        const float vs = a.c.vs[ph];
+        floatx4 x[NR][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                x[n][i] = zero4();
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                const Frag<bf16> lo = frag(values8(kr[i][j][0], kr[i][j][1], ks));
+                const Frag<bf16> hi = frag(values8(kr[i][j][2], kr[i][j][3], ks));
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    x[n][i] = mma(lo, q[n][2 * j], x[n][i]);
+                    x[n][i] = mma(hi, q[n][2 * j + 1], x[n][i]);
+                }
+            }
+        }
+        // the keys that this lane's scores belong to are its group's
+        const bool page_ok = now.v >= 0;
+        now = next;
+        if (tl + 4 < rg.last)
+            load_k(tl + 4, now.k);
+        next = pages(tl + 8);
+        const bool whole = __all(page_ok) && k0 + 63 <= sp.past + r0 / a.group &&
+                           (a.window <= 0 || k0 > sp.past + (r1 - 1) / a.group - a.window);
+        Seen seen[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            seen[n].hi = min(pos[n], rg.end - 1) - k0;
+            seen[n].lo = a.window > 0 ? pos[n] - a.window + 1 - k0 : 0;
+            seen[n].groups = page_ok ? 15u : 0u;
+        }
+        attend<D, NR>(st, x, a.c2, whole, seen,
+                      [&](int dt, int s) { return frag(values8(vr[dt][2 * s], vr[dt][2 * s + 1], vs)); },
+                      [&](int dt, int s) {
+                          const u32x2 w = *reinterpret_cast<const u32x2*>(vp + 16 * dt * P + 8 * s);
+                          return frag(values8(w[0], w[1], vs));
+                      },
+                      key);
+    }
+    // join the four waves
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const float l = quad_sum(st[n].l);
+        if (g == 0) {
+            ms[wave][16 * n + t] = st[n].m;
+            ls[wave][16 * n + t] = l;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int at = 16 * n + t;
+        const float m = fmaxf(fmaxf(ms[0][at], ms[1][at]), fmaxf(ms[2][at], ms[3][at]));
+        const float f = __builtin_amdgcn_exp2f((st[n].m - (m == -INFINITY ? 0.f : m)) * a.c2);
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+            *reinterpret_cast<floatx4*>(&red[wave][t][16 * i + 4 * g]) = st[n].acc[i] * f;
+        __syncthreads();
+        constexpr int LPR = D / 4;                       // lanes per row
+        for (int e = threadIdx.x; e < 16 * LPR; e += 256) {
+            const int rr = e / LPR, f4 = 4 * (e % LPR), row = r0 + 16 * n + rr, ra = 16 * n + rr;
+            if (row >= rows)
+                continue;
+            const float mr = fmaxf(fmaxf(ms[0][ra], ms[1][ra]), fmaxf(ms[2][ra], ms[3][ra]));
+            const float ref = mr == -INFINITY ? 0.f : mr;
+            float l = 0.f;
+            floatx4 y = zero4();
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                l += ls[w][ra] * __builtin_amdgcn_exp2f((ms[w][ra] - ref) * a.c2);
+                y += *reinterpret_cast<const floatx4*>(&red[w][rr][f4]);
+            }
+            if (a.nsplit == 1) {
+                write_row<D>(a, b, h, row, f4, y, mr, l);
+            } else {
+                *reinterpret_cast<floatx4*>(part_row<D>(a, split, b, h, row) + f4) = y;
+                if (f4 == 0) {
+                    float* s = part_stat<D>(a, split, b, h, row);
+                    s[0] = mr;
+                    s[1] = l;
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the splits of a row, in order: D / 4 lanes a row.
+template <int D>
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
+{
+    constexpr int LPR = D / 4;
+    const int row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, f4 = 4 * (threadIdx.x % LPR);
+    const int h = blockIdx.y, b = blockIdx.z;
+    const Span sp(a.past, a.n_new, b, a.T);
+    if (row >= sp.n * a.group)
+        return;
+    float m = -INFINITY;
+    for (int s = 0; s < a.nsplit; ++s)
+        m = fmaxf(m, part_stat<D>(a, s, b, h, row)[0]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    floatx4 y = zero4();
+    for (int s = 0; s < a.nsplit; ++s) {
+        const float* stat = part_stat<D>(a, s, b, h, row);
+        const float f = __builtin_amdgcn_exp2f((stat[0] - ref) * a.c2);
+        l += stat[1] * f;
+        y += *reinterpret_cast<const floatx4*>(part_row<D>(a, s, b, h, row) + f4) * f;
+    }
+    write_row<D>(a, b, h, row, f4, y, m, l);
+}
+
+// ---- many rows: pieces of a prompt ------------------------------------------
+//
+// Bound by the matrix and vector units (4 D flops a score, and about 8 vector
+// instructions with one exp).  Four waves of 32 rows each share every tile of
+// 64 keys: the codes are converted once, on the way into LDS ([key][feature]
+// and, for V, [feature][key]), two buffers deep, while the loads of the next
+// tile are in flight.
+template <int D>
+__global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
+{
+    constexpr int NR = 2, ROWS = 64 * NR, DT = D / 16, KP = D + 16, VP = 64 + 16;
+    constexpr int KV = 64 * D / 16 / 256;   // 16-byte vectors of K, and of V, a thread stages
+    __shared__ bf16 kt[2][64 * KP], vt[2][D * VP];
+    __shared__ int there[2][4];              // whether the page of each 16-key group is there
+    const int nbh = a.c.H * a.B;
+    const int bh = blockIdx.x % nbh, h = bh % a.c.H, b = bh / a.c.H;
+    const int unit = blockIdx.x / nbh, split = unit % a.nsplit;
+    const int tile = a.row_tiles - 1 - unit / a.nsplit;   // the longest first
+    const Span sp(a.past, a.n_new, b, a.T);
+    const int rows = sp.n * a.group, r0 = tile * ROWS;
+    if (r0 >= rows)
+        return;
+    const int r1 = min(rows, r0 + ROWS);
+    const Range rg(a, sp, r0, r1, split, 1);
+    const int wave = wave_id(), lane = lane_id(), t = lane & 15, g = lane >> 4, tid = threadIdx.x;
+    const int shift = a.c.shift, P = 1 << shift, H = a.c.H;
+    // product i = 2 s + u: rows 4 g + r are the keys 32 s + 8 g + 4 u + r
+    auto key = [&](int i, int r) { return 32 * (i / 2) + 8 * g + 4 * (i % 2) + r; };
+
+    Frag<bf16> q[NR][D / 32];
+    RowState<D> st[NR];
+    int pos[NR];
+    const int w0 = r0 + 16 * NR * wave;      // this wave's rows
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int row = w0 + 16 * n + t;
+        load_q<D>(q[n], a, b, h, row, rows, [&](int s) { return 32 * s + 8 * g; });
+        st[n].clear();
+        pos[n] = row < rows ? sp.past + row / a.group : -1;
+    }
+    // staging: K vector v is key kk, features kf; V vector v is feature row vf, keys 16 (tid % 4)
+    constexpr int KL = D / 16;               // lanes per key row
+    const int kk = tid / KL, kf = 16 * (tid % KL), vf = tid / 4, vg = 16 * (tid % 4);
+    int pk[KV], pv;
+    auto pages = [&](int tl) {
+        const int k = rg.k0 + 64 * tl;
+        const bool in = tl < rg.last;
+#pragma unroll
+        for (int v = 0; v < KV; ++v)
+            pk[v] = in ? page_of(a.c, b, (k + kk + 256 / KL * v) >> shift) : -1;
+        pv = in ? page_of(a.c, b, (k + vg) >> shift) : -1;
+    };
+    u32x4 kr[KV], vr[KV];
+    float ks[KV], vs;
+    bool v_ok;
+    auto load = [&](int tl) {
+        const int k = rg.k0 + 64 * tl;
+#pragma unroll
+        for (int v = 0; v < KV; ++v) {
+            const int64_t ph = (int64_t)max(pk[v], 0) * H + h;
+            kr[v] = *reinterpret_cast<const u32x4*>(a.c.k + (ph * P + ((k + kk + 256 / KL * v) & (P - 1))) * D + kf);
+            ks[v] = a.c.ks[ph];
+        }
+        const int64_t ph = (int64_t)max(pv, 0) * H + h;
+#pragma unroll
+        for (int v = 0; v < KV; ++v)
+            vr[v] = *reinterpret_cast<const u32x4*>(a.c.v + (ph * D + vf + 64 * v) * P + ((k + vg) & (P - 1)));
+        vs = a.c.vs[ph];
+        v_ok = pv >= 0;
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int v = 0; v < KV; ++v) {
+            bf16* kp = &kt[buf][(kk + 256 / KL * v) * KP + kf];
+            *reinterpret_cast<bf16x8*>(kp) = values8(kr[v][0], kr[v][1], ks[v]);
+            *reinterpret_cast<bf16x8*>(kp + 8) = values8(kr[v][2], kr[v][3], ks[v]);
+            bf16* vp = &vt[buf][(vf + 64 * v) * VP + vg];
+            *reinterpret_cast<bf16x8*>(vp) = values8(vr[v][0], vr[v][1], vs);
+            *reinterpret_cast<bf16x8*>(vp + 8) = values8(vr[v][2], vr[v][3], vs);
+        }
+        if (tid < 4)
+            there[buf][tid] = v_ok;
+    };
+    int tl = rg.first;
+    if (tl < rg.last) {
+        pages(tl);
+        load(tl);
+        pages(tl + 1);
+        stage(0);
+    }
+    __syncthreads();
+    for (int buf = 0; tl < rg.last; ++tl, buf ^= 1) {
+        const int k0 = rg.k0 + 64 * tl;
+        const bool more = tl + 1 < rg.last;
+        if (more) {
+            load(tl + 1);
+            pages(tl + 2);
+        }
+        if (w0 < rows) {
+            const bf16* kb = kt[buf];
+            const bf16* vb = vt[buf];
+            floatx4 x[NR][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    x[n][i] = zero4();
+                const bf16* kp = kb + (32 * (i / 2) + 8 * (t >> 2) + 4 * (i % 2) + (t & 3)) * KP + 8 * g;
+#pragma unroll
+                for (int s = 0; s < D / 32; ++s) {
+                    const Frag<bf16> kfr = frag(*reinterpret_cast<const bf16x8*>(kp + 32 * s));
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        x[n][i] = mma(kfr, q[n][s], x[n][i]);
+                }
+            }
+            const int w1 = min(rows, w0 + 16 * NR);
+            const unsigned groups = there[buf][0] | there[buf][1] << 1 | there[buf][2] << 2 | there[buf][3] << 3;
+            const bool whole = groups == 15u && k0 + 63 <= sp.past + w0 / a.group &&
+                               (a.window <= 0 || k0 > sp.past + (w1 - 1) / a.group - a.window);
+            Seen seen[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                seen[n].hi = min(pos[n], rg.end - 1) - k0;
+                seen[n].lo = a.window > 0 ? pos[n] - a.window + 1 - k0 : 0;
+                seen[n].groups = groups;
+            }
+            auto vfrag = [&](int dt, int s) {
+                return frag(*reinterpret_cast<const bf16x8*>(vb + (16 * dt + t) * VP + 32 * s + 8 * g));
+            };
+            attend<D, NR>(st, x, a.c2, whole, seen, vfrag, vfrag, key);
+        }
+        if (more)
+            stage(buf ^ 1);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const float l = quad_sum(st[n].l);
+        const int row = w0 + 16 * n + t;
+        if (row >= rows)
+            continue;
+        if (a.nsplit == 1) {
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+                write_row<D>(a, b, h, row, 16 * i + 4 * g, st[n].acc[i], st[n].m, l);
+        } else {
+            float* y = part_row<D>(a, split, b, h, row);
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+                *reinterpret_cast<floatx4*>(y + 16 * i + 4 * g) = st[n].acc[i];
+            if (g == 0) {
+                float* s = part_stat<D>(a, split, b, h, row);
+                s[0] = st[n].m;
+                s[1] = l;
+            }
+        }
+    }
+}
+
+// ---- host ------------------------------------------------------------------
+
+// How a call is cut: rows of a key/value head, tiles of them, splits of the keys.
+struct Plan {
+    int rows, row_tiles, nsplit;
+    bool token;
+};
+
+Plan plan_of(const linrec_kv_cache* c, int B, int T, int Hq)
+{
+    Plan p;
+    p.rows = T * (Hq / c->H);
+    // Up to 64 rows the cache's bytes cost more than the products.
+    p.token = p.rows <= 64;
+    const int tile_rows = p.token ? (p.rows <= 16 ? 16 : 32) : 128;
+    p.row_tiles = (p.rows + tile_rows - 1) / tile_rows;
+    const int64_t blocks = (int64_t)B * c->H * p.row_tiles;
+    const int64_t key_tiles = ((int64_t)c->max_pages * c->page + 63) / 64;
+    // splits fill the 256 CUs; each gets at least one tile a wave (token kernel)
+    // or 8 tiles (piece kernel)
+    const int64_t want = ((p.token ? 1024 : 512) + blocks - 1) / blocks;
+    const int64_t most = std::max<int64_t>(1, key_tiles / (p.token ? 4 : 8));
+    p.nsplit = (int)std::min<int64_t>(std::min(want, most), 64);
+    return p;
+}
+
+template <int D>
+hipError_t launch_attn(const AttnArgs& a, bool token, hipStream_t s)
+{
+    if (token) {
+        const dim3 grid(a.row_tiles * a.nsplit, a.c.H, a.B);
+        if (a.rows <= 16)
+            launch_kernel(kv_attn_token_kernel<D, 1>, grid, dim3(256), s, a);
+        else
+            launch_kernel(kv_attn_token_kernel<D, 2>, grid, dim3(256), s, a);
+    } else {
+        launch_kernel(kv_attn_piece_kernel<D>, dim3(a.c.H * a.B * a.row_tiles * a.nsplit), dim3(256), s, a);
+    }
+    if (a.nsplit > 1)
+        launch_kernel(kv_attn_join_kernel<D>, dim3((a.rows + 1024 / D - 1) / (1024 / D), a.c.H, a.B), dim3(256), s, a);
     return hipGetLastError();
 }
 
@@ -112,7 +687,10 @@ linrec_status check_attn(const linrec_kv_cache* cache, int32_t B, int32_t T, int
     const linrec_status st = check_kv(cache, B, T);
     if (st != LINREC_OK)
         return st;
-    return Hq < 1 || Hq > 65535 || Hq % cache->H ? LINREC_E_SHAPE : LINREC_OK;
+    // rows of the whole call are counted in 31 bits
+    if (Hq < 1 || Hq > 65535 || Hq % cache->H || (int64_t)B * Hq * T > 0x7fffffff)
+        return LINREC_E_SHAPE;
+    return LINREC_OK;
 }
 
 }  // namespace
@@ -124,7 +702,11 @@ extern "C" {
 
 size_t linrec_kv_attn_workspace_bytes(const linrec_kv_cache* cache, int32_t B, int32_t T, int32_t Hq)
 {
-    return 0;
+    if (check_attn(cache, B, T, Hq) != LINREC_OK || T == 0)
+        return 0;
+    const Plan p = plan_of(cache, B, T, Hq);
+    return p.nsplit == 1 ? 0
+                         : (size_t)p.nsplit * B * cache->H * p.rows * (size_t)(cache->D + 2) * sizeof(float);
 }
 
 linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int32_t B, int32_t T, int32_t Hq,
@@ -162,10 +744,18 @@ linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int3
     a.Hq = Hq;
     a.group = Hq / cache->H;
     a.window = window;
-    a.scale = scale;
+    // the products see q with the scale's sign; a factor of 0 would make
+    // 0 * inf of hidden scores
+    a.negate = scale < 0.f;
+    a.c2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-30f);
+    const Plan p = plan_of(cache, B, T, Hq);
+    a.rows = p.rows;
+    a.row_tiles = p.row_tiles;
+    a.nsplit = p.nsplit;
+    a.part = (float*)workspace;
     hipStream_t s = (hipStream_t)stream;
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_KV_ATTN, s, [&] {
-        return cache->D == 128 ? launch_attn<128>(a, s) : launch_attn<64>(a, s);
+        return cache->D == 128 ? launch_attn<128>(a, p.token, s) : launch_attn<64>(a, p.token, s);
     }));
     return LINREC_OK;
 }

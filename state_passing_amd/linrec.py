@@ -874,6 +874,13 @@ def _diag_setup(g, x, form, out_dtype, outs, carries):
                      BF16 if odt == torch.bfloat16 else F32), odt
 
 
+def _new_rows(like, dtype):
+    """A new [B,T,C] output whose rows are 16-byte aligned (a view of padded rows where C is odd)."""
+    B, T, C = like.shape
+    n = 16 // torch.empty(0, dtype=dtype).element_size()
+    return torch.empty(B, T, -(-C // n) * n, dtype=dtype, device=like.device)[..., :C]
+
+
 def _bytes(n, device):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
@@ -894,7 +901,7 @@ def diag_fwd(g, x, h_in=None, *, form="plain", h=None, h_out=None, states=None, 
                   ("workspace", workspace))
     dev = g.device
     if h is None:
-        h = torch.empty(g.shape, dtype=odt, device=dev)
+        h = _new_rows(g, odt)
     if h_out is None:
         h_out = torch.empty(g.shape[0], g.shape[2], dtype=torch.float32, device=dev)
     if states is None:
@@ -922,9 +929,9 @@ def diag_bwd(g, x, states, dh, dh_out=None, *, form="plain", dg=None, dx=None, d
                   ("dx", dx), ("dh_in", dh_in), ("workspace", workspace))
     dev = g.device
     if dg is None:
-        dg = torch.empty(g.shape, dtype=odt, device=dev)
+        dg = _new_rows(g, odt)
     if dx is None:
-        dx = torch.empty(g.shape, dtype=odt, device=dev)
+        dx = _new_rows(g, odt)
     if dh_in is None:
         dh_in = torch.empty(g.shape[0], g.shape[2], dtype=torch.float32, device=dev)
     if workspace is None and work:
