@@ -483,7 +483,8 @@ size_t linrec_diag_states_bytes(const linrec_diag_desc* d);
 
 /* Bytes of workspace linrec_diag_fwd and linrec_diag_bwd need (0 if `d` is
  * invalid or T <= 256: then workspace may be NULL): per 256 tokens and channel
- * the product of the gates and the sum of what the tokens add. */
+ * the map they make of the state that enters them, and the state that leaves.
+ * It is cleared within each call; calls that may run at once need their own. */
 size_t linrec_diag_workspace_bytes(const linrec_diag_desc* d);
 
 /* Forward.  h_in: NULL means zeros.  h_out: required, may alias h_in.  states:

@@ -4,13 +4,19 @@
 //
 // A token step is the affine map h -> a h + b, so 256 tokens (a segment) of a
 // channel are one map (P, B) too.  A workgroup holds a segment of CH channels
-// in registers: a lane owns one 16-byte vector of channels and R consecutive
+// in registers: a lane owns one 16-byte vector of channels and 8 consecutive
 // tokens (a run), so a load instruction reads 8 rows of 128 bytes.  Each run is
 // folded to its map, the maps of the 32 runs are folded through LDS from the
 // state that enters the segment, and the run is replayed from its entry.
-// Longer pieces first reduce every segment to its map (diag_sum_kernel), fold
-// the maps along the piece (diag_fold_kernel), then run the segments.
+//
+// Segments of a piece are chained in one pass over the data: a workgroup
+// publishes its segment's map, then finds the state that enters it by looking
+// back: from the nearest segment whose leaving state is published, through the
+// maps published since.  Whichever segment that is, the arithmetic is the same
+// sequence s <- P s + B, so results do not depend on timing.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "ctx.hpp"
 #include "device.hpp"
@@ -81,12 +87,12 @@ __device__ __forceinline__ void store_vec(OT* p, const float* y, int n)
 }
 
 // 1 - exp(g): near 0 the difference would cancel (relative error 2^-24 / |g|),
-// so the series takes over there; its first dropped term, g^7 / 8!, is below
-// 2^-28 of the sum at |g| = 1/4.
+// so the series takes over there; its first dropped term, g^5 / 720, is 2^-24 of
+// the sum at |g| = 1/8.
 __device__ __forceinline__ float one_minus_exp(float g, float a)
 {
-    const float s = 1.f + g * (1.f / 2 + g * (1.f / 6 + g * (1.f / 24 + g * (1.f / 120 + g * (1.f / 720 + g * (1.f / 5040))))));
-    return fabsf(g) < 0.25f ? -g * s : 1.f - a;
+    const float s = 1.f + g * (1.f / 2 + g * (1.f / 6 + g * (1.f / 24 + g * (1.f / 120))));
+    return fabsf(g) < 0.125f ? -g * s : 1.f - a;
 }
 
 template <bool MIX>
@@ -120,15 +126,167 @@ __device__ __forceinline__ void load_run(u32x4 (&v)[RUN], const T* base, int64_t
 
 // A token that does not exist has g = 0 and x = 0 (dh = 0): the identity.
 
+// ---- the chain of segments ---------------------------------------------------
+//
+// Per segment and channel, in workspace: its map (product, sum) in 64 bits and
+// the state leaving it in 32, both all ones until they are published, each by one
+// atomic store: a reader that sees a value sees all of it, so no fence orders
+// anything.  Tickets give workgroups their segments in the order they start, so
+// whoever waits for a map waits for a workgroup that runs already, and that
+// publishes its map before it waits for anything itself: every wait ends.
+constexpr unsigned UNSET = 0xffffffffu;
+
+struct Chain {
+    unsigned* ticket;
+    unsigned long long* map;
+    unsigned* value;
+};
+
+__device__ __forceinline__ unsigned settled(float x)   // any NaN but the mark
+{
+    const unsigned u = __float_as_uint(x);
+    return u == UNSET ? 0x7fc00000u : u;
+}
+
+__device__ __forceinline__ void publish_map(unsigned long long* p, float P, float B)
+{
+    __hip_atomic_store(p, (unsigned long long)settled(P) | (unsigned long long)__float_as_uint(B) << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ void publish_value(unsigned* p, float s)
+{
+    __hip_atomic_store(p, settled(s), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ unsigned long long look(const unsigned long long* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ unsigned look(const unsigned* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ float step_map(unsigned long long m, float s)
+{
+    return __builtin_fmaf(__uint_as_float((unsigned)m), s, __uint_as_float((unsigned)(m >> 32)));
+}
+
+// The state entering position i > 0 of a chain (this lane's channel; map and
+// value point at position 0, `ld` apart), called by the lanes of one wave
+// together.  The state that enters the piece is position 0's alone to read (its
+// memory may be the last position's output): it comes with value[0], which
+// waits for nobody.
+__device__ __forceinline__ float chain_enter(const unsigned long long* map, const unsigned* value, int64_t ld, int i)
+{
+    constexpr int W = 8;   // positions looked at together
+    int k = i - 1;         // nearest position of the window
+    float s;
+    for (;;) {
+        unsigned v[W];
+        unsigned long long m[W];
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+            v[u] = look(value + max(k - u, 0) * ld);
+            m[u] = look(map + max(k - u, 0) * ld);
+        }
+        int at = W;        // window offset of the state to start from
+        bool open = true;  // every map before it is there
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+            if (at == W && open) {
+                if (k - u < 0) {
+                    open = false;
+                } else if (__all(v[u] != UNSET)) {
+                    at = u;
+                    s = __uint_as_float(v[u]);
+                } else {
+                    open = __all((unsigned)m[u] != UNSET);
+                }
+            }
+        // something is missing, or all is there but the window's last position is 0,
+        // whose state is about to be: look again (never past position 0)
+        if (!open || (at == W && k < W)) {
+            __builtin_amdgcn_s_sleep(1);
+            continue;
+        }
+        if (at < W) {
+#pragma unroll
+            for (int u = W - 1; u >= 0; --u)
+                if (u < at)
+                    s = step_map(m[u], s);
+            break;
+        }
+        k -= W;
+    }
+    for (int j = k + 1; j < i; j += W) {   // the windows passed over: their maps are there
+        unsigned long long m[W];
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+            m[u] = look(map + min(j + u, i - 1) * ld);
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+            if (j + u < i)
+                s = step_map(m[u], s);
+    }
+    return s;
+}
+
+// This workgroup's place: its channel group, position in the chain and batch.
+struct Work {
+    int cg, pos, b;
+    __device__ __forceinline__ Work(const Chain& ch, int ncg, int B, int nseg)
+    {
+        unsigned id = blockIdx.x;
+        if (nseg > 1) {
+            __shared__ unsigned ticket;
+            if (threadIdx.x == 0)
+                ticket = atomicAdd(ch.ticket, 1u) + 1u;   // the counter starts at all ones
+            __syncthreads();
+            id = ticket;
+        }
+        cg = id % ncg;
+        b = id / ncg % B;
+        pos = id / ncg / B;
+    }
+};
+
+// Orders the work: what is computed from the packed inputs behind these does not
+// move in front of them, neither to the pass before (which would keep gates of
+// every token: twice the inputs' registers) nor to the tokens before.
+__device__ __forceinline__ void forget(u32x4 (&v)[RUN])
+{
+#pragma unroll
+    for (int r = 0; r < RUN; ++r)
+        asm volatile("" : "+v"(v[r]));
+}
+
+template <int N>
+__device__ __forceinline__ void after(u32x4& v, u32x4& w, float (&state)[N])
+{
+#pragma unroll
+    for (int j = 0; j < N; j += 4)
+        asm volatile("" : "+v"(v), "+v"(w), "+v"(state[j]), "+v"(state[j + 1]), "+v"(state[j + 2]), "+v"(state[j + 3]));
+}
+
+__global__ __launch_bounds__(256) void diag_clear_kernel(u32x4* p, int64_t n)
+{
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll)
+        p[i] = u32x4{UNSET, UNSET, UNSET, UNSET};
+}
+
 // Forward.  NRUN = 32: 256 threads, a segment.  NRUN = 1: 64 threads, up to 8
 // tokens of 64 vectors of channels (generation: no LDS, no barrier).
 template <typename T, typename OT, bool MIX, int NRUN>
-__global__ __launch_bounds__(NRUN == 1 ? 64 : 256) void diag_fwd_kernel(
-    Act<const T> g, Act<const T> x, Act<OT> h, const float* h_in, float* states, float* h_out, int T_,
-    int C, int ncg, int nseg)
+__global__ __launch_bounds__(NRUN == 1 ? 64 : 256, MIX && sizeof(T) == 2 ? 3 : 4) void diag_fwd_kernel(
+    Act<const T> g, Act<const T> x, Act<OT> h, const float* h_in, float* states, float* h_out, Chain ch,
+    int B_, int T_, int C, int ncg, int nseg)
 {
     constexpr int N = Vec<T>::N, NT = NRUN == 1 ? 64 : 256, CH = NT / NRUN * N;
-    const int cg = blockIdx.x % ncg, seg = blockIdx.x / ncg, b = blockIdx.y;
+    const Work work(ch, ncg, B_, nseg);
+    const int cg = work.cg, seg = work.pos, b = work.b;
     const Place<T, NRUN> p(cg, seg, T_, C, NT);
     u32x4 gv[RUN], xv[RUN];
     load_run(gv, g.ptr + b * g.sb + p.c0, g.st, p.t0, p.nt, p.nc);
@@ -150,13 +308,15 @@ __global__ __launch_bounds__(NRUN == 1 ? 64 : 256) void diag_fwd_kernel(
             B[j] = 0.f;
         }
 #pragma unroll
-        for (int r = 0; r < RUN; ++r)
+        for (int r = 0; r < RUN; ++r) {
+            after<N>(gv[r], xv[r], B);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float gg = vec_get<T>(gv[r], j), a = __expf(gg);
                 P[j] *= a;
                 B[j] = a * B[j] + added<MIX>(gg, a, vec_get<T>(xv[r], j));
             }
+        }
         const int cl = (threadIdx.x % (NT / NRUN)) * N;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -166,13 +326,21 @@ __global__ __launch_bounds__(NRUN == 1 ? 64 : 256) void diag_fwd_kernel(
         __syncthreads();
         const int c = cg * CH + threadIdx.x;
         if (threadIdx.x < CH && c < C) {
-            float s;
-            if (nseg == 1) {
-                s = h_in ? h_in[(int64_t)b * C + c] : 0.f;
-                states[(int64_t)b * C + c] = s;
-            } else {
-                s = states[((int64_t)b * nseg + seg) * C + c];
+            float s = seg == 0 && h_in ? h_in[(int64_t)b * C + c] : 0.f;
+            if (nseg > 1) {
+                const int64_t chain = (int64_t)b * nseg * C + c, at = chain + (int64_t)seg * C;
+                float sp = 1.f, sb = 0.f;
+#pragma unroll 8
+                for (int i = 0; i < NRUN; ++i) {
+                    sb = sP[i][threadIdx.x] * sb + sB[i][threadIdx.x];
+                    sp *= sP[i][threadIdx.x];
+                }
+                publish_map(ch.map + at, sp, sb);
+                if (seg > 0)
+                    s = chain_enter(ch.map + chain, ch.value + chain, C, seg);
+                publish_value(ch.value + at, __builtin_fmaf(sp, s, sb));
             }
+            states[((int64_t)b * nseg + seg) * C + c] = s;
 #pragma unroll 8
             for (int i = 0; i < NRUN; ++i) {   // sB becomes the state entering run i
                 const float bb = sB[i][threadIdx.x];
@@ -190,6 +358,7 @@ __global__ __launch_bounds__(NRUN == 1 ? 64 : 256) void diag_fwd_kernel(
     OT* hp = h.ptr + b * h.sb + p.c0;
 #pragma unroll
     for (int r = 0; r < RUN; ++r) {
+        after<N>(gv[r], xv[r], hc);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const float gg = vec_get<T>(gv[r], j), a = __expf(gg);
@@ -211,13 +380,14 @@ __global__ __launch_bounds__(NRUN == 1 ? 64 : 256) void diag_fwd_kernel(
 // from later tokens:  G = dh + R,  dx = G or (1 - a) G,  dg = a G (h_{t-1} - [mix] x),
 // R <- a G.  A run is also the map R -> P R + Q from its right end to its left.
 template <typename T, typename OT, bool MIX>
-__global__ __launch_bounds__(256) void diag_bwd_kernel(
+__global__ __launch_bounds__(256, sizeof(T) == 2 && sizeof(OT) == 2 ? 3 : 2) void diag_bwd_kernel(
     Act<const T> g, Act<const T> x, Act<const T> dh, Act<OT> dg, Act<OT> dx, const float* states,
-    const float* right, const float* dh_out, float* dh_in, int T_, int C, int ncg, int nseg)
+    const float* dh_out, float* dh_in, Chain ch, int B_, int T_, int C, int ncg, int nseg)
 {
     constexpr int N = Vec<T>::N, NT = 256, NRUN = SEG / RUN, CH = NT / NRUN * N;
     __shared__ float sP[NRUN][CH], sB[NRUN][CH], sQ[NRUN][CH];
-    const int cg = blockIdx.x % ncg, seg = blockIdx.x / ncg, b = blockIdx.y;
+    const Work work(ch, ncg, B_, nseg);
+    const int cg = work.cg, seg = nseg - 1 - work.pos, b = work.b;   // the chain runs from the right
     const Place<T, NRUN> p(cg, seg, T_, C, NT);
     u32x4 gv[RUN], xv[RUN], dv[RUN];
     load_run(gv, g.ptr + b * g.sb + p.c0, g.st, p.t0, p.nt, p.nc);
@@ -237,6 +407,7 @@ __global__ __launch_bounds__(256) void diag_bwd_kernel(
         sP[p.run][cl + j] = P;
         sB[p.run][cl + j] = B;
         sQ[p.run][cl + j] = Q;
+        forget(gv);
     }
     __syncthreads();
     // one wave-sized group of threads folds forward, another backward
@@ -252,8 +423,20 @@ __global__ __launch_bounds__(256) void diag_bwd_kernel(
     } else if (threadIdx.x >= 64 && threadIdx.x - 64 < CH && cg * CH + (int)threadIdx.x - 64 < C) {
         const int cc = threadIdx.x - 64;
         const int64_t at = (int64_t)b * C + cg * CH + cc;
-        float R = nseg == 1 ? (dh_out ? dh_out[at] : 0.f)
-                            : right[((int64_t)b * nseg + seg) * C + cg * CH + cc];
+        float R = work.pos == 0 && dh_out ? dh_out[at] : 0.f;
+        if (nseg > 1) {
+            const int64_t chain = (int64_t)b * nseg * C + cg * CH + cc, to = chain + (int64_t)work.pos * C;
+            float sp = 1.f, sq = 0.f;
+#pragma unroll 8
+            for (int i = NRUN - 1; i >= 0; --i) {
+                sq = sP[i][cc] * sq + sQ[i][cc];
+                sp *= sP[i][cc];
+            }
+            publish_map(ch.map + to, sp, sq);
+            if (work.pos > 0)
+                R = chain_enter(ch.map + chain, ch.value + chain, C, work.pos);
+            publish_value(ch.value + to, __builtin_fmaf(sp, R, sq));
+        }
 #pragma unroll 8
         for (int i = NRUN - 1; i >= 0; --i) {
             const float q = sQ[i][cc];
@@ -272,6 +455,11 @@ __global__ __launch_bounds__(256) void diag_bwd_kernel(
     constexpr bool PACK = sizeof(T) == 2 && sizeof(OT) == 2;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
+        if (j % 2 == 0) {
+            forget(gv);
+            forget(xv);
+            forget(dv);
+        }
         float s = sB[p.run][cl + j], R = sQ[p.run][cl + j];
         float hp[RUN];
 #pragma unroll
@@ -331,83 +519,6 @@ __global__ __launch_bounds__(256) void diag_bwd_kernel(
     }
 }
 
-// A segment's map.  REV: y = dh, the map R -> P R + Q (see diag_bwd_kernel);
-// else y = x, the map h -> P h + B.
-template <typename T, bool MIX, bool REV>
-__global__ __launch_bounds__(256) void diag_sum_kernel(Act<const T> g, Act<const T> y, float* prod,
-                                                       float* sum, int T_, int C, int ncg, int nseg)
-{
-    constexpr int N = Vec<T>::N, NT = 256, NRUN = SEG / RUN, CH = NT / NRUN * N;
-    __shared__ float sP[NRUN][CH], sB[NRUN][CH];
-    const int cg = blockIdx.x % ncg, seg = blockIdx.x / ncg, b = blockIdx.y;
-    const Place<T, NRUN> p(cg, seg, T_, C, NT);
-    u32x4 gv[RUN], yv[RUN];
-    load_run(gv, g.ptr + b * g.sb + p.c0, g.st, p.t0, p.nt, p.nc);
-    load_run(yv, y.ptr + b * y.sb + p.c0, y.st, p.t0, p.nt, p.nc);
-    const int cl = (threadIdx.x % (NT / NRUN)) * N;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        float P = 1.f, B = 0.f;
-#pragma unroll
-        for (int r = 0; r < RUN; ++r) {
-            const float gg = vec_get<T>(gv[r], j), a = __expf(gg), yy = vec_get<T>(yv[r], j);
-            if constexpr (REV) {
-                B += P * (a * yy);
-                P *= a;
-            } else {
-                P *= a;
-                B = a * B + added<MIX>(gg, a, yy);
-            }
-        }
-        sP[p.run][cl + j] = P;
-        sB[p.run][cl + j] = B;
-    }
-    __syncthreads();
-    const int c = cg * CH + threadIdx.x;
-    if (threadIdx.x < CH && c < C) {
-        float P = 1.f, B = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < NRUN; ++i) {
-            const int k = REV ? NRUN - 1 - i : i;
-            B = sP[k][threadIdx.x] * B + sB[k][threadIdx.x];
-            P *= sP[k][threadIdx.x];
-        }
-        const int64_t at = ((int64_t)b * nseg + seg) * C + c;
-        prod[at] = P;
-        sum[at] = B;
-    }
-}
-
-// Fold of the segments' maps along the piece, from `in` (NULL: zeros); each
-// segment's sum is replaced by the value that enters it (REV: from the right).
-template <bool REV>
-__global__ __launch_bounds__(64) void diag_fold_kernel(const float* prod, float* sum, const float* in,
-                                                       int C, int nseg)
-{
-    const int c = blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-    if (c >= C)
-        return;
-    float s = in ? in[(int64_t)b * C + c] : 0.f;
-    const int64_t base = (int64_t)b * nseg * C + c;
-    constexpr int U = 16;
-    for (int i0 = 0; i0 < nseg; i0 += U) {
-        float P[U], B[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = min(i0 + u, nseg - 1), k = REV ? nseg - 1 - i : i;
-            P[u] = prod[base + (int64_t)k * C];
-            B[u] = sum[base + (int64_t)k * C];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u < nseg) {
-                const int k = REV ? nseg - 1 - (i0 + u) : i0 + u;
-                sum[base + (int64_t)k * C] = s;
-                s = P[u] * s + B[u];
-            }
-    }
-}
-
 // ---- host ------------------------------------------------------------------
 
 int64_t nseg_of(int64_t T) { return (T + SEG - 1) / SEG; }
@@ -426,7 +537,7 @@ linrec_status check_diag_desc(const linrec_diag_desc* d)
         return LINREC_E_SHAPE;
     // a launch holds at most 2^32 - 1 threads along x
     const int64_t ncg = (d->C + channels_per_group(d->dtype) - 1) / channels_per_group(d->dtype);
-    if (nseg_of(d->T) * ncg * 256 > 0xffffffffll)
+    if (nseg_of(d->T) * ncg * d->B * 256 > 0xffffffffll)
         return LINREC_E_SHAPE;
     if (d->form != LINREC_DIAG_PLAIN && d->form != LINREC_DIAG_MIX)
         return LINREC_E_LAYOUT;
@@ -455,9 +566,28 @@ hipError_t dispatch(const linrec_diag_desc* d, F&& f)
     return d->out_dtype == LINREC_F32 ? form(bf16{}, float{}) : form(bf16{}, bf16{});
 }
 
+// Workspace: the ticket (16 bytes), then the maps, then the states leaving.
+int64_t chain_cells(const linrec_diag_desc* d) { return (int64_t)d->B * nseg_of(d->T) * d->C; }
+
+Chain chain_of(const linrec_diag_desc* d, void* workspace)
+{
+    if (d->T <= SEG)
+        return Chain{nullptr, nullptr, nullptr};
+    unsigned long long* map = (unsigned long long*)((char*)workspace + 16);
+    return Chain{(unsigned*)workspace, map, (unsigned*)(map + chain_cells(d))};
+}
+
+void clear_chain(const linrec_diag_desc* d, void* workspace, hipStream_t s)
+{
+    const int64_t n = (int64_t)linrec_diag_workspace_bytes(d) / 16;
+    if (n > 0)
+        launch_kernel(diag_clear_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), s,
+                      (u32x4*)workspace, n);
+}
+
 hipError_t launch_diag_fwd(const linrec_diag_desc* d, const linrec_tensor& g, const linrec_tensor& x,
                            const float* h_in, const linrec_tensor& h, float* h_out, float* states,
-                           float* prod, hipStream_t s)
+                           void* workspace, hipStream_t s)
 {
     return dispatch(d, [&](auto t, auto o, auto mix) {
         using T = decltype(t);
@@ -467,26 +597,22 @@ hipError_t launch_diag_fwd(const linrec_diag_desc* d, const linrec_tensor& g, co
         const int nseg = (int)nseg_of(d->T);
         if (d->T <= RUN) {
             const int n = (d->C + 64 * Vec<T>::N - 1) / (64 * Vec<T>::N);
-            launch_kernel(diag_fwd_kernel<T, OT, MIX, 1>, dim3(n, d->B), dim3(64), s, cact<T>(g),
-                          cact<T>(x), mact<OT>(h), h_in, states, h_out, d->T, d->C, n, 1);
+            launch_kernel(diag_fwd_kernel<T, OT, MIX, 1>, dim3(n * d->B), dim3(64), s, cact<T>(g), cact<T>(x),
+                          mact<OT>(h), h_in, states, h_out, Chain{}, d->B, d->T, d->C, n, 1);
             return hipGetLastError();
         }
-        if (nseg > 1) {
-            launch_kernel(diag_sum_kernel<T, MIX, false>, dim3(ncg * nseg, d->B), dim3(256), s, cact<T>(g),
-                          cact<T>(x), prod, states, d->T, d->C, ncg, nseg);
-            launch_kernel(diag_fold_kernel<false>, dim3((d->C + 63) / 64, d->B), dim3(64), s,
-                          (const float*)prod, states, h_in, d->C, nseg);
-        }
-        launch_kernel(diag_fwd_kernel<T, OT, MIX, SEG / RUN>, dim3(ncg * nseg, d->B), dim3(256), s,
-                      cact<T>(g), cact<T>(x), mact<OT>(h), h_in, states, h_out, d->T, d->C, ncg, nseg);
+        clear_chain(d, workspace, s);
+        launch_kernel(diag_fwd_kernel<T, OT, MIX, SEG / RUN>, dim3(ncg * nseg * d->B), dim3(256), s, cact<T>(g),
+                      cact<T>(x), mact<OT>(h), h_in, states, h_out, chain_of(d, workspace), d->B, d->T, d->C,
+                      ncg, nseg);
         return hipGetLastError();
     });
 }
 
 hipError_t launch_diag_bwd(const linrec_diag_desc* d, const linrec_tensor& g, const linrec_tensor& x,
                            const float* states, const linrec_tensor& dh, const float* dh_out,
-                           const linrec_tensor& dg, const linrec_tensor& dx, float* dh_in, float* prod,
-                           float* sum, hipStream_t s)
+                           const linrec_tensor& dg, const linrec_tensor& dx, float* dh_in, void* workspace,
+                           hipStream_t s)
 {
     return dispatch(d, [&](auto t, auto o, auto mix) {
         using T = decltype(t);
@@ -494,15 +620,10 @@ hipError_t launch_diag_bwd(const linrec_diag_desc* d, const linrec_tensor& g, co
         constexpr bool MIX = decltype(mix)::value;
         const int cpg = channels_per_group(d->dtype), ncg = (d->C + cpg - 1) / cpg;
         const int nseg = (int)nseg_of(d->T);
-        if (nseg > 1) {
-            launch_kernel(diag_sum_kernel<T, MIX, true>, dim3(ncg * nseg, d->B), dim3(256), s, cact<T>(g),
-                          cact<T>(dh), prod, sum, d->T, d->C, ncg, nseg);
-            launch_kernel(diag_fold_kernel<true>, dim3((d->C + 63) / 64, d->B), dim3(64), s,
-                          (const float*)prod, sum, dh_out, d->C, nseg);
-        }
-        launch_kernel(diag_bwd_kernel<T, OT, MIX>, dim3(ncg * nseg, d->B), dim3(256), s, cact<T>(g),
-                      cact<T>(x), cact<T>(dh), mact<OT>(dg), mact<OT>(dx), states, (const float*)sum,
-                      dh_out, dh_in, d->T, d->C, ncg, nseg);
+        clear_chain(d, workspace, s);
+        launch_kernel(diag_bwd_kernel<T, OT, MIX>, dim3(ncg * nseg * d->B), dim3(256), s, cact<T>(g), cact<T>(x),
+                      cact<T>(dh), mact<OT>(dg), mact<OT>(dx), states, dh_out, dh_in, chain_of(d, workspace),
+                      d->B, d->T, d->C, ncg, nseg);
         return hipGetLastError();
     });
 }
@@ -531,7 +652,9 @@ size_t linrec_diag_states_bytes(const linrec_diag_desc* d)
 
 size_t linrec_diag_workspace_bytes(const linrec_diag_desc* d)
 {
-    return d && d->T <= SEG ? 0 : 2 * linrec_diag_states_bytes(d);
+    if (check_diag_desc(d) != LINREC_OK || d->T <= SEG)
+        return 0;
+    return (16 + 12 * (size_t)chain_cells(d) + 15) / 16 * 16;
 }
 
 linrec_status linrec_diag_fwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec_tensor g, linrec_tensor x,
@@ -557,7 +680,7 @@ linrec_status linrec_diag_fwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec
     if (d->T == 0)
         return pass(d, h_in, h_out, s);
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_DIAG_FWD, s, [&] {
-        return launch_diag_fwd(d, g, x, h_in, h, h_out, (float*)states, (float*)workspace, s);
+        return launch_diag_fwd(d, g, x, h_in, h, h_out, (float*)states, workspace, s);
     }));
     return LINREC_OK;
 }
@@ -586,10 +709,8 @@ linrec_status linrec_diag_bwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec
     hipStream_t s = (hipStream_t)stream;
     if (d->T == 0)
         return pass(d, dh_out, dh_in, s);
-    float* prod = (float*)workspace;
-    float* sum = workspace ? prod + (size_t)d->B * nseg_of(d->T) * d->C : nullptr;
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_DIAG_BWD, s, [&] {
-        return launch_diag_bwd(d, g, x, (const float*)states, dh, dh_out, dg, dx, dh_in, prod, sum, s);
+        return launch_diag_bwd(d, g, x, (const float*)states, dh, dh_out, dg, dx, dh_in, workspace, s);
     }));
     return LINREC_OK;
 }

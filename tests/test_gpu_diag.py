@@ -91,6 +91,8 @@ CASES = [
     (1, 255, 72, BF, False, None), (2, 256, 128, F32, True, None), (3, 257, 40, BF, True, None),
     (1, 512, 136, BF, False, F32), (1, 1000, 32, F32, False, None), (2, 4099, 96, BF, True, None),
     (1, 5000, 200, F32, True, None), (40, 300, 8, BF, False, None),
+    # many chains of segments at once, their lengths multiples of the look-back window
+    (2, 4096, 1024, F32, False, None), (6, 2304, 512, BF, True, None),
 ]
 
 
