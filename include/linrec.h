@@ -574,7 +574,7 @@ typedef struct {
  * infinities are stored as +-448 s, NaN as NaN.
  * A page named more than once among the pages that the call writes is written
  * for the first (lowest b, then lowest token) alone.  Tokens at or past
- * max_pages * page are dropped.
+ * max_pages * page are dropped.  (T / page + 2) * H + T must be below 2^24.
  *   q.ptr == NULL: no queries (Hq, q_out ignored).  q_out may be q. */
 linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache* cache, int32_t B, int32_t T,
                                linrec_tensor k, linrec_tensor v, const int32_t* past,

@@ -15,6 +15,7 @@ struct AppendArgs {
     const int* n_new;
     const double* freq;
     int B, T, Hq, half, nblk;   // half: rotated pairs; nblk: pages a sequence may touch
+    int qshift;                 // queries: 1 << qshift tokens a workgroup
     bool inter;
 };
 
@@ -26,20 +27,43 @@ __device__ __forceinline__ void turn(int64_t pos, double freq, float& c, float& 
     sincospif((float)(2.0 * (t - rint(t))), &s, &c);
 }
 
-// Element i of a head's row after the rotation by `pos` (i: the feature).
-__device__ __forceinline__ float rotated(const AppendArgs& a, const bf16* row, int64_t pos, int i)
+// A row of D features is handled in units of 16: two 8-vectors that the rotation
+// keeps among themselves.  Half-split pairs (i, i + half): the first half / 8
+// units are vectors (u, u + half / 8); every other unit is (2 u, 2 u + 1).
+__device__ __forceinline__ void unit_vectors(int u, int half, bool inter, int& v0, int& v1)
 {
-    const float x = (float)row[i];
-    if (i >= 2 * a.half)
-        return x;
-    float c, s;
-    if (a.inter) {
-        turn(pos, a.freq[i >> 1], c, s);
-        return (i & 1) ? x * c + (float)row[i - 1] * s : x * c - (float)row[i + 1] * s;
+    const bool split = !inter && u < half / 8;
+    v0 = split ? u : 2 * u;
+    v1 = split ? u + half / 8 : 2 * u + 1;
+}
+
+// The 8 pairs of a rotated unit, cosines and sines given per pair.
+template <typename CosSin>
+__device__ __forceinline__ void rotate_unit(float (&y)[16], int u, int half, bool inter, CosSin cs)
+{
+    if (u >= half / 8)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // split: (8 u + i, that + half) is pair 8 u + i; interleaved: (16 u + 2 i, + 1) is pair 8 u + i
+        const int a = inter ? 2 * i : i, b = inter ? 2 * i + 1 : 8 + i;
+        float c, s;
+        cs(8 * u + i, c, s);
+        const float p = y[a], q = y[b];
+        y[a] = p * c - q * s;
+        y[b] = q * c + p * s;
     }
-    const int p = i < a.half ? i : i - a.half;
-    turn(pos, a.freq[p], c, s);
-    return i < a.half ? x * c - (float)row[i + a.half] * s : x * c + (float)row[i - a.half] * s;
+}
+
+__device__ __forceinline__ void load_unit(float (&y)[16], const bf16* row, int v0, int v1)
+{
+    const bf16x8 a = *reinterpret_cast<const bf16x8*>(row + 8 * v0);
+    const bf16x8 b = *reinterpret_cast<const bf16x8*>(row + 8 * v1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[i] = (float)a[i];
+        y[8 + i] = (float)b[i];
+    }
 }
 
 // The least power of two s with amax <= 448 s (448 = 1.75 * 2^8 is the largest
@@ -51,12 +75,25 @@ __device__ __forceinline__ float scale_of(float amax)
     return __uint_as_float((unsigned)max(e, 27) << 23);
 }
 
-// Two values as e4m3 codes in the low half-word: saturating, NaN kept.
-__device__ __forceinline__ unsigned codes2(float x, float y)
+// Saturating, NaN kept (the conversion itself would make an overflow NaN).
+__device__ __forceinline__ float saturated(float x)
 {
-    const float cx = x != x ? x : fminf(fmaxf(x, -448.f), 448.f);
-    const float cy = y != y ? y : fminf(fmaxf(y, -448.f), 448.f);
-    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(cx, cy, 0, false) & 0xffffu;
+    return x != x ? x : fminf(fmaxf(x, -448.f), 448.f);
+}
+
+// Four values as e4m3 codes in a word, round to nearest even.
+__device__ __forceinline__ unsigned codes4(float a, float b, float c, float d)
+{
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(saturated(a), saturated(b), 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(saturated(c), saturated(d), w, true);
+    return (unsigned)w;
+}
+
+// |x| for the scale: values that are not finite do not count.
+__device__ __forceinline__ float finite_abs(float x)
+{
+    const float y = fabsf(x);
+    return y <= 3.402823466e38f ? y : 0.f;
 }
 
 __device__ __forceinline__ float decode(unsigned char c)
@@ -64,16 +101,35 @@ __device__ __forceinline__ float decode(unsigned char c)
     return __builtin_amdgcn_cvt_f32_fp8((int)c, 0);
 }
 
-// One workgroup per (touched page, head, sequence): keys, then values, of the
-// page's new tokens through an LDS tile [token][feature].
+// The codes of a page's earlier tokens under a scale that grew (rare).
 template <int D>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a)
+__device__ __forceinline__ void rescale_old(uint8_t* kc, uint8_t* vc, int lo, int P, float kshrink, float vshrink)
 {
-    __shared__ float tile[128][D + 1];
-    __shared__ float red[4];
-    const int P = 1 << a.c.shift, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    for (int i = threadIdx.x; i < lo * D; i += 256) {
+        if (kshrink != 1.f)
+            kc[i] = (uint8_t)codes4(decode(kc[i]) * kshrink, 0.f, 0.f, 0.f);
+        if (vshrink != 1.f) {
+            uint8_t* at = vc + (i / lo) * P + i % lo;
+            *at = (uint8_t)codes4(decode(*at) * vshrink, 0.f, 0.f, 0.f);
+        }
+    }
+}
+
+// Keys and values of one page and head.  Bound by the bytes (6 D a token: two
+// rows of bf16 read, two of codes written); rotated keys stay in registers
+// between the maximum and the conversion, values are read as 4 tokens x 8
+// features a thread so that four neighbouring codes of V's row make a word, and
+// turned through LDS.
+template <int D, int P>
+__device__ __forceinline__ void append_page(const AppendArgs& a, int j, int h, int b)
+{
+    constexpr int U = D / 16, KR = 256 / U, KI = (P + KR - 1) / KR;           // units a row, rows a pass, passes
+    constexpr int VV = D / 8, VU = P / 4 * VV, VI = (VU + 255) / 256;         // V: vectors a row, units, passes
+    __shared__ uint8_t turned[D][P + 16];
+    __shared__ float red[2][4];
+    const int tid = threadIdx.x;
     const Span sp(a.past, a.n_new, b, a.T);
-    const int64_t blk = (sp.past >> a.c.shift) + (int64_t)blockIdx.x, base = blk << a.c.shift;
+    const int64_t blk = (sp.past >> a.c.shift) + (int64_t)j, base = blk << a.c.shift;
     // new tokens of the page: [lo, hi)
     const int lo = (int)max((int64_t)0, sp.past - base);
     const int hi = (int)min((int64_t)P, (int64_t)sp.past + sp.n - base);
@@ -82,91 +138,178 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a)
     const int page = page_of(a.c, b, (int)blk);
     if (page < 0)
         return;
+    const int64_t ph = (int64_t)page * a.c.H + h;
+    const float kwas = a.c.ks[ph], vwas = a.c.vs[ph];
+    const int64_t t0 = base - sp.past;            // the call's token of the page's first place
+    const int u = tid % U, kr = tid / U, vv = tid % VV, vq = tid / VV;
+    int v0, v1;
+    unit_vectors(u, a.half, a.inter, v0, v1);
+    float ky[KI][16], kmax = 0.f, vmax = 0.f;
+    u32x4 vr[VI][4];
+#pragma unroll
+    for (int i = 0; i < VI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 4 * (vq + 256 / VV * i) + r;
+            vr[i][r] = u32x4{0u, 0u, 0u, 0u};
+            if (t >= lo && t < hi)
+                vr[i][r] = *reinterpret_cast<const u32x4*>(a.v.head(b, h) + (t0 + t) * a.v.st + 8 * vv);
+        }
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+        const int t = kr + KR * i;
+        if (t >= lo && t < hi) {
+            load_unit(ky[i], a.k.head(b, h) + (t0 + t) * a.k.st, v0, v1);
+            rotate_unit(ky[i], u, a.half, a.inter,
+                        [&](int pair, float& c, float& s) { turn(base + t, a.freq[pair], c, s); });
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                kmax = fmaxf(kmax, finite_abs(ky[i][e]));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                vmax = fmaxf(vmax, finite_abs((float)__builtin_bit_cast(bf16x8, vr[i][r])[e]));
     // an earlier touched block with the same page owns it
     int dup = 0;
-    for (int64_t e = tid; e < (int64_t)b * a.nblk + blockIdx.x; e += 256) {
+    const int64_t before = (int64_t)b * a.nblk + j;
+    for (int64_t e = tid; e < before; e += 256) {
         const int eb = (int)(e / a.nblk), ej = (int)(e % a.nblk);
         const Span es(a.past, a.n_new, eb, a.T);
         const int first = es.past >> a.c.shift;
         if (es.n > 0 && ej <= ((es.past + es.n - 1) >> a.c.shift) - first)
             dup |= page_of(a.c, eb, first + ej) == page;
     }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        kmax = fmaxf(kmax, __shfl_xor(kmax, off, 64));
+        vmax = fmaxf(vmax, __shfl_xor(vmax, off, 64));
+    }
+    if ((tid & 63) == 0) {
+        red[0][tid >> 6] = kmax;
+        red[1][tid >> 6] = vmax;
+    }
     if (__syncthreads_or(dup))
         return;
-    const int64_t ph = (int64_t)page * a.c.H + h;
-    for (int which = 0; which < 2; ++which) {
-        const bool keys = which == 0;
-        const Act<const bf16>& x = keys ? a.k : a.v;
-        float amax = 0.f;
-        for (int i = tid; i < (hi - lo) * D; i += 256) {
-            const int t = lo + i / D, f = i % D;
-            const bf16* row = x.head(b, h) + (base + t - sp.past) * x.st;
-            const float y = keys ? rotated(a, row, base + t, f) : (float)row[f];
-            tile[t][f] = y;
-            if (fabsf(y) <= 3.402823466e38f)
-                amax = fmaxf(amax, fabsf(y));
-        }
+    float ks = scale_of(fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3])));
+    float vs = scale_of(fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3])));
+    uint8_t* kc = a.c.k + ph * P * D;
+    uint8_t* vc = a.c.v + ph * P * D;
+    if (lo > 0) {
+        ks = fmaxf(ks, kwas);
+        vs = fmaxf(vs, vwas);
+        if (ks != kwas || vs != vwas)
+            rescale_old<D>(kc, vc, lo, P, kwas / ks, vwas / vs);
+    }
+    const float kinv = 1.f / ks, vinv = 1.f / vs;
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1)
-            amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-        if ((tid & 63) == 0)
-            red[tid >> 6] = amax;
-        __syncthreads();
-        amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        float* sptr = keys ? a.c.ks : a.c.vs;
-        const float was = sptr[ph];
-        float s = scale_of(amax), shrink = 1.f;
-        if (lo > 0) {
-            s = fmaxf(s, was);
-            shrink = was / s;
+    for (int i = 0; i < KI; ++i) {
+        const int t = kr + KR * i;
+        if (t >= lo && t < hi) {
+            unsigned w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = codes4(ky[i][4 * e] * kinv, ky[i][4 * e + 1] * kinv, ky[i][4 * e + 2] * kinv,
+                              ky[i][4 * e + 3] * kinv);
+            *reinterpret_cast<u32x2*>(kc + t * D + 8 * v0) = u32x2{w[0], w[1]};
+            *reinterpret_cast<u32x2*>(kc + t * D + 8 * v1) = u32x2{w[2], w[3]};
         }
-        uint8_t* codes = (keys ? a.c.k : a.c.v) + ph * P * D;
-        if (shrink != 1.f)
-            for (int i = tid; i < lo * D; i += 256) {
-                uint8_t* at = codes + (keys ? (i / D) * D + i % D : (i / lo) * P + i % lo);
-                *at = (uint8_t)codes2(decode(*at) * shrink, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < VI; ++i) {
+        const int t = 4 * (vq + 256 / VV * i);
+        if (t < hi && t + 3 >= lo) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float y[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    y[r] = (float)__builtin_bit_cast(bf16x8, vr[i][r])[e] * vinv;
+                *reinterpret_cast<unsigned*>(&turned[8 * vv + e][t]) = codes4(y[0], y[1], y[2], y[3]);
             }
-        const float inv = 1.f / s;
-        for (int i = tid; i < (hi - lo) * D; i += 256) {
-            const int t = keys ? lo + i / D : lo + i % (hi - lo), f = keys ? i % D : i / (hi - lo);
-            codes[keys ? t * D + f : f * P + t] = (uint8_t)codes2(tile[t][f] * inv, 0.f);
         }
-        __syncthreads();   // everyone has read `was`; the tile is free
-        if (tid == 0)
-            sptr[ph] = s;
+    }
+    __syncthreads();
+    // rows of V: 16 tokens a thread, whole where all of them are new
+    for (int e = tid; e < D * P / 16; e += 256) {
+        const int f = e / (P / 16), t = e % (P / 16) * 16;
+        if (t >= lo && t + 16 <= hi)
+            *reinterpret_cast<u32x4*>(vc + f * P + t) = *reinterpret_cast<const u32x4*>(&turned[f][t]);
+        else
+            for (int i = max(t, lo); i < min(t + 16, hi); ++i)
+                vc[f * P + i] = turned[f][i];
+    }
+    if (tid == 0) {
+        a.c.ks[ph] = ks;
+        a.c.vs[ph] = vs;
     }
 }
 
-// Queries: one workgroup per (16 tokens, head, sequence).  A row is staged
-// before it is written, so q_out may be q.
+// Queries of 1 << qshift tokens, all heads: the angles are shared by the heads,
+// so their cosines and sines are formed once, in LDS.  A unit is read before it
+// is written and by the thread that writes it, so q_out may be q.
 template <int D>
-__global__ __launch_bounds__(256) void kv_rotate_q_kernel(AppendArgs a)
+__device__ __forceinline__ void rotate_queries(const AppendArgs& a, int tile, int b)
 {
-    const int h = blockIdx.y, b = blockIdx.z;
+    constexpr int U = D / 16;
+    __shared__ float2 cs[16 * D / 2];
     const Span sp(a.past, a.n_new, b, a.T);
-    const int t0 = blockIdx.x * 16;
-    float y[16 * D / 256];
-#pragma unroll
-    for (int i = 0; i < 16 * D / 256; ++i) {
-        const int e = threadIdx.x + 256 * i, t = t0 + e / D;
-        if (t < sp.n)
-            y[i] = rotated(a, a.q.head(b, h) + (int64_t)t * a.q.st, sp.past + t, e % D);
-    }
+    const int rows = 1 << a.qshift, t0 = tile << a.qshift, n = min(rows, sp.n - t0);
+    if (n <= 0)
+        return;
+    for (int i = threadIdx.x; i < n * a.half; i += 256)
+        turn((int64_t)sp.past + t0 + i / a.half, a.freq[i % a.half], cs[i].x, cs[i].y);
     __syncthreads();
+    for (int e = threadIdx.x; e < a.Hq * rows * U; e += 256) {
+        const int u = e % U, r = (e / U) & (rows - 1), h = e / U >> a.qshift;
+        if (r >= n)
+            continue;
+        int v0, v1;
+        unit_vectors(u, a.half, a.inter, v0, v1);
+        float y[16];
+        load_unit(y, a.q.head(b, h) + (int64_t)(t0 + r) * a.q.st, v0, v1);
+        rotate_unit(y, u, a.half, a.inter, [&](int pair, float& c, float& s) {
+            c = cs[r * a.half + pair].x;
+            s = cs[r * a.half + pair].y;
+        });
+        bf16x8 o0, o1;
 #pragma unroll
-    for (int i = 0; i < 16 * D / 256; ++i) {
-        const int e = threadIdx.x + 256 * i, t = t0 + e / D;
-        if (t < sp.n)
-            a.q_out.head(b, h)[(int64_t)t * a.q_out.st + e % D] = (bf16)y[i];
+        for (int i = 0; i < 8; ++i) {
+            o0[i] = (bf16)y[i];
+            o1[i] = (bf16)y[8 + i];
+        }
+        bf16* out = a.q_out.head(b, h) + (int64_t)(t0 + r) * a.q_out.st;
+        *reinterpret_cast<bf16x8*>(out + 8 * v0) = o0;
+        *reinterpret_cast<bf16x8*>(out + 8 * v1) = o1;
     }
+}
+
+// One launch: the pages of every head, then the queries.
+template <int D, int P>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a)
+{
+    const int b = blockIdx.y, pages = a.nblk * a.c.H;
+    if ((int)blockIdx.x < pages)
+        append_page<D, P>(a, blockIdx.x / a.c.H, blockIdx.x % a.c.H, b);
+    else
+        rotate_queries<D>(a, blockIdx.x - pages, b);
 }
 
 template <int D>
 hipError_t launch_append(const AppendArgs& a, hipStream_t s)
 {
-    launch_kernel(kv_append_kernel<D>, dim3(a.nblk, a.c.H, a.B), dim3(256), s, a);
-    if (a.q.ptr)
-        launch_kernel(kv_rotate_q_kernel<D>, dim3((a.T + 15) / 16, a.Hq, a.B), dim3(256), s, a);
+    const int tiles = a.q.ptr ? (a.T + (1 << a.qshift) - 1) >> a.qshift : 0;
+    const dim3 grid(a.nblk * a.c.H + tiles, a.B), block(256);
+    switch (a.c.shift) {
+    case 4: launch_kernel(kv_append_kernel<D, 16>, grid, block, s, a); break;
+    case 5: launch_kernel(kv_append_kernel<D, 32>, grid, block, s, a); break;
+    case 6: launch_kernel(kv_append_kernel<D, 64>, grid, block, s, a); break;
+    default: launch_kernel(kv_append_kernel<D, 128>, grid, block, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -187,6 +330,9 @@ extern "C" linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache
     if ((st = check_kv(cache, B, T)) != LINREC_OK)
         return st;
     if (rot < 0 || rot > cache->D || rot % 16 || (q.ptr && (Hq < 1 || Hq > 65535)))
+        return LINREC_E_SHAPE;
+    // a launch holds at most 2^32 - 1 threads along x
+    if (((int64_t)T / cache->page + 2) * cache->H + T > 0xffffff)
         return LINREC_E_SHAPE;
     if (T > 0) {
         if ((st = check_kv_ptrs(cache, B, past, n_new)) != LINREC_OK ||
@@ -220,6 +366,8 @@ extern "C" linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache
     a.half = rot / 2;
     a.nblk = (int)(((int64_t)T + cache->page - 2) / cache->page + 1);
     a.inter = interleaved != 0;
+    while (a.qshift < 4 && 1 << a.qshift < T)
+        ++a.qshift;
     hipStream_t s = (hipStream_t)stream;
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_KV_APPEND, s, [&] {
         return cache->D == 128 ? launch_append<128>(a, s) : launch_append<64>(a, s);
