@@ -166,64 +166,82 @@ struct Range {
 };
 
 // A tile at the border of what the rows see may hold, for some rows, values
-// they do not see.  Their weight is 0, but 0 * NaN is not 0.  Where a border
-// tile holds values that are not finite, they are taken out of V's fragments,
-// and rows that do see one get a NaN.
+// they do not see.  Their weight is 0, but 0 * NaN is not 0.  Values that are
+// not finite (a NaN code, or any code under a scale that is not) are therefore
+// taken out of a border tile when it is loaded, and rows that do see one get a
+// NaN in its feature afterwards.  Both are rare, and kept off the registers of
+// the rest.
 
-// Per 32-bit word of two bf16: the elements that are not finite, as 1.0.
-__device__ __forceinline__ unsigned nonfinite2(unsigned w)
+// 16 codes under `scale`: what is not finite becomes code 0; whether there was
+// any.  (finite_scale() of the scale then keeps 0 a 0.)
+__device__ __forceinline__ bool take_nonfinite(u32x4& v, float scale)
 {
-    return ((w & 0x7f80u) == 0x7f80u ? 0x3f80u : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0x3f800000u : 0u);
-}
-
-__device__ __forceinline__ u32x4 nonfinite(const Frag<bf16>& v)
-{
-    const u32x4 w = __builtin_bit_cast(u32x4, v.v);
-    return u32x4{nonfinite2(w[0]), nonfinite2(w[1]), nonfinite2(w[2]), nonfinite2(w[3])};
-}
-
-// Whether the tile holds any (wave-uniform).  vslow(dt, s): V's fragment, for
-// rolled loops: this is rare, and unrolled it would cost the others registers.
-template <int D, typename VSlow>
-__device__ __forceinline__ bool any_nonfinite(VSlow vslow)
-{
-    bool bad = false;
-#pragma unroll 1
-    for (int e = 0; e < D / 8; ++e) {
-        const u32x4 is = nonfinite(vslow(e >> 1, e & 1));
-        bad |= (is[0] | is[1] | is[2] | is[3]) != 0;
-    }
-    return __any(bad);
-}
-
-// Bit 4 dt + r: the row sees one in feature 16 dt + 4 g + r (a product over the
-// indicators of "not finite" and "seen").
-template <int D, typename VSlow, typename Key>
-__device__ __forceinline__ unsigned nonfinite_hits(const Seen& seen, VSlow vslow, Key key)
-{
-    unsigned hits = 0;
-#pragma unroll 1
-    for (int e = 0; e < D / 8; ++e) {
-        const int s = e & 1;
-        Frag<bf16> vis;
+    unsigned any = 0;
+    const bool inf = (__float_as_uint(scale) & 0x7f800000u) == 0x7f800000u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            vis.v[i] = (bf16)(seen(key(2 * s + i / 4, i % 4)) ? 1.f : 0.f);
-        const floatx4 hit = mma(frag(__builtin_bit_cast(bf16x8, nonfinite(vslow(e >> 1, s)))), vis, zero4());
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            hits |= (hit[r] > 0.f ? 1u : 0u) << (4 * (e >> 1) + r);
+    for (int i = 0; i < 4; ++i) {
+        // 0x7f, the NaN code, is the one whose low 7 bits carry into the top one
+        unsigned n = ((v[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        if (inf)
+            n = 0x80808080u;
+        v[i] &= ~((n >> 7) * 0xffu);
+        any |= n;
     }
-    return hits;
+    return any != 0;
+}
+
+__device__ __forceinline__ float finite_scale(float scale)
+{
+    return (__float_as_uint(scale) & 0x7f800000u) == 0x7f800000u ? 1.f : scale;
+}
+
+// Of 8 codes under `scale`, 1 for each that is not finite, as bf16.
+__device__ __forceinline__ Frag<bf16> nonfinite8(u32x2 w, float scale)
+{
+    const bool inf = (__float_as_uint(scale) & 0x7f800000u) == 0x7f800000u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const unsigned n = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        w[i] = inf ? 0x38383838u : (n >> 7) * 0x38u;   // 0x38 is 1
+    }
+    return frag(values8(w[0], w[1], 1.f));
+}
+
+// Gives the rows of st a NaN wherever they see a value that is not finite:
+// `codes(key, feature, scale)` reads the 8 codes from a key of the tile on.
+template <int D, int NR, typename Codes, typename Key>
+__device__ __forceinline__ void give_nonfinite(RowState<D> (&st)[NR], const Seen (&seen)[NR], Codes codes, Key key)
+{
+    const int t = lane_id() & 15;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        unsigned hits = 0;   // bit 4 dt + r: the row sees one in feature 16 dt + 4 g + r
+#pragma unroll 1
+        for (int e = 0; e < D / 8; ++e) {
+            const int dt = e >> 1, s = e & 1;
+            Frag<bf16> vis;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                vis.v[i] = (bf16)(seen[n](key(2 * s + i / 4, i % 4)) ? 1.f : 0.f);
+            float scale;
+            const u32x2 w = codes(key(2 * s, 0), 16 * dt + t, scale);
+            const floatx4 hit = mma(nonfinite8(w, scale), vis, zero4());
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                hits |= (hit[r] > 0.f ? 1u : 0u) << (4 * dt + r);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i)
+            st[n].acc[i / 4][i % 4] = hits >> i & 1 ? __builtin_nanf("") : st[n].acc[i / 4][i % 4];
+    }
 }
 
 // Weights and values of one tile, given its scores; vfrag(dt, s): V's fragment.
 // whole: every row sees all of the tile (wave-uniform).
-template <int D, int NR, typename VFrag, typename VSlow, typename Key>
+template <int D, int NR, typename VFrag, typename Key>
 __device__ __forceinline__ void attend(RowState<D> (&st)[NR], floatx4 (&x)[NR][4], float c2, bool whole,
-                                       const Seen (&seen)[NR], VFrag vfrag, VSlow vslow, Key key)
+                                       const Seen (&seen)[NR], VFrag vfrag, Key key)
 {
-    bool bad = false;
     if (!whole) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -232,7 +250,6 @@ __device__ __forceinline__ void attend(RowState<D> (&st)[NR], floatx4 (&x)[NR][4
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     x[n][i][r] = seen[n](key(i, r)) ? x[n][i][r] : -INFINITY;
-        bad = any_nonfinite<D>(vslow);
     }
     Frag<bf16> p[NR][2];
 #pragma unroll
@@ -242,29 +259,11 @@ __device__ __forceinline__ void attend(RowState<D> (&st)[NR], floatx4 (&x)[NR][4
     for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            Frag<bf16> v = vfrag(dt, s);
-            if (bad) {
-                const u32x4 is = nonfinite(v);
-                u32x4 w = __builtin_bit_cast(u32x4, v.v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] &= ((is[i] & 0xffffu) ? 0xffff0000u : ~0u) & ((is[i] >> 16) ? 0xffffu : ~0u);
-                v.v = __builtin_bit_cast(bf16x8, w);
-            }
+            const Frag<bf16> v = vfrag(dt, s);
 #pragma unroll
             for (int n = 0; n < NR; ++n)
                 st[n].acc[dt] = mma(v, p[n][s], st[n].acc[dt]);
         }
-    if (bad) {
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const unsigned hits = nonfinite_hits<D>(seen[n], vslow, key);
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i)
-                if (hits >> i & 1)
-                    st[n].acc[i / 4][i % 4] = __builtin_nanf("");
-        }
-    }
 }
 
 // A row's place in o and lse.
@@ -303,7 +302,7 @@ __device__ __forceinline__ float* part_stat(const AttnArgs& a, int split, int b,
 // barrier: a fragment is 16 contiguous bytes of K's or V's rows), the next
 // tile's K and its page numbers loaded ahead, and join at the end.
 template <int D, int NR>
-__global__ __launch_bounds__(256, 2) void kv_attn_token_kernel(AttnArgs a)
+__global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kernel(AttnArgs a)
 {
     constexpr int KS = D / 64, DT = D / 16;
     __shared__ float red[4][16][D + 4];
@@ -398,13 +397,21 @@ __global__ __launch_bounds__(256, 2) void kv_attn_token_kernel(AttnArgs a)
             seen[n].lo = a.window > 0 ? pos[n] - a.window + 1 - k0 : 0;
             seen[n].groups = page_ok ? 15u : 0u;
         }
+        bool bad = false;
+        float vuse = vs;
+        if (!whole) {
+            vuse = finite_scale(vs);
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+                bad |= take_nonfinite(vr[i], vs);
+        }
         attend<D, NR>(st, x, a.c2, whole, seen,
-                      [&](int dt, int s) { return frag(values8(vr[dt][2 * s], vr[dt][2 * s + 1], vs)); },
-                      [&](int dt, int s) {
-                          const u32x2 w = *reinterpret_cast<const u32x2*>(vp + 16 * dt * P + 8 * s);
-                          return frag(values8(w[0], w[1], vs));
-                      },
-                      key);
+                      [&](int dt, int s) { return frag(values8(vr[dt][2 * s], vr[dt][2 * s + 1], vuse)); }, key);
+        if (__any(bad))
+            give_nonfinite<D, NR>(st, seen, [&](int k, int f, float& scale) {
+                scale = vs;
+                return *reinterpret_cast<const u32x2*>(a.c.v + (ph * D + f) * P + ((k0 + k) & (P - 1)));
+            }, key);
     }
     // join the four waves
 #pragma unroll
@@ -454,29 +461,60 @@ __global__ __launch_bounds__(256, 2) void kv_attn_token_kernel(AttnArgs a)
     }
 }
 
-// Joins the splits of a row, in order: D / 4 lanes a row.
+// Joins the splits of a row, one workgroup a row: the splits' maxima and sums
+// by one lane each, their sums of values by D / 4 lanes for every 1024 / D-th
+// split, joined through LDS in a fixed order.
+constexpr int MAX_SPLITS = 64;
+
 template <int D>
 __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 {
-    constexpr int LPR = D / 4;
-    const int row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, f4 = 4 * (threadIdx.x % LPR);
-    const int h = blockIdx.y, b = blockIdx.z;
+    constexpr int LPR = D / 4, G = 256 / LPR;
+    __shared__ float factor[MAX_SPLITS];
+    __shared__ floatx4 sums[G][LPR];
+    const int row = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const Span sp(a.past, a.n_new, b, a.T);
     if (row >= sp.n * a.group)
         return;
-    float m = -INFINITY;
-    for (int s = 0; s < a.nsplit; ++s)
-        m = fmaxf(m, part_stat<D>(a, s, b, h, row)[0]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    floatx4 y = zero4();
-    for (int s = 0; s < a.nsplit; ++s) {
-        const float* stat = part_stat<D>(a, s, b, h, row);
-        const float f = __builtin_amdgcn_exp2f((stat[0] - ref) * a.c2);
-        l += stat[1] * f;
-        y += *reinterpret_cast<const floatx4*>(part_row<D>(a, s, b, h, row) + f4) * f;
+    const int lane = threadIdx.x & 63, grp = threadIdx.x / LPR, f4 = threadIdx.x % LPR;
+    constexpr int PER = MAX_SPLITS / G;
+    floatx4 y[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)     // in flight while the factors are formed
+        if (grp + G * i < a.nsplit)
+            y[i] = *reinterpret_cast<const floatx4*>(part_row<D>(a, grp + G * i, b, h, row) + 4 * f4);
+    // every wave forms them for itself
+    float m = -INFINITY, l = 0.f;
+    if (lane < a.nsplit) {
+        const float* stat = part_stat<D>(a, lane, b, h, row);
+        m = stat[0];
+        l = stat[1];
     }
-    write_row<D>(a, b, h, row, f4, y, m, l);
+    float top = m;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        top = fmaxf(top, __shfl_xor(top, off, 64));
+    const float f = __builtin_amdgcn_exp2f((m - (top == -INFINITY ? 0.f : top)) * a.c2);
+    l *= f;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        l += __shfl_xor(l, off, 64);
+    if (threadIdx.x < 64)
+        factor[lane] = f;
+    __syncthreads();
+    floatx4 sum = zero4();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (grp + G * i < a.nsplit)
+            sum += y[i] * factor[grp + G * i];
+    sums[grp][f4] = sum;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+        for (int i = 1; i < G; ++i)
+            sum += sums[i][f4];
+        write_row<D>(a, b, h, row, 4 * f4, sum, top, l);
+    }
 }
 
 // ---- many rows: pieces of a prompt ------------------------------------------
@@ -493,6 +531,7 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
     constexpr int KV = 64 * D / 16 / 256;   // 16-byte vectors of K, and of V, a thread stages
     __shared__ bf16 kt[2][64 * KP], vt[2][D * VP];
     __shared__ int there[2][4];              // whether the page of each 16-key group is there
+    __shared__ int bad[2];                   // border tile: values were taken out
     const int nbh = a.c.H * a.B;
     const int bh = blockIdx.x % nbh, h = bh % a.c.H, b = bh / a.c.H;
     const int unit = blockIdx.x / nbh, split = unit % a.nsplit;
@@ -549,25 +588,39 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
         vs = a.c.vs[ph];
         v_ok = pv >= 0;
     };
-    auto stage = [&](int buf) {
+    // whether rows [ra, rb) all see the whole tile from key k0 on
+    auto whole_for = [&](int k0, int ra, int rb) {
+        return k0 + 63 <= sp.past + ra / a.group && (a.window <= 0 || k0 > sp.past + (rb - 1) / a.group - a.window);
+    };
+    auto stage = [&](int tl, int buf) {
+        bool any = false;
+        const bool border = !v_ok || !whole_for(rg.k0 + 64 * tl, r0, r1);
+        const float vuse = border ? finite_scale(vs) : vs;
 #pragma unroll
         for (int v = 0; v < KV; ++v) {
             bf16* kp = &kt[buf][(kk + 256 / KL * v) * KP + kf];
             *reinterpret_cast<bf16x8*>(kp) = values8(kr[v][0], kr[v][1], ks[v]);
             *reinterpret_cast<bf16x8*>(kp + 8) = values8(kr[v][2], kr[v][3], ks[v]);
+            if (border)
+                any |= take_nonfinite(vr[v], vs);
             bf16* vp = &vt[buf][(vf + 64 * v) * VP + vg];
-            *reinterpret_cast<bf16x8*>(vp) = values8(vr[v][0], vr[v][1], vs);
-            *reinterpret_cast<bf16x8*>(vp + 8) = values8(vr[v][2], vr[v][3], vs);
+            *reinterpret_cast<bf16x8*>(vp) = values8(vr[v][0], vr[v][1], vuse);
+            *reinterpret_cast<bf16x8*>(vp + 8) = values8(vr[v][2], vr[v][3], vuse);
         }
         if (tid < 4)
             there[buf][tid] = v_ok;
+        if (any)
+            bad[buf] = tl;
     };
+    if (tid < 2)
+        bad[tid] = -1;
+    __syncthreads();
     int tl = rg.first;
     if (tl < rg.last) {
         pages(tl);
         load(tl);
         pages(tl + 1);
-        stage(0);
+        stage(tl, 0);
     }
     __syncthreads();
     for (int buf = 0; tl < rg.last; ++tl, buf ^= 1) {
@@ -597,8 +650,7 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
             }
             const int w1 = min(rows, w0 + 16 * NR);
             const unsigned groups = there[buf][0] | there[buf][1] << 1 | there[buf][2] << 2 | there[buf][3] << 3;
-            const bool whole = groups == 15u && k0 + 63 <= sp.past + w0 / a.group &&
-                               (a.window <= 0 || k0 > sp.past + (w1 - 1) / a.group - a.window);
+            const bool whole = groups == 15u && whole_for(k0, w0, w1);
             Seen seen[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -609,10 +661,16 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
             auto vfrag = [&](int dt, int s) {
                 return frag(*reinterpret_cast<const bf16x8*>(vb + (16 * dt + t) * VP + 32 * s + 8 * g));
             };
-            attend<D, NR>(st, x, a.c2, whole, seen, vfrag, vfrag, key);
+            attend<D, NR>(st, x, a.c2, whole, seen, vfrag, key);
+            if (bad[buf] == tl)
+                give_nonfinite<D, NR>(st, seen, [&](int k, int f, float& scale) {
+                    const int64_t ph = (int64_t)max(page_of(a.c, b, (k0 + k) >> shift), 0) * H + h;
+                    scale = a.c.vs[ph];
+                    return *reinterpret_cast<const u32x2*>(a.c.v + (ph * D + f) * P + ((k0 + k) & (P - 1)));
+                }, key);
         }
         if (more)
-            stage(buf ^ 1);
+            stage(tl + 1, buf ^ 1);
         __syncthreads();
     }
 #pragma unroll
@@ -661,7 +719,7 @@ Plan plan_of(const linrec_kv_cache* c, int B, int T, int Hq)
     // or 8 tiles (piece kernel)
     const int64_t want = ((p.token ? 1024 : 512) + blocks - 1) / blocks;
     const int64_t most = std::max<int64_t>(1, key_tiles / (p.token ? 4 : 8));
-    p.nsplit = (int)std::min<int64_t>(std::min(want, most), 64);
+    p.nsplit = (int)std::min<int64_t>(std::min(want, most), MAX_SPLITS);
     return p;
 }
 
@@ -678,7 +736,7 @@ hipError_t launch_attn(const AttnArgs& a, bool token, hipStream_t s)
         launch_kernel(kv_attn_piece_kernel<D>, dim3(a.c.H * a.B * a.row_tiles * a.nsplit), dim3(256), s, a);
     }
     if (a.nsplit > 1)
-        launch_kernel(kv_attn_join_kernel<D>, dim3((a.rows + 1024 / D - 1) / (1024 / D), a.c.H, a.B), dim3(256), s, a);
+        launch_kernel(kv_attn_join_kernel<D>, dim3(a.rows, a.c.H, a.B), dim3(256), s, a);
     return hipGetLastError();
 }
 

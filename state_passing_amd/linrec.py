@@ -819,6 +819,89 @@ def delta_bwd_seq(q, k, v, beta, decay, lengths: Sequence[int], saved, dO, dS_ou
 
 
 # ----------------------------------------------------------------- elementwise recurrence
+#
+# The calls from here on are also made for single tokens, where the time of
+# their checks counts: each argument is checked and described in one go, and
+# the functions that word the errors run only when a check fails.
+
+_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+_NONE = Tensor(None, 0, 0, 0)
+
+
+def _arg4(name, t, shape, dtype) -> Tensor:
+    """The description of a [B,H,T,d] activation of this shape and type."""
+    if not isinstance(t, torch.Tensor):
+        _fail(f"{name}: expected a tensor", TypeError)
+    if t.shape != shape or t.dtype is not dtype:
+        _check_act(name, t, torch.Size(shape), dtype)
+    s = t.stride()
+    if s[3] != 1:
+        _check_act(name, t, torch.Size(shape), dtype)
+    return Tensor(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _arg3(name, t, shape, dtype) -> Tensor:
+    """The description of a [B,T,C] activation of this shape and type."""
+    if not isinstance(t, torch.Tensor):
+        _fail(f"{name}: expected a tensor", TypeError)
+    if t.shape != shape:
+        _fail(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype is not dtype:
+        _fail(f"{name}: dtype {t.dtype} != {dtype}", TypeError)
+    s = t.stride()
+    if s[2] != 1 and shape[2] > 1:
+        _fail(f"{name}: the channel dimension must be contiguous (stride 1)")
+    return Tensor(t.data_ptr(), s[0], 0, s[1])
+
+
+def _state_ptr(name, t, shape):
+    """The address of a contiguous fp32 tensor of this shape, or None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.shape == shape and t.is_contiguous()):
+        _check_state(name, t, torch.Size(shape))
+    return t.data_ptr()
+
+
+def _int_ptr(name, t, shape, dtype=torch.int32):
+    """The address of a contiguous tensor of this shape and type, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        _fail(f"{name}: expected a tensor", TypeError)
+    if t.dtype is not dtype:
+        _fail(f"{name}: must be {dtype}, got {t.dtype}", TypeError)
+    if t.shape != shape:
+        _fail(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
+        _fail(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _same_device(first, *others) -> int:
+    """The GPU that holds `first` and every tensor of the (name, tensor) pairs."""
+    index = first.get_device()
+    if index >= 0:
+        for _, t in others:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return index
+    _check_device(first, *others)
+    return index
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _bytes(n, like):
+    return torch.empty(n, dtype=torch.uint8, device=like.device)
+
 
 def diag_desc(B, T, C, form, dtype_code, out_code=None) -> DiagDesc:
     return DiagDesc(B, T, C, form, dtype_code, dtype_code if out_code is None else out_code)
@@ -832,57 +915,36 @@ def diag_workspace_bytes(d: DiagDesc) -> int:
     return int(_lib().linrec_diag_workspace_bytes(ctypes.byref(d)))
 
 
-def _rows(t: torch.Tensor) -> Tensor:
-    s = t.stride()
-    return Tensor(t.data_ptr(), s[0], 0, s[1])
-
-
-def _check_rows(name, t, shape, dtype):
-    if not isinstance(t, torch.Tensor):
-        _fail(f"{name}: expected a tensor", TypeError)
-    if t.shape != shape:
-        _fail(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if t.dtype != dtype:
-        _fail(f"{name}: dtype {t.dtype} != {dtype}", TypeError)
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        _fail(f"{name}: the channel dimension must be contiguous (stride 1)")
-
-
-def _diag_setup(g, x, form, out_dtype, outs, carries):
-    """Checks of a diag call; returns (desc, output dtype)."""
-    if not isinstance(g, torch.Tensor) or g.dim() != 3:
-        _fail("g: must be a [B,T,C] tensor")
-    if form not in DIAG_FORMS:
-        _fail(f"form: {form!r} is none of {sorted(DIAG_FORMS)}")
-    if g.dtype not in (torch.bfloat16, torch.float32):
-        _fail(f"unsupported activation dtype {g.dtype}", TypeError)
-    _check_rows("g", g, g.shape, g.dtype)
-    _check_rows("x", x, g.shape, g.dtype)
-    odts = {t.dtype for _, t in outs if isinstance(t, torch.Tensor)}
-    if len(odts) > 1:
-        _fail(f"outputs must share one dtype, got {sorted(map(str, odts))}", TypeError)
-    odt = odts.pop() if odts else (g.dtype if out_dtype is None else out_dtype)
-    if odt not in (torch.bfloat16, torch.float32):
-        _fail(f"unsupported output dtype {odt}", TypeError)
-    for name, t in outs:
-        if t is not None:
-            _check_rows(name, t, g.shape, odt)
-    B, T, C = g.shape
-    for name, t in carries:
-        _check_state(name, t, torch.Size((B, C)))
-    return diag_desc(B, T, C, DIAG_FORMS[form], BF16 if g.dtype == torch.bfloat16 else F32,
-                     BF16 if odt == torch.bfloat16 else F32), odt
-
-
 def _new_rows(like, dtype):
     """A new [B,T,C] output whose rows are 16-byte aligned (a view of padded rows where C is odd)."""
-    B, T, C = like.shape
-    n = 16 // torch.empty(0, dtype=dtype).element_size()
-    return torch.empty(B, T, -(-C // n) * n, dtype=dtype, device=like.device)[..., :C]
+    n = 8 if dtype is torch.bfloat16 else 4
+    C = like.shape[2]
+    if C % n == 0:
+        return torch.empty(like.shape, dtype=dtype, device=like.device)
+    return torch.empty(*like.shape[:2], -(-C // n) * n, dtype=dtype, device=like.device)[..., :C]
 
 
-def _bytes(n, device):
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+def _diag_setup(g, form, out_dtype, *outs):
+    """The shape, description and output type of a diag call."""
+    if not isinstance(g, torch.Tensor) or g.dim() != 3:
+        _fail("g: must be a [B,T,C] tensor")
+    code = _CODE.get(g.dtype)
+    if code is None:
+        _fail(f"unsupported activation dtype {g.dtype}", TypeError)
+    kind = DIAG_FORMS.get(form)
+    if kind is None:
+        _fail(f"form: {form!r} is none of {sorted(DIAG_FORMS)}")
+    odt = g.dtype if out_dtype is None else out_dtype
+    given = [t.dtype for t in outs if isinstance(t, torch.Tensor)]
+    if given:
+        odt = given[0]
+        if len(set(given)) > 1:
+            _fail(f"outputs must share one dtype, got {sorted(map(str, set(given)))}", TypeError)
+    out = _CODE.get(odt)
+    if out is None:
+        _fail(f"unsupported output dtype {odt}", TypeError)
+    B, T, C = shape = g.shape
+    return shape, DiagDesc(B, T, C, kind, code, out), odt
 
 
 def diag_fwd(g, x, h_in=None, *, form="plain", h=None, h_out=None, states=None, workspace=None,
@@ -891,25 +953,30 @@ def diag_fwd(g, x, h_in=None, *, form="plain", h=None, h_out=None, states=None, 
     h_t = exp(g_t) h_{t-1} + b_t per channel, b = x ("plain") or
     (1 - exp(g)) x ("mix"); g, x: [B,T,C], h_in, h_out: fp32 [B,C].
     Returns (h, h_out, states); states is what diag_bwd needs."""
-    d, odt = _diag_setup(g, x, form, out_dtype, (("h", h),), (("h_in", h_in), ("h_out", h_out)))
+    shape, d, odt = _diag_setup(g, form, out_dtype, h)
+    carry = (shape[0], shape[2])
+    ga, xa = _arg3("g", g, shape, g.dtype), _arg3("x", x, shape, g.dtype)
+    ha = None if h is None else _arg3("h", h, shape, odt)
+    in_ptr, out_ptr = _state_ptr("h_in", h_in, carry), _state_ptr("h_out", h_out, carry)
     need, work = diag_states_bytes(d), diag_workspace_bytes(d)
     if states is not None:
         _check_buffer("states", states, need)
     if workspace is not None:
         _check_buffer("workspace", workspace, work)
-    _check_device(g, ("x", x), ("h_in", h_in), ("h", h), ("h_out", h_out), ("states", states),
-                  ("workspace", workspace))
-    dev = g.device
+    dev = _same_device(g, ("x", x), ("h_in", h_in), ("h", h), ("h_out", h_out), ("states", states),
+                       ("workspace", workspace))
     if h is None:
         h = _new_rows(g, odt)
+        ha = _arg3("h", h, shape, odt)
     if h_out is None:
-        h_out = torch.empty(g.shape[0], g.shape[2], dtype=torch.float32, device=dev)
+        h_out = torch.empty(carry, dtype=torch.float32, device=g.device)
+        out_ptr = h_out.data_ptr()
     if states is None:
-        states = _bytes(need, dev)
+        states = _bytes(max(need, 16), g)
     if workspace is None and work:
-        workspace = _bytes(work, dev)
-    rc = _lib().linrec_diag_fwd(context(dev.index), ctypes.byref(d), _rows(g), _rows(x), _ptr(h_in),
-                                _rows(h), _ptr(h_out), _ptr(states), _ptr(workspace), _stream(dev))
+        workspace = _bytes(work, g)
+    rc = _lib().linrec_diag_fwd(context(dev), ctypes.byref(d), ga, xa, in_ptr, ha, out_ptr,
+                                states.data_ptr(), _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_diag_fwd")
     return h, h_out, states
 
@@ -918,43 +985,37 @@ def diag_bwd(g, x, states, dh, dh_out=None, *, form="plain", dg=None, dx=None, d
              workspace=None, out_dtype=None):
     """Backward of diag_fwd over one piece (linrec_diag_bwd), from its states,
     for the loss <dh, h> + <dh_out, h_out>.  Returns (dg, dx, dh_in)."""
-    d, odt = _diag_setup(g, x, form, out_dtype, (("dg", dg), ("dx", dx)),
-                         (("dh_out", dh_out), ("dh_in", dh_in)))
-    _check_rows("dh", dh, g.shape, g.dtype)
+    shape, d, odt = _diag_setup(g, form, out_dtype, dg, dx)
+    carry = (shape[0], shape[2])
+    ga, xa = _arg3("g", g, shape, g.dtype), _arg3("x", x, shape, g.dtype)
+    da = _arg3("dh", dh, shape, g.dtype)
+    dga = None if dg is None else _arg3("dg", dg, shape, odt)
+    dxa = None if dx is None else _arg3("dx", dx, shape, odt)
+    out_ptr, in_ptr = _state_ptr("dh_out", dh_out, carry), _state_ptr("dh_in", dh_in, carry)
     work = diag_workspace_bytes(d)
     _check_buffer("states", states, diag_states_bytes(d))
     if workspace is not None:
         _check_buffer("workspace", workspace, work)
-    _check_device(g, ("x", x), ("states", states), ("dh", dh), ("dh_out", dh_out), ("dg", dg),
-                  ("dx", dx), ("dh_in", dh_in), ("workspace", workspace))
-    dev = g.device
+    dev = _same_device(g, ("x", x), ("states", states), ("dh", dh), ("dh_out", dh_out), ("dg", dg),
+                       ("dx", dx), ("dh_in", dh_in), ("workspace", workspace))
     if dg is None:
         dg = _new_rows(g, odt)
+        dga = _arg3("dg", dg, shape, odt)
     if dx is None:
         dx = _new_rows(g, odt)
+        dxa = _arg3("dx", dx, shape, odt)
     if dh_in is None:
-        dh_in = torch.empty(g.shape[0], g.shape[2], dtype=torch.float32, device=dev)
+        dh_in = torch.empty(carry, dtype=torch.float32, device=g.device)
+        in_ptr = dh_in.data_ptr()
     if workspace is None and work:
-        workspace = _bytes(work, dev)
-    rc = _lib().linrec_diag_bwd(context(dev.index), ctypes.byref(d), _rows(g), _rows(x), _ptr(states),
-                                _rows(dh), _ptr(dh_out), _rows(dg), _rows(dx), _ptr(dh_in),
-                                _ptr(workspace), _stream(dev))
+        workspace = _bytes(work, g)
+    rc = _lib().linrec_diag_bwd(context(dev), ctypes.byref(d), ga, xa, states.data_ptr(), da, out_ptr,
+                                dga, dxa, in_ptr, _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_diag_bwd")
     return dg, dx, dh_in
 
 
 # ----------------------------------------------------------------- generation
-
-def _check_int(name, t, shape, dtype=torch.int32):
-    if not isinstance(t, torch.Tensor):
-        _fail(f"{name}: expected a tensor", TypeError)
-    if t.dtype != dtype:
-        _fail(f"{name}: must be {dtype}, got {t.dtype}", TypeError)
-    if t.shape != shape:
-        _fail(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if not t.is_contiguous():
-        _fail(f"{name}: must be contiguous")
-
 
 def step(q, k, v, decay, S, *, beta=None, slots=None, o=None, out_dtype=None):
     """One or a few tokens of the layer (beta None) or of the gated delta rule
@@ -962,24 +1023,40 @@ def step(q, k, v, decay, S, *, beta=None, slots=None, o=None, out_dtype=None):
     decay as fwd; beta: fp32 [B,H,T]; S: fp32 [n,H,d_k,d_v], entry b at slots[b]
     (int32 [B] on the device) or at b.  An entry whose slot is outside the
     pool, or taken by an earlier entry, is skipped (o = 0).  Returns o."""
-    odt = _out_dtype(q, out_dtype, o)
-    _validate(q, k, v, decay, outs=_outs(q, v, odt, o=o))
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        _fail("q: must be a [B,H,T,d_k] tensor")
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        _fail("v: must be a [B,H,T,d_v] tensor")
+    dt = q.dtype
+    code = _CODE.get(dt)
+    if code is None:
+        _fail(f"unsupported activation dtype {dt}", TypeError)
     B, H, T, DK = q.shape
+    DV = v.shape[3]
+    qa, ka = _arg4("q", q, q.shape, dt), _arg4("k", k, q.shape, dt)
+    va = _arg4("v", v, (B, H, T, DV), dt)
+    odt = o.dtype if isinstance(o, torch.Tensor) else dt if out_dtype is None else out_dtype
+    out = _CODE.get(odt)
+    if out is None:
+        _fail(f"unsupported output dtype {odt}", TypeError)
+    oa = None if o is None else _arg4("o", o, (B, H, T, DV), odt)
+    _check_decay(decay, B, H, T)
+    kind, dec = _decay(decay)
     if not isinstance(S, torch.Tensor) or S.dim() != 4:
         _fail("S: must be a float32 [n,H,d_k,d_v] tensor")
-    _check_state("S", S, torch.Size((S.shape[0], H, DK, v.shape[3])))
-    if slots is not None:
-        _check_int("slots", slots, torch.Size((B,)))
-    elif S.shape[0] < B:
-        _fail(f"S: {S.shape[0]} states for {B} entries")
-    barg = _beta_arg("beta", beta, B, H, T) if beta is not None else Tensor(None, 0, 0, 0)
-    kind, dec = _decay(decay)
-    d = _desc_of(q, v, kind, odt)
-    _check_device(q, ("k", k), ("v", v), ("decay", decay), ("S", S), ("beta", beta),
-                  ("slots", slots), ("o", o))
-    o = _new_act(q, v.shape[3], odt, o)
-    rc = _lib().linrec_step(context(q.device.index), ctypes.byref(d), _act(q), _act(k), _act(v), barg,
-                            dec, _ptr(S), _ptr(slots), S.shape[0], _act(o), _stream(q.device))
+    n = S.shape[0]
+    S_ptr = _state_ptr("S", S, (n, H, DK, DV))
+    slot_ptr = _int_ptr("slots", slots, (B,))
+    if slots is None and n < B:
+        _fail(f"S: {n} states for {B} entries")
+    barg = _NONE if beta is None else _beta_arg("beta", beta, B, H, T)
+    dev = _same_device(q, ("k", k), ("v", v), ("decay", decay), ("S", S), ("beta", beta),
+                       ("slots", slots), ("o", o))
+    if o is None:
+        o = torch.empty((B, H, T, DV), dtype=odt, device=q.device)
+        oa = _arg4("o", o, o.shape, odt)
+    rc = _lib().linrec_step(context(dev), ctypes.byref(Desc(B, H, T, DK, DV, CHUNK, code, kind, out)), qa, ka,
+                            va, barg, dec, S_ptr, slot_ptr, n, oa, _raw_stream(dev))
     _check(rc, "linrec_step")
     return o
 
@@ -1004,33 +1081,39 @@ def kv_cache(pages, heads, page, width, table, device=None) -> KvCache:
                    table)
 
 
-def _kv_desc(cache: KvCache, B: int):
+def _codes_ptr(name, t, shape):
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        _fail(f"{name}: must be a 4-dimensional tensor")
+    if t.dtype is not torch.float8_e4m3fn:
+        _fail(f"{name}: must be float8_e4m3fn, got {t.dtype}", TypeError)
+    if shape is not None and t.shape != shape:
+        _fail(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
+        _fail(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _kv_desc(cache: KvCache, B: int) -> KvCacheDesc:
     """Checks of a cache's tensors; returns the C description."""
     k, v, ks, vs, table = cache
-    for name, t in (("cache.k", k), ("cache.v", v)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            _fail(f"{name}: must be a 4-dimensional tensor")
-        if t.dtype != torch.float8_e4m3fn:
-            _fail(f"{name}: must be float8_e4m3fn, got {t.dtype}", TypeError)
-        if not t.is_contiguous():
-            _fail(f"{name}: must be contiguous")
+    k_ptr = _codes_ptr("cache.k", k, None)
     pages, H, page, D = k.shape
-    if v.shape != (pages, H, D, page):
-        _fail(f"cache.v: shape {tuple(v.shape)} != {(pages, H, D, page)}")
-    _check_state("cache.k_scale", ks, torch.Size((pages, H)))
-    _check_state("cache.v_scale", vs, torch.Size((pages, H)))
+    v_ptr = _codes_ptr("cache.v", v, (pages, H, D, page))
     if ks is None or vs is None:
         _fail("cache: the scales are needed")
+    ks_ptr = _state_ptr("cache.k_scale", ks, (pages, H))
+    vs_ptr = _state_ptr("cache.v_scale", vs, (pages, H))
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         _fail("cache.table: must be an int32 [B,max_pages] tensor")
-    if table.dtype != torch.int32:
+    if table.dtype is not torch.int32:
         _fail(f"cache.table: must be torch.int32, got {table.dtype}", TypeError)
-    if table.shape[0] != B:
-        _fail(f"cache.table: {table.shape[0]} rows for {B} sequences")
-    if table.shape[1] > 1 and table.stride(1) != 1:
+    rows, width = table.shape
+    if rows != B:
+        _fail(f"cache.table: {rows} rows for {B} sequences")
+    stride, one = table.stride()
+    if width > 1 and one != 1:
         _fail("cache.table: rows must be contiguous")
-    return KvCacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(),
-                       table.stride(0), pages, page, table.shape[1], H, D)
+    return KvCacheDesc(k_ptr, v_ptr, ks_ptr, vs_ptr, table.data_ptr(), stride, pages, page, width, H, D)
 
 
 def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interleaved=False, q=None,
@@ -1042,38 +1125,35 @@ def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interlea
     that n_new excludes are left as they were (zeros in a new q_out)."""
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         _fail("k: must be a [B,H,T,D] tensor")
-    B, H, T, D = k.shape
+    B, _, T, _ = k.shape
     c = _kv_desc(cache, B)
-    bf = torch.bfloat16
-    shape = torch.Size((B, c.H, T, c.D))
-    _check_act("k", k, shape, bf)
-    _check_act("v", v, shape, bf)
-    _check_int("past", past, torch.Size((B,)))
-    if n_new is not None:
-        _check_int("n_new", n_new, torch.Size((B,)))
-    rot = 0
+    shape, bf = (B, c.H, T, c.D), torch.bfloat16
+    ka, va = _arg4("k", k, shape, bf), _arg4("v", v, shape, bf)
+    if past is None:
+        _fail("past: expected a tensor", TypeError)
+    past_ptr, n_ptr = _int_ptr("past", past, (B,)), _int_ptr("n_new", n_new, (B,))
+    rot, freq_ptr = 0, None
     if inv_freq is not None:
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             _fail("inv_freq: must be a float64 vector")
-        _check_int("inv_freq", inv_freq, inv_freq.shape, torch.float64)
-        rot = 2 * inv_freq.numel()
-    Hq = 0
+        freq_ptr, rot = _int_ptr("inv_freq", inv_freq, inv_freq.shape, torch.float64), 2 * inv_freq.numel()
+    Hq, qa, oa = 0, _NONE, _NONE
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             _fail("q: must be a [B,Hq,T,D] tensor")
         Hq = q.shape[1]
-        _check_act("q", q, torch.Size((B, Hq, T, D)), bf)
+        qa = _arg4("q", q, (B, Hq, T, c.D), bf)
         if q_out is not None:
-            _check_act("q_out", q_out, q.shape, bf)
+            oa = _arg4("q_out", q_out, (B, Hq, T, c.D), bf)
     elif q_out is not None:
         _fail("q_out: there is no q")
-    _check_device(k, ("v", v), ("past", past), ("n_new", n_new), ("inv_freq", inv_freq), ("q", q),
-                  ("q_out", q_out), *zip(KvCache._fields, cache))
+    dev = _same_device(k, ("v", v), ("past", past), ("n_new", n_new), ("inv_freq", inv_freq), ("q", q),
+                       ("q_out", q_out), *zip(KvCache._fields, cache))
     if q is not None and q_out is None:
-        q_out = torch.zeros_like(q) if n_new is not None else torch.empty_like(q)
-    rc = _lib().linrec_kv_append(context(k.device.index), ctypes.byref(c), B, T, _act(k), _act(v),
-                                 _ptr(past), _ptr(n_new), _ptr(inv_freq), rot, 1 if interleaved else 0,
-                                 Hq, _act(q), _act(q_out), _stream(k.device))
+        q_out = (torch.zeros if n_new is not None else torch.empty)((B, Hq, T, c.D), dtype=bf, device=q.device)
+        oa = _arg4("q_out", q_out, q_out.shape, bf)
+    rc = _lib().linrec_kv_append(context(dev), ctypes.byref(c), B, T, ka, va, past_ptr, n_ptr, freq_ptr, rot,
+                                 1 if interleaved else 0, Hq, qa, oa, _raw_stream(dev))
     _check(rc, "linrec_kv_append")
     return q_out
 
@@ -1087,31 +1167,30 @@ def kv_attn(cache: KvCache, q, past, *, n_new=None, scale=None, window=0, o=None
     left as they were (zeros in a new o)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         _fail("q: must be a [B,Hq,T,D] tensor")
-    B, Hq, T, D = q.shape
+    B, Hq, T, _ = q.shape
     c = _kv_desc(cache, B)
-    bf = torch.bfloat16
-    shape = torch.Size((B, Hq, T, c.D))
-    _check_act("q", q, shape, bf)
-    _check_int("past", past, torch.Size((B,)))
-    if n_new is not None:
-        _check_int("n_new", n_new, torch.Size((B,)))
-    if o is not None:
-        _check_act("o", o, shape, bf)
-    _check_state("lse", lse, torch.Size((B, Hq, T)))
-    if Hq % c.H:
+    shape, bf = (B, Hq, T, c.D), torch.bfloat16
+    qa = _arg4("q", q, shape, bf)
+    oa = None if o is None else _arg4("o", o, shape, bf)
+    if past is None:
+        _fail("past: expected a tensor", TypeError)
+    past_ptr, n_ptr = _int_ptr("past", past, (B,)), _int_ptr("n_new", n_new, (B,))
+    lse_ptr = _state_ptr("lse", lse, (B, Hq, T))
+    if c.H < 1 or Hq % c.H:
         _fail(f"q: {Hq} heads are no multiple of the cache's {c.H}")
-    need = int(_lib().linrec_kv_attn_workspace_bytes(ctypes.byref(c), B, T, Hq))
+    need = _lib().linrec_kv_attn_workspace_bytes(ctypes.byref(c), B, T, Hq)
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
-    _check_device(q, ("past", past), ("n_new", n_new), ("o", o), ("lse", lse), ("workspace", workspace),
-                  *zip(KvCache._fields, cache))
+    dev = _same_device(q, ("past", past), ("n_new", n_new), ("o", o), ("lse", lse), ("workspace", workspace),
+                       *zip(KvCache._fields, cache))
     if o is None:
-        o = torch.zeros_like(q) if n_new is not None else torch.empty_like(q)
+        o = (torch.zeros if n_new is not None else torch.empty)(shape, dtype=bf, device=q.device)
+        oa = _arg4("o", o, shape, bf)
     if workspace is None and need:
-        workspace = _bytes(need, q.device)
-    rc = _lib().linrec_kv_attn(context(q.device.index), ctypes.byref(c), B, T, Hq, _act(q), _ptr(past),
-                               _ptr(n_new), D ** -0.5 if scale is None else float(scale), int(window),
-                               _act(o), _ptr(lse), _ptr(workspace), _stream(q.device))
+        workspace = _bytes(need, q)
+    rc = _lib().linrec_kv_attn(context(dev), ctypes.byref(c), B, T, Hq, qa, past_ptr, n_ptr,
+                               c.D ** -0.5 if scale is None else float(scale), int(window), oa, lse_ptr,
+                               _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_kv_attn")
     return o
 
