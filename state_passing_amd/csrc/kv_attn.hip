@@ -64,8 +64,8 @@ __device__ __forceinline__ Frag<bf16> frag(bf16x8 v)
     return f;
 }
 
-// Running softmax of the 16 rows of a lane column (row t): the maximum of the
-// raw scores, this lane's share of the sum, and the sums O^T: tile dt of lane
+// Running softmax of the 16 rows of a lane column (row t): a bound on the raw
+// scores (softmax_tile), this lane's share of the sum, and the sums O^T: tile dt of lane
 // (g, t) holds features 16 dt + 4 g + r of row t.
 template <int D>
 struct RowState {
@@ -102,16 +102,19 @@ __device__ __forceinline__ void softmax_tile(RowState<D>& st, floatx4 (&x)[4], F
 #pragma unroll
     for (int i = 1; i < 4; ++i)
         mx = fmaxf(mx, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
-    mx = fmaxf(st.m, quad_max(mx));
-    const float ref = mx == -INFINITY ? 0.f : mx, off = ref * c2;
-    if (__any(mx > st.m)) {   // most tiles leave every row's maximum as it is
-        const float keep = __builtin_amdgcn_exp2f((st.m - ref) * c2);
+    // st.m only has to keep the exponents in range, so it is moved (for all 4
+    // lanes of a row together) when a score passes it by 2^8, not at every new
+    // maximum: most tiles then need neither the exchange nor the rescaling
+    if (__any((mx - st.m) * c2 > 8.f)) {
+        mx = fmaxf(st.m, quad_max(mx));
+        const float keep = __builtin_amdgcn_exp2f((st.m - (mx == -INFINITY ? 0.f : mx)) * c2);
         st.l *= keep;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
             st.acc[i] *= keep;
         st.m = mx;
     }
+    const float off = (st.m == -INFINITY ? 0.f : st.m) * c2;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -301,7 +304,9 @@ __device__ __forceinline__ float* part_stat(const AttnArgs& a, int split, int b,
 // of a split's keys each, straight from global memory to registers (no LDS, no
 // barrier: a fragment is 16 contiguous bytes of K's or V's rows), the next
 // tile's K and its page numbers loaded ahead, and join at the end.
-template <int D, int NR>
+// PAGED: a tile may span pages (pages of 16 and 32 tokens); else it lies in one,
+// whose number, scales and address are then the wave's, not the lane's.
+template <int D, int NR, bool PAGED>
 __global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kernel(AttnArgs a)
 {
     constexpr int KS = D / 64, DT = D / 16;
@@ -336,16 +341,25 @@ __global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kern
     auto pages = [&](int tl) {
         const int k = rg.k0 + 64 * tl;
         const bool in = tl < rg.last;
-        return Pages{in ? page_of(a.c, b, (k + 16 * (t >> 2)) >> shift) : -1,
-                     in ? page_of(a.c, b, (k + 16 * g) >> shift) : -1};
+        if constexpr (!PAGED) {
+            const int p = in ? __builtin_amdgcn_readfirstlane(page_of(a.c, b, k >> shift)) : -1;
+            return Pages{p, p};
+        } else {
+            return Pages{in ? page_of(a.c, b, (k + 16 * (t >> 2)) >> shift) : -1,
+                         in ? page_of(a.c, b, (k + 16 * g) >> shift) : -1};
+        }
     };
+    const int k_lane = (16 * (t >> 2) + (t & 3)) * D + 16 * g, v_lane = t * P + 16 * g;
     u32x4 kr[4][KS], vr[DT];
     float ks;
     auto load_k = [&](int tl, int page) {
         const int k = rg.k0 + 64 * tl;
         const int64_t ph = (int64_t)max(page, 0) * H + h;
-        const int in_page = ((k + 16 * (t >> 2)) & (P - 1)) + (t & 3);
-        const uint8_t* p = a.c.k + (ph * P + in_page) * D + 16 * g;
+        const uint8_t* p;
+        if constexpr (PAGED)
+            p = a.c.k + (ph * P + ((k + 16 * (t >> 2)) & (P - 1)) + (t & 3)) * D + 16 * g;
+        else
+            p = a.c.k + (ph * P + (k & (P - 1))) * D + k_lane;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -360,7 +374,11 @@ __global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kern
     for (; tl < rg.last; tl += 4) {
         const int k0 = rg.k0 + 64 * tl;
         const int64_t ph = (int64_t)max(now.v, 0) * H + h;
-        const uint8_t* vp = a.c.v + (ph * D + t) * P + ((k0 + 16 * g) & (P - 1));
+        const uint8_t* vp;
+        if constexpr (PAGED)
+            vp = a.c.v + (ph * D + t) * P + ((k0 + 16 * g) & (P - 1));
+        else
+            vp = a.c.v + (ph * D * P + (k0 & (P - 1))) + v_lane;
 #pragma unroll
         for (int i = 0; i < DT; ++i)
             vr[i] = *reinterpret_cast<const u32x4*>(vp + 16 * i * P);
@@ -524,7 +542,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 // 64 keys: the codes are converted once, on the way into LDS ([key][feature]
 // and, for V, [feature][key]), two buffers deep, while the loads of the next
 // tile are in flight.
-template <int D>
+template <int D, bool PAGED>
 __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
 {
     constexpr int NR = 2, ROWS = 64 * NR, DT = D / 16, KP = D + 16, VP = 64 + 16;
@@ -535,7 +553,10 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
     const int nbh = a.c.H * a.B;
     const int bh = blockIdx.x % nbh, h = bh % a.c.H, b = bh / a.c.H;
     const int unit = blockIdx.x / nbh, split = unit % a.nsplit;
-    const int tile = a.row_tiles - 1 - unit / a.nsplit;   // the longest first
+    // rows of later tokens read more keys: the longest first, and in the second
+    // half, which shares the CUs with the first, the shortest first
+    const int rank = unit / a.nsplit, half = (a.row_tiles + 1) / 2;
+    const int tile = rank < half ? a.row_tiles - 1 - rank : rank - half;
     const Span sp(a.past, a.n_new, b, a.T);
     const int rows = sp.n * a.group, r0 = tile * ROWS;
     if (r0 >= rows)
@@ -565,26 +586,41 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
     auto pages = [&](int tl) {
         const int k = rg.k0 + 64 * tl;
         const bool in = tl < rg.last;
+        if constexpr (PAGED) {
 #pragma unroll
-        for (int v = 0; v < KV; ++v)
-            pk[v] = in ? page_of(a.c, b, (k + kk + 256 / KL * v) >> shift) : -1;
-        pv = in ? page_of(a.c, b, (k + vg) >> shift) : -1;
+            for (int v = 0; v < KV; ++v)
+                pk[v] = in ? page_of(a.c, b, (k + kk + 256 / KL * v) >> shift) : -1;
+            pv = in ? page_of(a.c, b, (k + vg) >> shift) : -1;
+        } else {
+            pv = in ? __builtin_amdgcn_readfirstlane(page_of(a.c, b, k >> shift)) : -1;
+        }
     };
+    const int k_lane = kk * D + kf, v_lane = vf * P + vg;
     u32x4 kr[KV], vr[KV];
     float ks[KV], vs;
     bool v_ok;
     auto load = [&](int tl) {
         const int k = rg.k0 + 64 * tl;
-#pragma unroll
-        for (int v = 0; v < KV; ++v) {
-            const int64_t ph = (int64_t)max(pk[v], 0) * H + h;
-            kr[v] = *reinterpret_cast<const u32x4*>(a.c.k + (ph * P + ((k + kk + 256 / KL * v) & (P - 1))) * D + kf);
-            ks[v] = a.c.ks[ph];
-        }
         const int64_t ph = (int64_t)max(pv, 0) * H + h;
+        if constexpr (PAGED) {
 #pragma unroll
-        for (int v = 0; v < KV; ++v)
-            vr[v] = *reinterpret_cast<const u32x4*>(a.c.v + (ph * D + vf + 64 * v) * P + ((k + vg) & (P - 1)));
+            for (int v = 0; v < KV; ++v) {
+                const int64_t kh = (int64_t)max(pk[v], 0) * H + h;
+                kr[v] = *reinterpret_cast<const u32x4*>(a.c.k + (kh * P + ((k + kk + 256 / KL * v) & (P - 1))) * D + kf);
+                ks[v] = a.c.ks[kh];
+                vr[v] = *reinterpret_cast<const u32x4*>(a.c.v + (ph * D + vf + 64 * v) * P + ((k + vg) & (P - 1)));
+            }
+        } else {
+            const uint8_t* kp = a.c.k + (ph * P + (k & (P - 1))) * D;
+            const uint8_t* vp = a.c.v + (ph * D * P + (k & (P - 1)));
+            ks[0] = a.c.ks[ph];
+#pragma unroll
+            for (int v = 0; v < KV; ++v) {
+                kr[v] = *reinterpret_cast<const u32x4*>(kp + k_lane + 256 / KL * v * D);
+                vr[v] = *reinterpret_cast<const u32x4*>(vp + v_lane + 64 * v * P);
+                ks[v] = ks[0];
+            }
+        }
         vs = a.c.vs[ph];
         v_ok = pv >= 0;
     };
@@ -607,7 +643,7 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
             *reinterpret_cast<bf16x8*>(vp) = values8(vr[v][0], vr[v][1], vuse);
             *reinterpret_cast<bf16x8*>(vp + 8) = values8(vr[v][2], vr[v][3], vuse);
         }
-        if (tid < 4)
+        if (PAGED && tid < 4)
             there[buf][tid] = v_ok;
         if (any)
             bad[buf] = tl;
@@ -616,11 +652,13 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
         bad[tid] = -1;
     __syncthreads();
     int tl = rg.first;
+    bool ok = true;   // the page of the tile in LDS is there (one page a tile)
     if (tl < rg.last) {
         pages(tl);
         load(tl);
         pages(tl + 1);
         stage(tl, 0);
+        ok = v_ok;
     }
     __syncthreads();
     for (int buf = 0; tl < rg.last; ++tl, buf ^= 1) {
@@ -649,7 +687,9 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
                 }
             }
             const int w1 = min(rows, w0 + 16 * NR);
-            const unsigned groups = there[buf][0] | there[buf][1] << 1 | there[buf][2] << 2 | there[buf][3] << 3;
+            unsigned groups = ok ? 15u : 0u;
+            if constexpr (PAGED)
+                groups = there[buf][0] | there[buf][1] << 1 | there[buf][2] << 2 | there[buf][3] << 3;
             const bool whole = groups == 15u && whole_for(k0, w0, w1);
             Seen seen[NR];
 #pragma unroll
@@ -669,8 +709,10 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
                     return *reinterpret_cast<const u32x2*>(a.c.v + (ph * D + f) * P + ((k0 + k) & (P - 1)));
                 }, key);
         }
-        if (more)
+        if (more) {
             stage(tl + 1, buf ^ 1);
+            ok = v_ok;
+        }
         __syncthreads();
     }
 #pragma unroll
@@ -717,23 +759,23 @@ Plan plan_of(const linrec_kv_cache* c, int B, int T, int Hq)
     const int64_t key_tiles = ((int64_t)c->max_pages * c->page + 63) / 64;
     // splits fill the 256 CUs; each gets at least one tile a wave (token kernel)
     // or 8 tiles (piece kernel)
-    const int64_t want = ((p.token ? 1024 : 512) + blocks - 1) / blocks;
+    const int64_t want = (512 + blocks - 1) / blocks;
     const int64_t most = std::max<int64_t>(1, key_tiles / (p.token ? 4 : 8));
     p.nsplit = (int)std::min<int64_t>(std::min(want, most), MAX_SPLITS);
     return p;
 }
 
-template <int D>
+template <int D, bool PAGED>
 hipError_t launch_attn(const AttnArgs& a, bool token, hipStream_t s)
 {
     if (token) {
         const dim3 grid(a.row_tiles * a.nsplit, a.c.H, a.B);
         if (a.rows <= 16)
-            launch_kernel(kv_attn_token_kernel<D, 1>, grid, dim3(256), s, a);
+            launch_kernel(kv_attn_token_kernel<D, 1, PAGED>, grid, dim3(256), s, a);
         else
-            launch_kernel(kv_attn_token_kernel<D, 2>, grid, dim3(256), s, a);
+            launch_kernel(kv_attn_token_kernel<D, 2, PAGED>, grid, dim3(256), s, a);
     } else {
-        launch_kernel(kv_attn_piece_kernel<D>, dim3(a.c.H * a.B * a.row_tiles * a.nsplit), dim3(256), s, a);
+        launch_kernel(kv_attn_piece_kernel<D, PAGED>, dim3(a.c.H * a.B * a.row_tiles * a.nsplit), dim3(256), s, a);
     }
     if (a.nsplit > 1)
         launch_kernel(kv_attn_join_kernel<D>, dim3(a.rows, a.c.H, a.B), dim3(256), s, a);
@@ -813,7 +855,9 @@ linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int3
     a.part = (float*)workspace;
     hipStream_t s = (hipStream_t)stream;
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_KV_ATTN, s, [&] {
-        return cache->D == 128 ? launch_attn<128>(a, p.token, s) : launch_attn<64>(a, p.token, s);
+        if (cache->D == 128)
+            return cache->page < 64 ? launch_attn<128, true>(a, p.token, s) : launch_attn<128, false>(a, p.token, s);
+        return cache->page < 64 ? launch_attn<64, true>(a, p.token, s) : launch_attn<64, false>(a, p.token, s);
     }));
     return LINREC_OK;
 }
