@@ -239,9 +239,25 @@ __device__ __forceinline__ void give_nonfinite(RowState<D> (&st)[NR], const Seen
     }
 }
 
-// Weights and values of one tile, given its scores; vfrag(dt, s): V's fragment.
+// Asks the scheduler for the order of a product loop over READS fragments from
+// LDS, NR products each: four reads ahead of the products, where it would read
+// two, wait, and multiply (piece kernel, 4096 tokens behind 12K: 530 -> 503 us).
+template <int NR, int READS>
+__device__ __forceinline__ void read_ahead()
+{
+    constexpr int AHEAD = 4;
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);        // LDS reads
+#pragma unroll
+    for (int i = 0; i < READS - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, NR, 0);         // matrix instructions
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, AHEAD * NR, 0);
+}
+
+// Weights and values of one tile, given its scores; LDS: they are read from LDS; vfrag(dt, s): V's fragment.
 // whole: every row sees all of the tile (wave-uniform).
-template <int D, int NR, typename VFrag, typename Key>
+template <int D, int NR, bool LDS, typename VFrag, typename Key>
 __device__ __forceinline__ void attend(RowState<D> (&st)[NR], floatx4 (&x)[NR][4], float c2, bool whole,
                                        const Seen (&seen)[NR], VFrag vfrag, Key key)
 {
@@ -267,6 +283,8 @@ __device__ __forceinline__ void attend(RowState<D> (&st)[NR], floatx4 (&x)[NR][4
             for (int n = 0; n < NR; ++n)
                 st[n].acc[dt] = mma(v, p[n][s], st[n].acc[dt]);
         }
+    if constexpr (LDS)
+        read_ahead<NR, D / 8>();
 }
 
 // A row's place in o and lse.
@@ -423,7 +441,7 @@ __global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kern
             for (int i = 0; i < DT; ++i)
                 bad |= take_nonfinite(vr[i], vs);
         }
-        attend<D, NR>(st, x, a.c2, whole, seen,
+        attend<D, NR, false>(st, x, a.c2, whole, seen,
                       [&](int dt, int s) { return frag(values8(vr[dt][2 * s], vr[dt][2 * s + 1], vuse)); }, key);
         if (__any(bad))
             give_nonfinite<D, NR>(st, seen, [&](int k, int f, float& scale) {
@@ -686,6 +704,7 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
                         x[n][i] = mma(kfr, q[n][s], x[n][i]);
                 }
             }
+            read_ahead<NR, 4 * (D / 32)>();
             const int w1 = min(rows, w0 + 16 * NR);
             unsigned groups = ok ? 15u : 0u;
             if constexpr (PAGED)
@@ -701,7 +720,7 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
             auto vfrag = [&](int dt, int s) {
                 return frag(*reinterpret_cast<const bf16x8*>(vb + (16 * dt + t) * VP + 32 * s + 8 * g));
             };
-            attend<D, NR>(st, x, a.c2, whole, seen, vfrag, key);
+            attend<D, NR, true>(st, x, a.c2, whole, seen, vfrag, key);
             if (bad[buf] == tl)
                 give_nonfinite<D, NR>(st, seen, [&](int k, int f, float& scale) {
                     const int64_t ph = (int64_t)max(page_of(a.c, b, (k0 + k) >> shift), 0) * H + h;
