@@ -497,35 +497,27 @@ __global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kern
     }
 }
 
-// Joins the splits of a row, one workgroup a row: the splits' maxima and sums
-// by one lane each, their sums of values by D / 4 lanes for every 1024 / D-th
-// split, joined through LDS in a fixed order.
+// Joins the splits of a row, one wave a row: lane s forms split s's factor, then
+// D / 4 lanes take the sums of every (256 / D)-th split, added in a fixed order.
 constexpr int MAX_SPLITS = 64;
 
 template <int D>
 __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 {
-    constexpr int LPR = D / 4, G = 256 / LPR;
-    __shared__ float factor[MAX_SPLITS];
-    __shared__ floatx4 sums[G][LPR];
-    const int row = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    constexpr int LPR = D / 4, G = 64 / LPR;
+    const int row = blockIdx.x * 4 + wave_id(), h = blockIdx.y, b = blockIdx.z;
     const Span sp(a.past, a.n_new, b, a.T);
     if (row >= sp.n * a.group)
         return;
-    const int lane = threadIdx.x & 63, grp = threadIdx.x / LPR, f4 = threadIdx.x % LPR;
-    constexpr int PER = MAX_SPLITS / G;
-    floatx4 y[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i)     // in flight while the factors are formed
-        if (grp + G * i < a.nsplit)
-            y[i] = *reinterpret_cast<const floatx4*>(part_row<D>(a, grp + G * i, b, h, row) + 4 * f4);
-    // every wave forms them for itself
+    const int lane = lane_id(), grp = lane / LPR, f4 = lane % LPR;
     float m = -INFINITY, l = 0.f;
     if (lane < a.nsplit) {
         const float* stat = part_stat<D>(a, lane, b, h, row);
         m = stat[0];
         l = stat[1];
     }
+    const float* y = part_row<D>(a, 0, b, h, row) + 4 * f4;
+    const int64_t next = (int64_t)a.B * a.c.H * a.rows * (D + 2);   // from one split to the next
     float top = m;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
@@ -535,22 +527,22 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         l += __shfl_xor(l, off, 64);
-    if (threadIdx.x < 64)
-        factor[lane] = f;
-    __syncthreads();
     floatx4 sum = zero4();
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (grp + G * i < a.nsplit)
-            sum += y[i] * factor[grp + G * i];
-    sums[grp][f4] = sum;
-    __syncthreads();
-    if (grp == 0) {
-#pragma unroll
-        for (int i = 1; i < G; ++i)
-            sum += sums[i][f4];
-        write_row<D>(a, b, h, row, 4 * f4, sum, top, l);
+#pragma unroll 4
+    for (int s0 = 0; s0 < a.nsplit; s0 += G) {
+        const int s = s0 + grp, at = min(s, a.nsplit - 1);
+        const floatx4 part = *reinterpret_cast<const floatx4*>(y + at * next);
+        const float w = __shfl(f, at, 64);
+        if (s < a.nsplit)
+            sum += part * w;
     }
+#pragma unroll
+    for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sum[j] += __shfl_xor(sum[j], off, 64);
+    if (grp == 0)
+        write_row<D>(a, b, h, row, 4 * f4, sum, top, l);
 }
 
 // ---- many rows: pieces of a prompt ------------------------------------------
@@ -797,7 +789,7 @@ hipError_t launch_attn(const AttnArgs& a, bool token, hipStream_t s)
         launch_kernel(kv_attn_piece_kernel<D, PAGED>, dim3(a.c.H * a.B * a.row_tiles * a.nsplit), dim3(256), s, a);
     }
     if (a.nsplit > 1)
-        launch_kernel(kv_attn_join_kernel<D>, dim3(a.rows, a.c.H, a.B), dim3(256), s, a);
+        launch_kernel(kv_attn_join_kernel<D>, dim3((a.rows + 3) / 4, a.c.H, a.B), dim3(256), s, a);
     return hipGetLastError();
 }
 
