@@ -55,10 +55,18 @@ __device__ __forceinline__ void rotate_unit(float (&y)[16], int u, int half, boo
     }
 }
 
-__device__ __forceinline__ void load_unit(float (&y)[16], const bf16* row, int v0, int v1)
+struct Unit {
+    bf16x8 a, b;
+};
+
+__device__ __forceinline__ Unit load_unit(const bf16* row, int v0, int v1)
 {
-    const bf16x8 a = *reinterpret_cast<const bf16x8*>(row + 8 * v0);
-    const bf16x8 b = *reinterpret_cast<const bf16x8*>(row + 8 * v1);
+    return Unit{*reinterpret_cast<const bf16x8*>(row + 8 * v0), *reinterpret_cast<const bf16x8*>(row + 8 * v1)};
+}
+
+__device__ __forceinline__ void widen(float (&y)[16], const Unit& u)
+{
+    const bf16x8 a = u.a, b = u.b;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         y[i] = (float)a[i];
@@ -155,11 +163,29 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int j, int h, i
             if (t >= lo && t < hi)
                 vr[i][r] = *reinterpret_cast<const u32x4*>(a.v.head(b, h) + (t0 + t) * a.v.st + 8 * vv);
         }
+    Unit kraw[KI];
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+        const int t = kr + KR * i;
+        if (t >= lo && t < hi)
+            kraw[i] = load_unit(a.k.head(b, h) + (t0 + t) * a.k.st, v0, v1);
+    }
+    // (while those loads are in flight)
+    // an earlier touched block with the same page owns it
+    int dup = 0;
+    const int64_t before = (int64_t)b * a.nblk + j;
+    for (int64_t e = tid; e < before; e += 256) {
+        const int eb = (int)(e / a.nblk), ej = (int)(e % a.nblk);
+        const Span es(a.past, a.n_new, eb, a.T);
+        const int first = es.past >> a.c.shift;
+        if (es.n > 0 && ej <= ((es.past + es.n - 1) >> a.c.shift) - first)
+            dup |= page_of(a.c, eb, first + ej) == page;
+    }
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
         const int t = kr + KR * i;
         if (t >= lo && t < hi) {
-            load_unit(ky[i], a.k.head(b, h) + (t0 + t) * a.k.st, v0, v1);
+            widen(ky[i], kraw[i]);
             rotate_unit(ky[i], u, a.half, a.inter,
                         [&](int pair, float& c, float& s) { turn(base + t, a.freq[pair], c, s); });
 #pragma unroll
@@ -174,16 +200,6 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int j, int h, i
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 vmax = fmaxf(vmax, finite_abs((float)__builtin_bit_cast(bf16x8, vr[i][r])[e]));
-    // an earlier touched block with the same page owns it
-    int dup = 0;
-    const int64_t before = (int64_t)b * a.nblk + j;
-    for (int64_t e = tid; e < before; e += 256) {
-        const int eb = (int)(e / a.nblk), ej = (int)(e % a.nblk);
-        const Span es(a.past, a.n_new, eb, a.T);
-        const int first = es.past >> a.c.shift;
-        if (es.n > 0 && ej <= ((es.past + es.n - 1) >> a.c.shift) - first)
-            dup |= page_of(a.c, eb, first + ej) == page;
-    }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
         kmax = fmaxf(kmax, __shfl_xor(kmax, off, 64));
@@ -271,7 +287,7 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int tile, in
         int v0, v1;
         unit_vectors(u, a.half, a.inter, v0, v1);
         float y[16];
-        load_unit(y, a.q.head(b, h) + (int64_t)(t0 + r) * a.q.st, v0, v1);
+        widen(y, load_unit(a.q.head(b, h) + (int64_t)(t0 + r) * a.q.st, v0, v1));
         rotate_unit(y, u, a.half, a.inter, [&](int pair, float& c, float& s) {
             c = cs[r * a.half + pair].x;
             s = cs[r * a.half + pair].y;
