@@ -86,6 +86,40 @@ __device__ __forceinline__ void store_vec(OT* p, const float* y, int n)
     }
 }
 
+// N floats of a carried state, n of which exist; p may be NULL (zeros).
+template <int N>
+__device__ __forceinline__ void load_floats(float (&y)[N], const float* p, int n)
+{
+    if (p && n >= N && ((uintptr_t)p & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const floatx4 v = *reinterpret_cast<const floatx4*>(p + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[j + i] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            y[j] = p && j < n ? p[j] : 0.f;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_floats(float* p, const float (&y)[N], int n)
+{
+    if (n >= N && ((uintptr_t)p & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+            *reinterpret_cast<floatx4*>(p + j) = floatx4{y[j], y[j + 1], y[j + 2], y[j + 3]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < n)
+                p[j] = y[j];
+    }
+}
+
 // 1 - exp(g): near 0 the difference would cancel (relative error 2^-24 / |g|),
 // so the series takes over there; its first dropped term, g^5 / 720, is 2^-24 of
 // the sum at |g| = 1/8.
@@ -116,11 +150,11 @@ struct Place {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void load_run(u32x4 (&v)[RUN], const T* base, int64_t st, int t0, int nt, int nc)
+template <typename T, int R = RUN>
+__device__ __forceinline__ void load_run(u32x4 (&v)[R], const T* base, int64_t st, int t0, int nt, int nc)
 {
 #pragma unroll
-    for (int r = 0; r < RUN; ++r)
+    for (int r = 0; r < R; ++r)
         v[r] = r < nt ? load_vec(base + (int64_t)(t0 + r) * st, nc) : u32x4{0u, 0u, 0u, 0u};
 }
 
@@ -131,13 +165,19 @@ __device__ __forceinline__ void load_run(u32x4 (&v)[RUN], const T* base, int64_t
 // Per segment and channel, in workspace: its map (product, sum) in 64 bits and
 // the state leaving it in 32, both all ones until they are published, each by one
 // atomic store: a reader that sees a value sees all of it, so no fence orders
-// anything.  Tickets give workgroups their segments in the order they start, so
-// whoever waits for a map waits for a workgroup that runs already, and that
-// publishes its map before it waits for anything itself: every wait ends.
+// anything.  Counters hand out the segments of the chains (a channel group of a
+// batch each) in the order the workgroups start: whoever waits for a map waits
+// for a workgroup that runs already, and that publishes its map before it waits
+// for anything itself, so every wait ends.  One counter is the bottleneck of a
+// launch (about 25 ns a workgroup); one a chain lets chains drift apart, and rows
+// are then read 128 bytes here and there.
 constexpr unsigned UNSET = 0xffffffffu;
 
+constexpr int COUNTERS = 8;   // at most
+constexpr int COUNTER = 16;   // words from one counter to the next (64 bytes)
+
 struct Chain {
-    unsigned* ticket;
+    unsigned* counter;
     unsigned long long* map;
     unsigned* value;
 };
@@ -239,17 +279,22 @@ struct Work {
     int cg, pos, b;
     __device__ __forceinline__ Work(const Chain& ch, int ncg, int B, int nseg)
     {
-        unsigned id = blockIdx.x;
+        const int chains = ncg * B, c = blockIdx.x % chains;
+        int chain = c;
+        pos = 0;
         if (nseg > 1) {
-            __shared__ unsigned ticket;
+            // counter k hands out the segments of chains [first, end), a row of them at a time
+            const int K = min(COUNTERS, chains), k = (int)((int64_t)c * K / chains);
+            const int first = (int)(((int64_t)k * chains + K - 1) / K), end = (int)(((int64_t)(k + 1) * chains + K - 1) / K);
+            __shared__ int next;
             if (threadIdx.x == 0)
-                ticket = atomicAdd(ch.ticket, 1u) + 1u;   // the counter starts at all ones
+                next = (int)(atomicAdd(ch.counter + k * COUNTER, 1u) + 1u);   // starts at all ones
             __syncthreads();
-            id = ticket;
+            pos = next / (end - first);
+            chain = first + next % (end - first);
         }
-        cg = id % ncg;
-        b = id / ncg % B;
-        pos = id / ncg / B;
+        cg = chain % ncg;
+        b = chain / ncg;
     }
 };
 
@@ -277,14 +322,45 @@ __global__ __launch_bounds__(256) void diag_clear_kernel(u32x4* p, int64_t n)
         p[i] = u32x4{UNSET, UNSET, UNSET, UNSET};
 }
 
-// Forward.  NRUN = 32: 256 threads, a segment.  NRUN = 1: 64 threads, up to 8
-// tokens of 64 vectors of channels (generation: no LDS, no barrier).
-template <typename T, typename OT, bool MIX, int NRUN>
-__global__ __launch_bounds__(NRUN == 1 ? 64 : 256, MIX && sizeof(T) == 2 ? 3 : 4) void diag_fwd_kernel(
+// Forward over R tokens at most, for generation: one lane a vector of channels,
+// no LDS, no barrier.
+template <typename T, typename OT, bool MIX, int R>
+__global__ __launch_bounds__(64) void diag_token_kernel(Act<const T> g, Act<const T> x, Act<OT> h, const float* h_in,
+                                                        float* states, float* h_out, int T_, int C)
+{
+    constexpr int N = Vec<T>::N;
+    const int c0 = (blockIdx.x * 64 + threadIdx.x) * N, b = blockIdx.y, nc = C - c0;
+    if (nc <= 0)
+        return;
+    u32x4 gv[R], xv[R];
+    load_run<T, R>(gv, g.ptr + b * g.sb + c0, g.st, 0, T_, nc);
+    load_run<T, R>(xv, x.ptr + b * x.sb + c0, x.st, 0, T_, nc);
+    const int64_t at = (int64_t)b * C + c0;
+    float hc[N];
+    load_floats<N>(hc, h_in ? h_in + at : nullptr, nc);
+    store_floats<N>(states + at, hc, nc);
+    OT* hp = h.ptr + b * h.sb + c0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float gg = vec_get<T>(gv[r], j), a = __expf(gg);
+            hc[j] = a * hc[j] + added<MIX>(gg, a, vec_get<T>(xv[r], j));
+        }
+        if (r < T_)
+            store_vec<OT, N>(hp + (int64_t)r * h.st, hc, nc);
+    }
+    store_floats<N>(h_out + at, hc, nc);
+}
+
+// Forward over a segment.
+template <typename T, typename OT, bool MIX>
+__global__ __launch_bounds__(256, MIX && sizeof(T) == 2 ? 3 : 4) void diag_fwd_kernel(
     Act<const T> g, Act<const T> x, Act<OT> h, const float* h_in, float* states, float* h_out, Chain ch,
     int B_, int T_, int C, int ncg, int nseg)
 {
-    constexpr int N = Vec<T>::N, NT = NRUN == 1 ? 64 : 256, CH = NT / NRUN * N;
+    constexpr int N = Vec<T>::N, NT = 256, NRUN = SEG / RUN, CH = NT / NRUN * N;
+    __shared__ float sP[NRUN][CH], sB[NRUN][CH];
     const Work work(ch, ncg, B_, nseg);
     const int cg = work.cg, seg = work.pos, b = work.b;
     const Place<T, NRUN> p(cg, seg, T_, C, NT);
@@ -292,69 +368,59 @@ __global__ __launch_bounds__(NRUN == 1 ? 64 : 256, MIX && sizeof(T) == 2 ? 3 : 4
     load_run(gv, g.ptr + b * g.sb + p.c0, g.st, p.t0, p.nt, p.nc);
     load_run(xv, x.ptr + b * x.sb + p.c0, x.st, p.t0, p.nt, p.nc);
     float hc[N];
-    if constexpr (NRUN == 1) {
+    float P[N], B[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            hc[j] = h_in && j < p.nc ? h_in[(int64_t)b * C + p.c0 + j] : 0.f;
-            if (j < p.nc)
-                states[(int64_t)b * C + p.c0 + j] = hc[j];
-        }
-    } else {
-        __shared__ float sP[NRUN][CH], sB[NRUN][CH];
-        float P[N], B[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            P[j] = 1.f;
-            B[j] = 0.f;
-        }
-#pragma unroll
-        for (int r = 0; r < RUN; ++r) {
-            after<N>(gv[r], xv[r], B);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float gg = vec_get<T>(gv[r], j), a = __expf(gg);
-                P[j] *= a;
-                B[j] = a * B[j] + added<MIX>(gg, a, vec_get<T>(xv[r], j));
-            }
-        }
-        const int cl = (threadIdx.x % (NT / NRUN)) * N;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            sP[p.run][cl + j] = P[j];
-            sB[p.run][cl + j] = B[j];
-        }
-        __syncthreads();
-        const int c = cg * CH + threadIdx.x;
-        if (threadIdx.x < CH && c < C) {
-            float s = seg == 0 && h_in ? h_in[(int64_t)b * C + c] : 0.f;
-            if (nseg > 1) {
-                const int64_t chain = (int64_t)b * nseg * C + c, at = chain + (int64_t)seg * C;
-                float sp = 1.f, sb = 0.f;
-#pragma unroll 8
-                for (int i = 0; i < NRUN; ++i) {
-                    sb = sP[i][threadIdx.x] * sb + sB[i][threadIdx.x];
-                    sp *= sP[i][threadIdx.x];
-                }
-                publish_map(ch.map + at, sp, sb);
-                if (seg > 0)
-                    s = chain_enter(ch.map + chain, ch.value + chain, C, seg);
-                publish_value(ch.value + at, __builtin_fmaf(sp, s, sb));
-            }
-            states[((int64_t)b * nseg + seg) * C + c] = s;
-#pragma unroll 8
-            for (int i = 0; i < NRUN; ++i) {   // sB becomes the state entering run i
-                const float bb = sB[i][threadIdx.x];
-                sB[i][threadIdx.x] = s;
-                s = sP[i][threadIdx.x] * s + bb;
-            }
-            if (seg == nseg - 1)
-                h_out[(int64_t)b * C + c] = s;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            hc[j] = sB[p.run][cl + j];
+    for (int j = 0; j < N; ++j) {
+        P[j] = 1.f;
+        B[j] = 0.f;
     }
+#pragma unroll
+    for (int r = 0; r < RUN; ++r) {
+        after<N>(gv[r], xv[r], B);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float gg = vec_get<T>(gv[r], j), a = __expf(gg);
+            P[j] *= a;
+            B[j] = a * B[j] + added<MIX>(gg, a, vec_get<T>(xv[r], j));
+        }
+    }
+    const int cl = (threadIdx.x % (NT / NRUN)) * N;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        sP[p.run][cl + j] = P[j];
+        sB[p.run][cl + j] = B[j];
+    }
+    __syncthreads();
+    const int c = cg * CH + threadIdx.x;
+    if (threadIdx.x < CH && c < C) {
+        float s = seg == 0 && h_in ? h_in[(int64_t)b * C + c] : 0.f;
+        if (nseg > 1) {
+            const int64_t chain = (int64_t)b * nseg * C + c, at = chain + (int64_t)seg * C;
+            float sp = 1.f, sb = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < NRUN; ++i) {
+                sb = sP[i][threadIdx.x] * sb + sB[i][threadIdx.x];
+                sp *= sP[i][threadIdx.x];
+            }
+            publish_map(ch.map + at, sp, sb);
+            if (seg > 0)
+                s = chain_enter(ch.map + chain, ch.value + chain, C, seg);
+            publish_value(ch.value + at, __builtin_fmaf(sp, s, sb));
+        }
+        states[((int64_t)b * nseg + seg) * C + c] = s;
+#pragma unroll 8
+        for (int i = 0; i < NRUN; ++i) {   // sB becomes the state entering run i
+            const float bb = sB[i][threadIdx.x];
+            sB[i][threadIdx.x] = s;
+            s = sP[i][threadIdx.x] * s + bb;
+        }
+        if (seg == nseg - 1)
+            h_out[(int64_t)b * C + c] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        hc[j] = sB[p.run][cl + j];
     OT* hp = h.ptr + b * h.sb + p.c0;
 #pragma unroll
     for (int r = 0; r < RUN; ++r) {
@@ -366,12 +432,6 @@ __global__ __launch_bounds__(NRUN == 1 ? 64 : 256, MIX && sizeof(T) == 2 ? 3 : 4
         }
         if (r < p.nt)
             store_vec<OT, N>(hp + (int64_t)(p.t0 + r) * h.st, hc, p.nc);
-    }
-    if constexpr (NRUN == 1) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < p.nc)
-                h_out[(int64_t)b * C + p.c0 + j] = hc[j];
     }
 }
 
@@ -566,14 +626,16 @@ hipError_t dispatch(const linrec_diag_desc* d, F&& f)
     return d->out_dtype == LINREC_F32 ? form(bf16{}, float{}) : form(bf16{}, bf16{});
 }
 
-// Workspace: the ticket (16 bytes), then the maps, then the states leaving.
+// Workspace: the chains' counters, then the maps, then the states leaving.
 int64_t chain_cells(const linrec_diag_desc* d) { return (int64_t)d->B * nseg_of(d->T) * d->C; }
+
+constexpr int64_t COUNTER_BYTES = COUNTERS * COUNTER * sizeof(unsigned);
 
 Chain chain_of(const linrec_diag_desc* d, void* workspace)
 {
     if (d->T <= SEG)
         return Chain{nullptr, nullptr, nullptr};
-    unsigned long long* map = (unsigned long long*)((char*)workspace + 16);
+    unsigned long long* map = (unsigned long long*)((char*)workspace + COUNTER_BYTES);
     return Chain{(unsigned*)workspace, map, (unsigned*)(map + chain_cells(d))};
 }
 
@@ -596,13 +658,17 @@ hipError_t launch_diag_fwd(const linrec_diag_desc* d, const linrec_tensor& g, co
         const int cpg = channels_per_group(d->dtype), ncg = (d->C + cpg - 1) / cpg;
         const int nseg = (int)nseg_of(d->T);
         if (d->T <= RUN) {
-            const int n = (d->C + 64 * Vec<T>::N - 1) / (64 * Vec<T>::N);
-            launch_kernel(diag_fwd_kernel<T, OT, MIX, 1>, dim3(n * d->B), dim3(64), s, cact<T>(g), cact<T>(x),
-                          mact<OT>(h), h_in, states, h_out, Chain{}, d->B, d->T, d->C, n, 1);
+            const dim3 grid((d->C + 64 * Vec<T>::N - 1) / (64 * Vec<T>::N), d->B);
+            if (d->T == 1)
+                launch_kernel(diag_token_kernel<T, OT, MIX, 1>, grid, dim3(64), s, cact<T>(g), cact<T>(x), mact<OT>(h),
+                              h_in, states, h_out, d->T, d->C);
+            else
+                launch_kernel(diag_token_kernel<T, OT, MIX, RUN>, grid, dim3(64), s, cact<T>(g), cact<T>(x),
+                              mact<OT>(h), h_in, states, h_out, d->T, d->C);
             return hipGetLastError();
         }
         clear_chain(d, workspace, s);
-        launch_kernel(diag_fwd_kernel<T, OT, MIX, SEG / RUN>, dim3(ncg * nseg * d->B), dim3(256), s, cact<T>(g),
+        launch_kernel(diag_fwd_kernel<T, OT, MIX>, dim3(ncg * nseg * d->B), dim3(256), s, cact<T>(g),
                       cact<T>(x), mact<OT>(h), h_in, states, h_out, chain_of(d, workspace), d->B, d->T, d->C,
                       ncg, nseg);
         return hipGetLastError();
@@ -654,7 +720,7 @@ size_t linrec_diag_workspace_bytes(const linrec_diag_desc* d)
 {
     if (check_diag_desc(d) != LINREC_OK || d->T <= SEG)
         return 0;
-    return (16 + 12 * (size_t)chain_cells(d) + 15) / 16 * 16;
+    return ((size_t)COUNTER_BYTES + 12 * (size_t)chain_cells(d) + 15) / 16 * 16;
 }
 
 linrec_status linrec_diag_fwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec_tensor g, linrec_tensor x,
