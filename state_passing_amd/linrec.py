@@ -958,7 +958,7 @@ def diag_fwd(g, x, h_in=None, *, form="plain", h=None, h_out=None, states=None, 
     ga, xa = _arg3("g", g, shape, g.dtype), _arg3("x", x, shape, g.dtype)
     ha = None if h is None else _arg3("h", h, shape, odt)
     in_ptr, out_ptr = _state_ptr("h_in", h_in, carry), _state_ptr("h_out", h_out, carry)
-    need, work = diag_states_bytes(d), diag_workspace_bytes(d)
+    need, work = diag_states_bytes(d), diag_workspace_bytes(d) if shape[1] > 256 else 0
     if states is not None:
         _check_buffer("states", states, need)
     if workspace is not None:
@@ -992,7 +992,7 @@ def diag_bwd(g, x, states, dh, dh_out=None, *, form="plain", dg=None, dx=None, d
     dga = None if dg is None else _arg3("dg", dg, shape, odt)
     dxa = None if dx is None else _arg3("dx", dx, shape, odt)
     out_ptr, in_ptr = _state_ptr("dh_out", dh_out, carry), _state_ptr("dh_in", dh_in, carry)
-    work = diag_workspace_bytes(d)
+    work = diag_workspace_bytes(d) if shape[1] > 256 else 0
     _check_buffer("states", states, diag_states_bytes(d))
     if workspace is not None:
         _check_buffer("workspace", workspace, work)
