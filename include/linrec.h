@@ -591,7 +591,7 @@ size_t linrec_kv_attn_workspace_bytes(const linrec_kv_cache* cache, int32_t B, i
  * (linrec_kv_append).  Query head h reads key/value head h / (Hq / H):
  *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j - lse_i),
  * over the cached tokens j with past[b] + i - window < j <= past[b] + i
- * (window <= 0: no lower bound).  lse: fp32 contiguous [B,Hq,T], the natural
+ * (window <= 0 or >= LINREC_MAX_T: no lower bound).  lse: fp32 contiguous [B,Hq,T], the natural
  * logarithm of the sum, or NULL.  A row that sees no token gets o = 0 and
  * lse = -inf.  Cached values that a row does not see never reach it, whatever
  * they are.  Hq: a multiple of cache->H.  scale: finite.

@@ -834,6 +834,10 @@ linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int3
             (st = check_view(q, B, Hq, T, cache->D, 2, false)) != LINREC_OK ||
             (st = check_view(o, B, Hq, T, cache->D, 2, true)) != LINREC_OK)
             return st;
+        const Plan p = plan_of(cache, B, T, Hq);
+        // a launch holds at most 2^32 - 1 threads along x
+        if ((int64_t)B * cache->H * p.row_tiles * p.nsplit > 0xffffff)
+            return LINREC_E_SHAPE;
         if (!aligned(lse, 4))
             return LINREC_E_ALIGN;
         if (linrec_kv_attn_workspace_bytes(cache, B, T, Hq) && (st = check_buffer(workspace)) != LINREC_OK)
@@ -854,7 +858,7 @@ linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int3
     a.T = T;
     a.Hq = Hq;
     a.group = Hq / cache->H;
-    a.window = window;
+    a.window = window < LINREC_MAX_T ? window : 0;   // offsets within a window fit 31 bits
     // the products see q with the scale's sign; a factor of 0 would make
     // 0 * inf of hidden scores
     a.negate = scale < 0.f;

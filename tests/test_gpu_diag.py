@@ -125,10 +125,11 @@ def test_channel_counts_that_end_inside_a_vector(C, dtype):
     assert all((o[..., C:] == 5).all() for o in outs)
 
 
-def test_strides_and_aliases():
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_strides_and_aliases(dtype):
     """Token-major memory ([T,B,C]); gradients written over the inputs."""
     B, T, C = 3, 600, 64
-    g, x, h_in, dh, dh_out = draw(11, B, T, C, BF)
+    g, x, h_in, dh, dh_out = draw(11, B, T, C, dtype)
     tb = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
     want = check(g, x, h_in, dh, dh_out, True, view=tb)
     gd, xd, dd, h, r = (t.to(DEV) for t in (g, x, dh, h_in, dh_out))

@@ -182,6 +182,13 @@ def test_attention_scales(T, scale):
     check_attn(cache, (q * 0.3).to(torch.bfloat16), [60, 20], [T, T], scale=scale)
 
 
+@pytest.mark.parametrize("T", [1, 70])
+@pytest.mark.parametrize("window", [1, 2147479551, 2147483647])
+def test_attention_windows_at_the_ends(T, window):
+    _, cache, q = draw(9, 2, T, 4, 2, 64, 32, 9)
+    check_attn(cache, q, [200, 3], [T, T], window=window)
+
+
 @pytest.mark.parametrize("T", [1, 5, 70])
 def test_attention_token_major_views_and_replays(T):
     """q and o as [B,T,H,D] memory; the same call captured: every replay, between
