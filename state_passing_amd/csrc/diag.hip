@@ -125,8 +125,9 @@ __device__ __forceinline__ void store_floats(float* p, const float (&y)[N], int 
 // the sum at |g| = 1/8.
 __device__ __forceinline__ float one_minus_exp(float g, float a)
 {
-    const float s = 1.f + g * (1.f / 2 + g * (1.f / 6 + g * (1.f / 24 + g * (1.f / 120))));
-    return fabsf(g) < 0.125f ? -g * s : 1.f - a;
+    float s = -g * (1.f + g * (1.f / 2 + g * (1.f / 6 + g * (1.f / 24 + g * (1.f / 120)))));
+    asm("" : "+v"(s));   // both sides and a select: a branch for every value costs more
+    return fabsf(g) < 0.125f ? s : 1.f - a;
 }
 
 template <bool MIX>
@@ -355,7 +356,7 @@ __global__ __launch_bounds__(64) void diag_token_kernel(Act<const T> g, Act<cons
 
 // Forward over a segment.
 template <typename T, typename OT, bool MIX>
-__global__ __launch_bounds__(256, MIX && sizeof(T) == 2 ? 3 : 4) void diag_fwd_kernel(
+__global__ __launch_bounds__(256, 4) void diag_fwd_kernel(
     Act<const T> g, Act<const T> x, Act<OT> h, const float* h_in, float* states, float* h_out, Chain ch,
     int B_, int T_, int C, int ncg, int nseg)
 {
@@ -521,20 +522,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && sizeof(OT) == 2 ? 3 : 2) voi
             forget(dv);
         }
         float s = sB[p.run][cl + j], R = sQ[p.run][cl + j];
-        float hp[RUN];
+        float hp[RUN], a[RUN], w[RUN];   // h_{t-1}, the gate, what it lets in
 #pragma unroll
         for (int r = 0; r < RUN; ++r) {
-            const float gg = vec_get<T>(gv[r], j), a = __expf(gg);
+            const float gg = vec_get<T>(gv[r], j);
+            a[r] = __expf(gg);
+            w[r] = MIX ? one_minus_exp(gg, a[r]) : 1.f;
             hp[r] = s;
-            s = a * s + added<MIX>(gg, a, vec_get<T>(xv[r], j));
+            s = a[r] * s + w[r] * vec_get<T>(xv[r], j);
         }
 #pragma unroll
         for (int r = RUN - 1; r >= 0; --r) {
-            const float gg = vec_get<T>(gv[r], j), a = __expf(gg), xx = vec_get<T>(xv[r], j);
             const float G = vec_get<T>(dv[r], j) + R;
-            R = a * G;
-            outg[r][j & 1] = R * (MIX ? hp[r] - xx : hp[r]);
-            outx[r][j & 1] = MIX ? one_minus_exp(gg, a) * G : G;
+            R = a[r] * G;
+            outg[r][j & 1] = R * (MIX ? hp[r] - vec_get<T>(xv[r], j) : hp[r]);
+            outx[r][j & 1] = w[r] * G;
         }
         if constexpr (PACK) {
             if (j & 1) {
