@@ -832,12 +832,12 @@ def _arg4(name, t, shape, dtype) -> Tensor:
     """The description of a [B,H,T,d] activation of this shape and type."""
     if not isinstance(t, torch.Tensor):
         _fail(f"{name}: expected a tensor", TypeError)
-    if t.shape != shape or t.dtype is not dtype:
-        _check_act(name, t, torch.Size(shape), dtype)
-    s = t.stride()
-    if s[3] != 1:
-        _check_act(name, t, torch.Size(shape), dtype)
-    return Tensor(t.data_ptr(), s[0], s[1], s[2])
+    if t.shape == shape and t.dtype is dtype:
+        b, h, r, one = t.stride()
+        if one == 1:
+            return Tensor(t.data_ptr(), b, h, r)
+    _check_act(name, t, torch.Size(shape), dtype)
+    return _act(t)
 
 
 def _arg3(name, t, shape, dtype) -> Tensor:
@@ -920,7 +920,7 @@ def _new_rows(like, dtype):
     n = 8 if dtype is torch.bfloat16 else 4
     C = like.shape[2]
     if C % n == 0:
-        return torch.empty(like.shape, dtype=dtype, device=like.device)
+        return torch.empty_like(like, dtype=dtype)
     return torch.empty(*like.shape[:2], -(-C // n) * n, dtype=dtype, device=like.device)[..., :C]
 
 
@@ -1040,8 +1040,10 @@ def step(q, k, v, decay, S, *, beta=None, slots=None, o=None, out_dtype=None):
     if out is None:
         _fail(f"unsupported output dtype {odt}", TypeError)
     oa = None if o is None else _arg4("o", o, (B, H, T, DV), odt)
-    _check_decay(decay, B, H, T)
-    kind, dec = _decay(decay)
+    kind, dec = DECAY_NONE, _NONE
+    if decay is not None:
+        _check_decay(decay, B, H, T)
+        kind, dec = _decay(decay)
     if not isinstance(S, torch.Tensor) or S.dim() != 4:
         _fail("S: must be a float32 [n,H,d_k,d_v] tensor")
     n = S.shape[0]
@@ -1053,7 +1055,7 @@ def step(q, k, v, decay, S, *, beta=None, slots=None, o=None, out_dtype=None):
     dev = _same_device(q, ("k", k), ("v", v), ("decay", decay), ("S", S), ("beta", beta),
                        ("slots", slots), ("o", o))
     if o is None:
-        o = torch.empty((B, H, T, DV), dtype=odt, device=q.device)
+        o = torch.empty_like(v, dtype=odt)
         oa = _arg4("o", o, o.shape, odt)
     rc = _lib().linrec_step(context(dev), ctypes.byref(Desc(B, H, T, DK, DV, CHUNK, code, kind, out)), qa, ka,
                             va, barg, dec, S_ptr, slot_ptr, n, oa, _raw_stream(dev))
