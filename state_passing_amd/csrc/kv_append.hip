@@ -127,7 +127,10 @@ __device__ __forceinline__ void rescale_old(uint8_t* kc, uint8_t* vc, int lo, in
 // rows of bf16 read, two of codes written); rotated keys stay in registers
 // between the maximum and the conversion, values are read as 4 tokens x 8
 // features a thread so that four neighbouring codes of V's row make a word, and
-// turned through LDS.
+// turned through LDS.  With the queries in the same launch, 2 x 4096 tokens of
+// 32 + 8 heads take 50 us (185 MB, 3.7 TB/s; element by element through an LDS
+// tile, in two launches: 283 us); one token of 64 sequences 8.9 us, the time of
+// four dependent loads (length, table, scale, row) and a launch.
 template <int D, int P>
 __device__ __forceinline__ void append_page(const AppendArgs& a, int j, int h, int b)
 {

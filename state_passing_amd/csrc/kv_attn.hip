@@ -321,7 +321,9 @@ __device__ __forceinline__ float* part_stat(const AttnArgs& a, int split, int b,
 // Bound by the cache's bytes (2 D per key).  Four waves take every fourth tile
 // of a split's keys each, straight from global memory to registers (no LDS, no
 // barrier: a fragment is 16 contiguous bytes of K's or V's rows), the next
-// tile's K and its page numbers loaded ahead, and join at the end.
+// tile's K and its page numbers loaded ahead, and join at the end.  32 sequences
+// of 12K-16K tokens, 32 / 8 heads of 128: 167 us, 5.6 TB/s; one sequence of 4096
+// tokens: 6.4-8 us, a chain of dependent loads.
 // PAGED: a tile may span pages (pages of 16 and 32 tokens); else it lies in one,
 // whose number, scales and address are then the wave's, not the lane's.
 template <int D, int NR, bool PAGED>
@@ -499,6 +501,8 @@ __global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kern
 
 // Joins the splits of a row, one wave a row: lane s forms split s's factor, then
 // D / 4 lanes take the sums of every (256 / D)-th split, added in a fixed order.
+// Latency: 4-5 us for few rows, 10 us for 16384 rows of 4 splits (a workgroup
+// a row took 72).
 constexpr int MAX_SPLITS = 64;
 
 template <int D>
@@ -506,18 +510,24 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 {
     constexpr int LPR = D / 4, G = 64 / LPR;
     const int row = blockIdx.x * 4 + wave_id(), h = blockIdx.y, b = blockIdx.z;
+    if (row >= a.rows)
+        return;
+    // the sequence's length, the splits' sums and their first parts are read
+    // together (a row that is not there has a place, and nothing of it is used)
+    const int lane = lane_id(), grp = lane / LPR, f4 = lane % LPR;
+    const float2 stat = *reinterpret_cast<const float2*>(part_stat<D>(a, min(lane, a.nsplit - 1), b, h, row));
+    const float* y = part_row<D>(a, 0, b, h, row) + 4 * f4;
+    const int64_t next = (int64_t)a.B * a.c.H * a.rows * (D + 2);   // from one split to the next
+    constexpr int U = 4;
+    floatx4 first[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        first[u] = *reinterpret_cast<const floatx4*>(y + min(grp + G * u, a.nsplit - 1) * next);
     const Span sp(a.past, a.n_new, b, a.T);
     if (row >= sp.n * a.group)
         return;
-    const int lane = lane_id(), grp = lane / LPR, f4 = lane % LPR;
-    float m = -INFINITY, l = 0.f;
-    if (lane < a.nsplit) {
-        const float* stat = part_stat<D>(a, lane, b, h, row);
-        m = stat[0];
-        l = stat[1];
-    }
-    const float* y = part_row<D>(a, 0, b, h, row) + 4 * f4;
-    const int64_t next = (int64_t)a.B * a.c.H * a.rows * (D + 2);   // from one split to the next
+    const float m = lane < a.nsplit ? stat.x : -INFINITY;
+    float l = lane < a.nsplit ? stat.y : 0.f;
     float top = m;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
@@ -528,8 +538,14 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
     for (int off = 32; off > 0; off >>= 1)
         l += __shfl_xor(l, off, 64);
     floatx4 sum = zero4();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const float w = __shfl(f, min(grp + G * u, a.nsplit - 1), 64);
+        if (grp + G * u < a.nsplit)
+            sum += first[u] * w;
+    }
 #pragma unroll 4
-    for (int s0 = 0; s0 < a.nsplit; s0 += G) {
+    for (int s0 = G * U; s0 < a.nsplit; s0 += G) {
         const int s = s0 + grp, at = min(s, a.nsplit - 1);
         const floatx4 part = *reinterpret_cast<const floatx4*>(y + at * next);
         const float w = __shfl(f, at, 64);
@@ -547,8 +563,11 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 
 // ---- many rows: pieces of a prompt ------------------------------------------
 //
-// Bound by the matrix and vector units (4 D flops a score, and about 8 vector
-// instructions with one exp).  Four waves of 32 rows each share every tile of
+// Bound by the matrix and vector units (4 D flops a score, and about 7 vector
+// instructions with one exp), which two waves a SIMD (226 registers) overlap in
+// part: 4096 tokens behind 12K, 16 / 4 heads of 128, take 503 us (957 TFLOP/s,
+// matrix unit busy 40% of the cycles, vector unit 48%; a library's large product reaches
+// 1210).  Four waves of 32 rows each share every tile of
 // 64 keys: the codes are converted once, on the way into LDS ([key][feature]
 // and, for V, [feature][key]), two buffers deep, while the loads of the next
 // tile are in flight.
@@ -768,8 +787,10 @@ Plan plan_of(const linrec_kv_cache* c, int B, int T, int Hq)
     p.row_tiles = (p.rows + tile_rows - 1) / tile_rows;
     const int64_t blocks = (int64_t)B * c->H * p.row_tiles;
     const int64_t key_tiles = ((int64_t)c->max_pages * c->page + 63) / 64;
-    // splits fill the 256 CUs; each gets at least one tile a wave (token kernel)
-    // or 8 tiles (piece kernel)
+    // Splits fill the 256 CUs with one round of workgroups (two a CU); each gets
+    // at least one tile a wave (token kernel) or 8 tiles (piece kernel).  Rounds of
+    // 512, 768, 1024, 2048, 4096 workgroups: 180, 194, 180, 182, 194 us at 32
+    // sequences of 16K, 15.6, 19.2, 20.8, 23.1, 23.1 at 16 windows of 2048.
     const int64_t want = (512 + blocks - 1) / blocks;
     const int64_t most = std::max<int64_t>(1, key_tiles / (p.token ? 4 : 8));
     p.nsplit = (int)std::min<int64_t>(std::min(want, most), MAX_SPLITS);
