@@ -36,8 +36,8 @@ __global__ __launch_bounds__(256) void step_kernel(Act<const T> q, Act<const T> 
         for (int i = threadIdx.x; i < b; i += 256)
             skip |= slots[i] == slot;
         if (__syncthreads_or(skip)) {
-            for (int i = threadIdx.x; i < T_ * DVT; i += 256)
-                o.head(b, h)[(int64_t)(i / DVT) * o.st + blockIdx.x * DVT + i % DVT] = (OT)0.f;
+            for (int64_t i = threadIdx.x; i < (int64_t)T_ * DVT; i += 256)
+                o.head(b, h)[i / DVT * o.st + blockIdx.x * DVT + i % DVT] = (OT)0.f;
             return;
         }
     }

@@ -143,3 +143,16 @@ def test_replay_advances_the_state():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(S1, S2) and torch.equal(o1, o2)
+
+
+def test_skipped_sequence_of_very_many_tokens():
+    """2^25 + 1 tokens of 64 columns: 2^31 + 64 outputs, every one of them zeroed."""
+    T = 2 ** 25 + 1
+    x = torch.ones(1, 1, T, 64, dtype=BF, device=DEV)
+    o = torch.full_like(x, 5.0)
+    S = torch.ones(2, 1, 64, 64, device=DEV)
+    linrec.step(x, x, x, None, S, slots=torch.tensor([-1], dtype=torch.int32, device=DEV), o=o)
+    torch.cuda.synchronize()
+    # (in parts: a reduction over the whole would count in 64 bits anyway, but holds a copy)
+    assert not any(bool(p.any()) for p in o.view(-1).split(2 ** 28))
+    assert (S == 1).all()
