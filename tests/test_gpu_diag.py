@@ -250,3 +250,25 @@ def test_replays_and_streams(T):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(h, h3) and torch.equal(e, e3) and all(torch.equal(a, b) for a, b in zip(back, back3))
+
+
+def test_two_calls_at_once():
+    """Calls of many segments on two streams, each with its own workspace, in flight
+    together: every result equals that of the call made alone, bit for bit."""
+    sets = [[t.to(DEV) for t in draw(20 + i, 2, 5000 - 700 * i, 1024, BF)] for i in range(2)]
+
+    def both(s):
+        g, x, h_in, dh, dh_out = s
+        h, e, st = linrec.diag_fwd(g, x, h_in, form="mix")
+        return (h, e, *linrec.diag_bwd(g, x, st, dh, dh_out, form="mix"))
+
+    want = [both(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(4):
+        got = []
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                got.append(both(s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
