@@ -560,6 +560,10 @@ typedef struct {
     int32_t H, D;             /* key/value heads, head width */
 } linrec_kv_cache;
 
+/* Bytes of workspace linrec_kv_append needs (0 if the arguments are invalid or
+ * none is needed, as in calls of a few pages: then workspace may be NULL). */
+size_t linrec_kv_append_workspace_bytes(const linrec_kv_cache* cache, int32_t B, int32_t T);
+
 /* Append k, v [B,H,T,D] at positions past[b] + t, rotating keys (and, when q is
  * given, queries q [B,Hq,T,D] into q_out) by their position on the way:
  *   features (i, i + rot/2) of a head (interleaved: (2i, 2i+1)), i < rot/2,
@@ -575,12 +579,14 @@ typedef struct {
  * A page named more than once among the pages that the call writes is written
  * for the first (lowest b, then lowest token) alone.  Tokens at or past
  * max_pages * page are dropped.  (T / page + 2) * H + T must be below 2^24.
- *   q.ptr == NULL: no queries (Hq, q_out ignored).  q_out may be q. */
+ *   q.ptr == NULL: no queries (Hq, q_out ignored).  q_out may be q.
+ *   workspace: linrec_kv_append_workspace_bytes(), contents without meaning
+ *   before and after. */
 linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache* cache, int32_t B, int32_t T,
                                linrec_tensor k, linrec_tensor v, const int32_t* past,
                                const int32_t* n_new, const double* inv_freq, int32_t rot,
                                int32_t interleaved, int32_t Hq, linrec_tensor q,
-                               linrec_tensor q_out, void* stream);
+                               linrec_tensor q_out, void* workspace, void* stream);
 
 /* Bytes of workspace linrec_kv_attn needs (0 if the arguments are invalid or
  * none is needed: then workspace may be NULL). */

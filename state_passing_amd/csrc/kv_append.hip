@@ -2,6 +2,8 @@
 // rotation by position applied on the way (linrec_kv_append).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "kv.hpp"
 
 namespace linrec {
@@ -14,6 +16,7 @@ struct AppendArgs {
     const int* past;
     const int* n_new;
     const double* freq;
+    const unsigned long long* owner;   // by page: the first touched block that has it; NULL: each block looks itself
     int B, T, Hq, half, nblk;   // half: rotated pairs; nblk: pages a sequence may touch
     int qshift;                 // queries: 1 << qshift tokens a workgroup
     bool inter;
@@ -123,6 +126,36 @@ __device__ __forceinline__ void rescale_old(uint8_t* kc, uint8_t* vc, int lo, in
     }
 }
 
+// The page of the call's touched block e = b * nblk + j, -1 if there is none.
+__device__ __forceinline__ int touched_page(const AppendArgs& a, int64_t e)
+{
+    const int b = (int)(e / a.nblk), j = (int)(e % a.nblk);
+    const Span sp(a.past, a.n_new, b, a.T);
+    const int first = sp.past >> a.c.shift;
+    if (sp.n <= 0 || j > ((sp.past + sp.n - 1) >> a.c.shift) - first)
+        return -1;
+    return page_of(a.c, b, first + j);
+}
+
+// A page belongs to the first of the call's touched blocks that names it.  Every
+// page and head may look through the blocks before its own, which takes no memory
+// and no launch but time in the square of their number; or two small kernels
+// write each page's owner down first: MARK = false empties the entries that the
+// call uses, MARK = true takes the minimum.
+template <bool MARK>
+__global__ __launch_bounds__(256) void kv_owner_kernel(AppendArgs a, unsigned long long* owner)
+{
+    for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < (int64_t)a.B * a.nblk; e += gridDim.x * 256ll) {
+        const int page = touched_page(a, e);
+        if (page < 0)
+            continue;
+        if constexpr (MARK)
+            atomicMin(owner + page, (unsigned long long)e);
+        else
+            owner[page] = ~0ull;
+    }
+}
+
 // Keys and values of one page and head.  Bound by the bytes (6 D a token: two
 // rows of bf16 read, two of codes written); rotated keys stay in registers
 // between the maximum and the conversion, values are read as 4 tokens x 8
@@ -177,13 +210,11 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int j, int h, i
     // an earlier touched block with the same page owns it
     int dup = 0;
     const int64_t before = (int64_t)b * a.nblk + j;
-    for (int64_t e = tid; e < before; e += 256) {
-        const int eb = (int)(e / a.nblk), ej = (int)(e % a.nblk);
-        const Span es(a.past, a.n_new, eb, a.T);
-        const int first = es.past >> a.c.shift;
-        if (es.n > 0 && ej <= ((es.past + es.n - 1) >> a.c.shift) - first)
-            dup |= page_of(a.c, eb, first + ej) == page;
-    }
+    if (a.owner)
+        dup = a.owner[page] != (unsigned long long)before;
+    else
+        for (int64_t e = tid; e < before; e += 256)
+            dup |= touched_page(a, e) == page;
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
         const int t = kr + KR * i;
@@ -332,6 +363,14 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
+int blocks_of(const linrec_kv_cache* c, int32_t T) { return (int)(((int64_t)T + c->page - 2) / c->page + 1); }
+
+// From this many touched blocks on their owners are written down.  Looking against
+// writing down, 8 heads of 128: 19.6 / 22.0 us at 512 sequences of one token, 38.1 /
+// 35.5 at 1024, 216 / 113 at 4096; 92.8 / 68.3 at 32768 tokens in pages of 16 (2049
+// blocks), 7450 / 1200 at 64 x 8192, 1270 / 677 in pages of 64.
+constexpr int64_t OWNERS_FROM = 1024;
+
 Act<const bf16> cact(const linrec_tensor& t) { return Act<const bf16>{(const bf16*)t.ptr, t.sb, t.sh, t.st}; }
 
 }  // namespace
@@ -339,11 +378,18 @@ Act<const bf16> cact(const linrec_tensor& t) { return Act<const bf16>{(const bf1
 
 using namespace linrec;
 
+extern "C" size_t linrec_kv_append_workspace_bytes(const linrec_kv_cache* cache, int32_t B, int32_t T)
+{
+    if (check_kv(cache, B, T) != LINREC_OK || T == 0 || (int64_t)B * blocks_of(cache, T) < OWNERS_FROM)
+        return 0;
+    return (size_t)cache->pages * sizeof(unsigned long long);
+}
+
 extern "C" linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache* cache, int32_t B, int32_t T,
                                           linrec_tensor k, linrec_tensor v, const int32_t* past,
                                           const int32_t* n_new, const double* inv_freq, int32_t rot,
                                           int32_t interleaved, int32_t Hq, linrec_tensor q,
-                                          linrec_tensor q_out, void* stream)
+                                          linrec_tensor q_out, void* workspace, void* stream)
 {
     linrec_status st;
     if ((st = check_kv(cache, B, T)) != LINREC_OK)
@@ -365,6 +411,8 @@ extern "C" linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache
             return LINREC_E_NULL;
         if (!aligned(inv_freq, 8))
             return LINREC_E_ALIGN;
+        if (linrec_kv_append_workspace_bytes(cache, B, T) && (st = check_buffer(workspace)) != LINREC_OK)
+            return st;
     }
     if ((st = check_ctx(ctx)) != LINREC_OK)
         return st;
@@ -383,12 +431,19 @@ extern "C" linrec_status linrec_kv_append(linrec_ctx* ctx, const linrec_kv_cache
     a.T = T;
     a.Hq = Hq;
     a.half = rot / 2;
-    a.nblk = (int)(((int64_t)T + cache->page - 2) / cache->page + 1);
+    a.nblk = blocks_of(cache, T);
     a.inter = interleaved != 0;
     while (a.qshift < 4 && 1 << a.qshift < T)
         ++a.qshift;
     hipStream_t s = (hipStream_t)stream;
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_KV_APPEND, s, [&] {
+        if (linrec_kv_append_workspace_bytes(cache, B, T)) {
+            unsigned long long* owner = (unsigned long long*)workspace;
+            const dim3 grid((unsigned)std::min<int64_t>(((int64_t)B * a.nblk + 255) / 256, 2048));
+            launch_kernel(kv_owner_kernel<false>, grid, dim3(256), s, a, owner);
+            launch_kernel(kv_owner_kernel<true>, grid, dim3(256), s, a, owner);
+            a.owner = owner;
+        }
         return cache->D == 128 ? launch_append<128>(a, s) : launch_append<64>(a, s);
     }));
     return LINREC_OK;

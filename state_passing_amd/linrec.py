@@ -50,7 +50,8 @@ EXPORTS = (
     "linrec_delta_fwd_seq_workspace_bytes", "linrec_delta_bwd_seq_workspace_bytes",
     "linrec_delta_fwd_seq", "linrec_delta_bwd_seq",
     "linrec_diag_states_bytes", "linrec_diag_workspace_bytes", "linrec_diag_fwd", "linrec_diag_bwd",
-    "linrec_step", "linrec_kv_append", "linrec_kv_attn_workspace_bytes", "linrec_kv_attn",
+    "linrec_step", "linrec_kv_append_workspace_bytes", "linrec_kv_append",
+    "linrec_kv_attn_workspace_bytes", "linrec_kv_attn",
 )
 
 KERNEL_KINDS = {0: "fwd_sum", 1: "fwd_fold", 2: "fwd_seg", 3: "bwd_sum", 4: "bwd_fold",
@@ -138,7 +139,8 @@ def _lib():
         "linrec_diag_fwd": ([P, DD, T, T, P, T, P, P, P, P], ctypes.c_int),
         "linrec_diag_bwd": ([P, DD, T, T, P, T, P, T, T, P, P, P], ctypes.c_int),
         "linrec_step": ([P, D, T, T, T, T, T, P, P, I32, T, P], ctypes.c_int),
-        "linrec_kv_append": ([P, KC, I32, I32, T, T, P, P, P, I32, I32, I32, T, T, P], ctypes.c_int),
+        "linrec_kv_append_workspace_bytes": ([KC, I32, I32], ctypes.c_size_t),
+        "linrec_kv_append": ([P, KC, I32, I32, T, T, P, P, P, I32, I32, I32, T, T, P, P], ctypes.c_int),
         "linrec_kv_attn_workspace_bytes": ([KC, I32, I32, I32], ctypes.c_size_t),
         "linrec_kv_attn": ([P, KC, I32, I32, I32, T, P, P, ctypes.c_float, I32, T, P, P, P],
                            ctypes.c_int),
@@ -1119,7 +1121,7 @@ def _kv_desc(cache: KvCache, B: int) -> KvCacheDesc:
 
 
 def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interleaved=False, q=None,
-              q_out=None):
+              q_out=None, workspace=None):
     """Append k, v [B,H,T,D] (bf16) behind past[b] (int32 [B]) tokens of every
     sequence's cache, the first n_new[b] of the T, with the rotation of
     inv_freq (fp64 [rot/2]) applied to the keys and to q [B,Hq,T,D]
@@ -1149,13 +1151,18 @@ def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interlea
             oa = _arg4("q_out", q_out, (B, Hq, T, c.D), bf)
     elif q_out is not None:
         _fail("q_out: there is no q")
+    need = _lib().linrec_kv_append_workspace_bytes(ctypes.byref(c), B, T)
+    if workspace is not None:
+        _check_buffer("workspace", workspace, need)
     dev = _same_device(k, ("v", v), ("past", past), ("n_new", n_new), ("inv_freq", inv_freq), ("q", q),
-                       ("q_out", q_out), *zip(KvCache._fields, cache))
+                       ("q_out", q_out), ("workspace", workspace), *zip(KvCache._fields, cache))
     if q is not None and q_out is None:
         q_out = (torch.zeros if n_new is not None else torch.empty)((B, Hq, T, c.D), dtype=bf, device=q.device)
         oa = _arg4("q_out", q_out, q_out.shape, bf)
+    if workspace is None and need:
+        workspace = _bytes(need, k)
     rc = _lib().linrec_kv_append(context(dev), ctypes.byref(c), B, T, ka, va, past_ptr, n_ptr, freq_ptr, rot,
-                                 1 if interleaved else 0, Hq, qa, oa, _raw_stream(dev))
+                                 1 if interleaved else 0, Hq, qa, oa, _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_kv_append")
     return q_out
 

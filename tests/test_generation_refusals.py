@@ -160,9 +160,9 @@ def kact(H=2, T=3, D=128, **kw):
     return linrec.Tensor(*base.values())
 
 
-def append(c=None, B=2, T=3, k=None, v=None, past=FAKE, n=None, freq=FAKE, rot=128, Hq=4, q=None, q_out=None):
+def append(c=None, B=2, T=3, k=None, v=None, past=FAKE, n=None, freq=FAKE, rot=128, Hq=4, q=None, q_out=None, work=None):
     return linrec._lib().linrec_kv_append(None, ctypes.byref(c or cache()), B, T, k or kact(), v or kact(), past, n, freq, rot, 0, Hq,
-                                          q or kact(4), q_out or kact(4), None)
+                                          q or kact(4), q_out or kact(4), work, None)
 
 
 def attn(c=None, B=2, T=3, Hq=4, q=None, past=FAKE, n=None, scale=0.1, window=0, o=None, lse=None, work=FAKE):
@@ -185,6 +185,7 @@ CACHE = [
     (dict(freq=None), "LINREC_E_NULL"), (dict(freq=FAKE + 4), "LINREC_E_ALIGN"), (dict(Hq=0), "LINREC_E_SHAPE"),
     (dict(k=kact(ptr=None)), "LINREC_E_NULL"), (dict(v=kact(st=64)), "LINREC_E_LAYOUT"), (dict(q_out=kact(4, sh=0)), "LINREC_E_LAYOUT"),
     (dict(q_out=kact(4, ptr=None)), "LINREC_E_NULL"), (dict(k=kact(ptr=FAKE + 2)), "LINREC_E_ALIGN"), (dict(T=1 << 24), "LINREC_E_SHAPE"),
+    (dict(B=1024, T=1), "LINREC_E_WORKSPACE"), (dict(B=1024, T=1, work=FAKE + 8), "LINREC_E_WORKSPACE"),
 ])
 def test_append_statuses(kw, name):
     status(append(**kw), name)
@@ -198,6 +199,15 @@ def test_append_statuses(kw, name):
 ])
 def test_attn_statuses(kw, name):
     status(attn(**kw), name)
+
+
+def test_append_workspace_sizes():
+    size = lambda c, B, T: linrec._lib().linrec_kv_append_workspace_bytes(ctypes.byref(c), B, T)  # noqa: E731
+    for B in (1, 64, 1023):
+        assert size(cache(), B, 1) == 0
+    assert size(cache(), 1024, 1) == 8 * cache().pages      # an owner of every page
+    assert size(cache(page=16), 1, 32768) == 8 * cache().pages and size(cache(page=128), 1, 32768) == 0
+    assert size(cache(), 2048, 0) == 0 and size(cache(D=32), 2048, 1) == 0 and size(cache(page=100), 2048, 1) == 0
 
 
 def test_attn_workspace_sizes():

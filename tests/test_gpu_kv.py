@@ -370,6 +370,39 @@ def test_append_pages_missing_or_named_twice():
     check_append(cache, mk(), mk(), [3, 0, 5], [40, 40, 40], freqs(32), False)
 
 
+@pytest.mark.parametrize("B,T,page,past", [(70, 500, 16, 9), (2100, 1, 16, 30)])
+def test_append_of_very_many_pages(B, T, page, past):
+    """Enough pages that their owners are written down first: the same rules for pages
+    that are missing or named twice; and every replay of a captured call, its
+    workspace full of other bytes, equals the eager one."""
+    g = torch.Generator().manual_seed(36)
+    cache = filled_cache(g, B, 1, 64, page, (past + T) // page + 2)
+    first, last = past // page, (past + T - 1) // page
+    cache.table[1, first] = -1
+    cache.table[B - 1, first] = cache.table[0, last]
+    cache.table[B // 2, last] = cache.table[2, last]
+    cache.table[3, last] = cache.table[4, first]
+    cache.table[5, last] = cache.k.shape[0]
+    mk = lambda: torch.randn(B, 1, T, 64, generator=g).to(torch.bfloat16)  # noqa: E731
+    k, v = mk(), mk()
+    n = [T if b % 7 else T // 2 for b in range(B)]
+    one = check_append(cache, k, v, [past] * B, n, None, False)
+    two, nd, pd = to_dev(cache), torch.tensor(n, dtype=torch.int32, device=DEV), torch.full((B,), past, dtype=torch.int32, device=DEV)
+    kd, vd = k.to(DEV), v.to(DEV)
+    work = torch.empty(8 * cache.k.shape[0], dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        linrec.kv_append(two, kd, vd, pd, n_new=nd, workspace=work)
+    for fill in (0, 255, 7):
+        for t, c in zip(two, cache):
+            t.view(torch.uint8).copy_(c.view(torch.uint8))
+        work.fill_(fill)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(one, two):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_append_in_place_queries_and_replays():
     """q_out = q; and a captured append repeats what an eager one leaves."""
     g = torch.Generator().manual_seed(35)
