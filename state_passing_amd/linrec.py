@@ -1151,7 +1151,8 @@ def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interlea
             oa = _arg4("q_out", q_out, (B, Hq, T, c.D), bf)
     elif q_out is not None:
         _fail("q_out: there is no q")
-    need = _lib().linrec_kv_append_workspace_bytes(ctypes.byref(c), B, T)
+    # a call of fewer than 1024 tokens, so of fewer pages, needs none
+    need = _lib().linrec_kv_append_workspace_bytes(ctypes.byref(c), B, T) if B * T >= 1024 else 0
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
     dev = _same_device(k, ("v", v), ("past", past), ("n_new", n_new), ("inv_freq", inv_freq), ("q", q),

@@ -206,6 +206,8 @@ def test_append_workspace_sizes():
     for B in (1, 64, 1023):
         assert size(cache(), B, 1) == 0
     assert size(cache(), 1024, 1) == 8 * cache().pages      # an owner of every page
+    # (the binding does not ask below 1024 tokens)
+    assert not any(size(cache(page=p), B, T) for p in (16, 128) for B, T in ((1, 1023), (511, 2), (341, 3), (2, 511)))
     assert size(cache(page=16), 1, 32768) == 8 * cache().pages and size(cache(page=128), 1, 32768) == 0
     assert size(cache(), 2048, 0) == 0 and size(cache(D=32), 2048, 1) == 0 and size(cache(page=100), 2048, 1) == 0
 
