@@ -98,10 +98,14 @@ __device__ __forceinline__ float quad_sum(float x)
 template <int D>
 __device__ __forceinline__ void softmax_tile(RowState<D>& st, floatx4 (&x)[4], Frag<bf16> (&p)[2], float c2)
 {
-    float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
+    // (of a NaN this maximum is NaN, which moves nothing: the row ends as NaN whatever
+    // st.m is.  One that passed NaN by would take 20 instructions for 8.)
+    float mx = __builtin_elementwise_maximum(x[0][0], x[0][1]);
 #pragma unroll
-    for (int i = 1; i < 4; ++i)
-        mx = fmaxf(mx, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = i ? 0 : 2; r < 4; r += 2)
+            mx = __builtin_elementwise_maximum(__builtin_elementwise_maximum(mx, x[i][r]), x[i][r + 1]);
     // st.m only has to keep the exponents in range, so it is moved (for all 4
     // lanes of a row together) when a score passes it by 2^8, not at every new
     // maximum: most tiles then need neither the exchange nor the rescaling
@@ -563,14 +567,15 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 
 // ---- many rows: pieces of a prompt ------------------------------------------
 //
-// Bound by the matrix and vector units (4 D flops a score, and about 7 vector
-// instructions with one exp), which two waves a SIMD (226 registers) overlap in
-// part: 4096 tokens behind 12K, 16 / 4 heads of 128, take 503 us (957 TFLOP/s,
-// matrix unit busy 40% of the cycles, vector unit 48%; a library's large product reaches
-// 1210).  Four waves of 32 rows each share every tile of
-// 64 keys: the codes are converted once, on the way into LDS ([key][feature]
+// Bound by the matrix and vector units (4 D flops a score, and about 6 vector
+// instructions with one exp), which two waves a SIMD (237 registers) overlap in
+// part: 4096 tokens behind 12K, 16 / 4 heads of 128, take 475 us (1010 TFLOP/s; a
+// library's large product reaches 1210).  Four waves of 32 rows each share every
+// tile of 64 keys: the codes are converted once, on the way into LDS ([key][feature]
 // and, for V, [feature][key]), two buffers deep, while the loads of the next
-// tile are in flight.
+// tile are in flight.  64 rows a wave halve the LDS reads but leave one wave a SIMD:
+// 939 us; eight waves in two halves, one multiplying while the other forms weights:
+// 470, and 230 for 203 us where a head has 68 rows; LDS without bank conflicts: 472.
 template <int D, bool PAGED>
 __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
 {
@@ -611,7 +616,11 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
     // staging: K vector v is key kk, features kf; V vector v is feature row vf, keys 16 (tid % 4)
     constexpr int KL = D / 16;               // lanes per key row
     const int kk = tid / KL, kf = 16 * (tid % KL), vf = tid / 4, vg = 16 * (tid % 4);
-    int pk[KV], pv;
+    // One page a tile: its number and scales are the wave's, but come through vector
+    // loads, each used a tile after it is asked for.  A scalar load in flight would
+    // make every wait for an LDS read a wait for memory (489 -> 475 us).
+    int pk[KV], pv = -1, entry = -1;
+    bool entry_in = false;
     auto pages = [&](int tl) {
         const int k = rg.k0 + 64 * tl;
         const bool in = tl < rg.last;
@@ -621,7 +630,10 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
                 pk[v] = in ? page_of(a.c, b, (k + kk + 256 / KL * v) >> shift) : -1;
             pv = in ? page_of(a.c, b, (k + vg) >> shift) : -1;
         } else {
-            pv = in ? __builtin_amdgcn_readfirstlane(page_of(a.c, b, k >> shift)) : -1;
+            int64_t at = b * a.c.table_stride + min(k >> shift, a.c.max_pages - 1);
+            asm("" : "+v"(at));
+            entry = a.c.table[at];
+            entry_in = in && k >> shift < a.c.max_pages;
         }
     };
     const int k_lane = kk * D + kf, v_lane = vf * P + vg;
@@ -630,6 +642,10 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
     bool v_ok;
     auto load = [&](int tl) {
         const int k = rg.k0 + 64 * tl;
+        if constexpr (!PAGED) {
+            const int e = __builtin_amdgcn_readfirstlane(entry);
+            pv = entry_in && e >= 0 && e < a.c.pages ? e : -1;
+        }
         const int64_t ph = (int64_t)max(pv, 0) * H + h;
         if constexpr (PAGED) {
 #pragma unroll
@@ -639,10 +655,14 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
                 ks[v] = a.c.ks[kh];
                 vr[v] = *reinterpret_cast<const u32x4*>(a.c.v + (ph * D + vf + 64 * v) * P + ((k + vg) & (P - 1)));
             }
+            vs = a.c.vs[ph];
         } else {
             const uint8_t* kp = a.c.k + (ph * P + (k & (P - 1))) * D;
             const uint8_t* vp = a.c.v + (ph * D * P + (k & (P - 1)));
-            ks[0] = a.c.ks[ph];
+            int none = 0;
+            asm("" : "+v"(none));
+            ks[0] = a.c.ks[ph + none];
+            vs = a.c.vs[ph + none];
 #pragma unroll
             for (int v = 0; v < KV; ++v) {
                 kr[v] = *reinterpret_cast<const u32x4*>(kp + k_lane + 256 / KL * v * D);
@@ -650,7 +670,6 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
                 ks[v] = ks[0];
             }
         }
-        vs = a.c.vs[ph];
         v_ok = pv >= 0;
     };
     // whether rows [ra, rb) all see the whole tile from key k0 on
