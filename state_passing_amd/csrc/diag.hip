@@ -17,7 +17,7 @@
 //
 // Bound by HBM: 3 elements a token and channel forward, 5 backward.  65536 x 2048
 // bf16: 166 us forward (4.9 TB/s), 254 us backward (5.3 TB/s); 2 x 4096 x 1024
-// fp32 forward 21 us (4.8 TB/s); a copy reaches 4.85.  A ragged 3 x 4099 x 1000
+// fp32 forward 20 us (4.9 TB/s); a copy reaches 4.85.  A ragged 3 x 4099 x 1000
 // in the mix form, about one round of workgroups, takes 28 and 47 us (2.6 TB/s):
 // its loads, exponentials and stores follow each other.
 #include <hip/hip_runtime.h>
