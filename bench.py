@@ -28,7 +28,9 @@ decay gradient.
 Flags: --gpus N (only 1 is supported: one GPU), --steps K, --warmup W,
 --no-cpu-baseline, --copy-probe BYTES (run only a device copy of that size,
 for calibrating rocprofv3 byte counters), --profile (run only the
-serialized pass, so a profiler sees undisturbed dispatches).
+serialized pass, so a profiler sees undisturbed dispatches), --profile-delta
+and --profile-generation [NAME] (likewise the delta rule's drivers; the calls of
+the elementwise recurrence and the generation operators whose names hold NAME).
 """
 from __future__ import annotations
 
@@ -104,6 +106,8 @@ def parse():
     p.add_argument("--profile", action="store_true")
     p.add_argument("--profile-delta", action="store_true",
                    help="run one forward and one backward of the delta-rule workload's sequence drivers only")
+    p.add_argument("--profile-generation", nargs="?", const="", default=None, metavar="NAME",
+                   help="run the elementwise recurrence's and the generation operators' workloads only")
     return p.parse_args()
 
 
@@ -286,6 +290,88 @@ def delta_bench(linrec, dev, args):
             "per_piece_calls": {"fwd_ms": ms_fwd_pp, "bwd_ms": ms_bwd_pp}}
 
 
+def generation_calls(linrec, dev):
+    """(name, function that makes three sets of inputs' calls) of the elementwise
+    recurrence and the generation operators."""
+    import torch
+    bf, f32 = torch.bfloat16, torch.float32
+    gen = torch.Generator(device=dev).manual_seed(0)
+    rand = lambda *s, dtype=bf: torch.randn(*s, device=dev, generator=gen).to(dtype)  # noqa: E731
+    unit = lambda *s: torch.nn.functional.normalize(rand(*s, dtype=f32), dim=-1).to(bf)  # noqa: E731
+
+    def diag(B, T, C, dtype, form, train):
+        g, x, dh = -rand(B, T, C, dtype=f32).abs().mul_(0.1).to(dtype), rand(B, T, C, dtype=dtype), rand(B, T, C, dtype=dtype)
+        h_in, dh_out = rand(B, C, dtype=f32), rand(B, C, dtype=f32)
+
+        def call():
+            states = linrec.diag_fwd(g, x, h_in, form=form)[2]
+            if train:
+                linrec.diag_bwd(g, x, states, dh, dh_out, form=form)
+        return call
+
+    def step(B, H, d, delta):
+        q, k, v, S = unit(B, H, 1, d), unit(B, H, 1, d), rand(B, H, 1, d), rand(B, H, d, d, dtype=f32)
+        decay = torch.rand(B, H, 1, device=dev, generator=gen).mul_(0.1).add_(0.9)
+        beta = torch.rand(B, H, 1, device=dev, generator=gen) if delta else None
+        slots = torch.randperm(B, device=dev, generator=gen).to(torch.int32) if delta else None
+        return lambda: linrec.step(q, k, v, decay, S, beta=beta, slots=slots)
+
+    def cache(B, T, past, H, page, D):
+        n = (past + T + page - 1) // page
+        table = torch.randperm(B * n, device=dev, generator=gen).to(torch.int32).view(B, n)
+        c = linrec.kv_cache(B * n, H, page, D, table)
+        for t in (c.k, c.v):
+            t.copy_((rand(*t.shape) * 30).to(t.dtype))
+        c.k_scale.fill_(2.0 ** -5)
+        c.v_scale.fill_(2.0 ** -5)
+        return c
+
+    def append(B, T, Hq, H, D, page, past):
+        c, k, v, q = cache(B, T, past, H, page, D), rand(B, H, T, D), rand(B, H, T, D), rand(B, Hq, T, D)
+        at = torch.full((B,), past, dtype=torch.int32, device=dev)
+        freq = 1e4 ** (-torch.arange(D // 2, dtype=torch.float64, device=dev) * 2 / D)
+        return lambda: linrec.kv_append(c, k, v, at, inv_freq=freq, q=q)
+
+    def attn(B, T, Hq, H, D, page, past, window=0, spread=0):
+        c, q = cache(B, T, past, H, page, D), rand(B, Hq, T, D)
+        at = past - torch.arange(B, device=dev, dtype=torch.int32) * spread // max(B - 1, 1)
+        return lambda: linrec.kv_attn(c, q, at, window=window)
+
+    cases = [
+        ("recurrence, 1 token, 64 x 2048, bf16 mix", diag, (64, 1, 2048, bf, "mix", False)),
+        ("recurrence, 2 x 4096 x 1024 fp32, forward", diag, (2, 4096, 1024, f32, "plain", False)),
+        ("recurrence, 3 x 4099 x 1000 bf16 mix, forward + backward", diag, (3, 4099, 1000, bf, "mix", True)),
+        ("recurrence, 65536 x 2048 bf16, forward + backward", diag, (1, 65536, 2048, bf, "plain", True)),
+        ("step, linear, 4 x 16 heads, d = 128", step, (4, 16, 128, False)),
+        ("step, delta rule, 96 x 32 heads by slots, d = 128", step, (96, 32, 128, True)),
+        ("append, 1 token, 64 sequences, 32 + 8 heads", append, (64, 1, 32, 8, 128, 64, 1500)),
+        ("append, 2 x 4096 tokens, 32 + 8 heads", append, (2, 4096, 32, 8, 128, 64, 4000)),
+        ("attention, 1 token, 1 sequence of 4096, 16 / 4 heads", attn, (1, 1, 16, 4, 128, 64, 4095)),
+        ("attention, 1 token, 32 sequences of 12K to 16K, 32 / 8 heads", attn, (32, 1, 32, 8, 128, 64, 16384, 0, 4096)),
+        ("attention, 5 tokens, 16 sequences, window 2048, d = 64, pages of 16", attn, (16, 5, 16, 2, 64, 16, 6001, 2048)),
+        ("attention, 4096 tokens behind 12K, 16 / 4 heads", attn, (1, 4096, 16, 4, 128, 64, 12288)),
+    ]
+    for name, make, args in cases:
+        yield name, lambda make=make, args=args: [make(*args) for _ in range(3)]
+
+
+def profile_generation(linrec, dev, only):
+    """12 calls of each workload, over three sets of inputs in turn, for a profiler."""
+    import torch
+    done = []
+    for name, make in generation_calls(linrec, dev):
+        if only not in name:
+            continue
+        calls = make()
+        for i in range(12):
+            calls[i % 3]()
+        torch.cuda.synchronize()
+        done.append(name)
+        del calls
+        torch.cuda.empty_cache()
+    return {"profile": "generation operators", "workloads": done, "calls": 12}
+
+
 def main():
     args = parse()
     if args.gpus != 1:
@@ -296,6 +382,12 @@ def main():
     if args.copy_probe:
         print(json.dumps({"copy_probe_bytes": args.copy_probe,
                           "read_plus_write_GBs": copy_probe(args.copy_probe)}))
+        return
+    if args.profile_generation is not None:
+        from state_passing_amd import linrec
+        dev = torch.device("cuda:0")
+        torch.cuda.set_device(dev)
+        print(json.dumps(profile_generation(linrec, dev, args.profile_generation)))
         return
     if args.profile_delta:
         from state_passing_amd import linrec
