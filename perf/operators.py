@@ -211,7 +211,7 @@ def _diag(s):
     h = _scan(a, b)
     out = [h.to(dt), h[:, -1].clone()]
     if s["train"]:
-        up = s["dh"].float()
+        up = s["dh"].to(torch.float32, copy=True)   # (float() of a float32 tensor is the tensor itself)
         up[:, -1] += s["dh_out"]
         nxt = torch.cat([a[:, 1:], torch.zeros_like(a[:, :1])], 1)
         G = _scan(nxt.flip(1), up.flip(1)).flip(1)
