@@ -1172,9 +1172,9 @@ def kv_attn(cache: KvCache, q, past, *, n_new=None, scale=None, window=0, o=None
             workspace=None):
     """Attention of q [B,Hq,T,D] (bf16) over the cache, which already holds
     these T tokens behind past[b] earlier ones (linrec_kv_attn).  scale:
-    1/sqrt(D) by default; window > 0: the last `window` tokens only.  lse: fp32
-    [B,Hq,T] to be filled, or None.  Returns o; rows that n_new excludes are
-    left as they were (zeros in a new o)."""
+    1/sqrt(D) by default; window: the last `window` tokens only (<= 0 or >=
+    MAX_T: all).  lse: fp32 [B,Hq,T] to be filled, or None.  Returns o; rows
+    that n_new excludes are left as they were (zeros in a new o)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         _fail("q: must be a [B,Hq,T,D] tensor")
     B, Hq, T, _ = q.shape
@@ -1188,6 +1188,9 @@ def kv_attn(cache: KvCache, q, past, *, n_new=None, scale=None, window=0, o=None
     lse_ptr = _state_ptr("lse", lse, (B, Hq, T))
     if c.H < 1 or Hq % c.H:
         _fail(f"q: {Hq} heads are no multiple of the cache's {c.H}")
+    window = int(window)
+    if not 0 < window < MAX_T:
+        window = 0   # no lower bound; the C argument has 32 bits
     need = _lib().linrec_kv_attn_workspace_bytes(ctypes.byref(c), B, T, Hq)
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
@@ -1199,7 +1202,7 @@ def kv_attn(cache: KvCache, q, past, *, n_new=None, scale=None, window=0, o=None
     if workspace is None and need:
         workspace = _bytes(need, q)
     rc = _lib().linrec_kv_attn(context(dev), ctypes.byref(c), B, T, Hq, qa, past_ptr, n_ptr,
-                               c.D ** -0.5 if scale is None else float(scale), int(window), oa, lse_ptr,
+                               c.D ** -0.5 if scale is None else float(scale), window, oa, lse_ptr,
                                _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_kv_attn")
     return o
