@@ -1126,7 +1126,8 @@ def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interlea
     sequence's cache, the first n_new[b] of the T, with the rotation of
     inv_freq (fp64 [rot/2]) applied to the keys and to q [B,Hq,T,D]
     (linrec_kv_append).  Returns the rotated queries (None without q); rows
-    that n_new excludes are left as they were (zeros in a new q_out)."""
+    that are not there (behind n_new, of a sequence with a negative past) are
+    left as they were (zeros in a new q_out)."""
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         _fail("k: must be a [B,H,T,D] tensor")
     B, _, T, _ = k.shape
@@ -1158,7 +1159,7 @@ def kv_append(cache: KvCache, k, v, past, *, n_new=None, inv_freq=None, interlea
     dev = _same_device(k, ("v", v), ("past", past), ("n_new", n_new), ("inv_freq", inv_freq), ("q", q),
                        ("q_out", q_out), ("workspace", workspace), *zip(KvCache._fields, cache))
     if q is not None and q_out is None:
-        q_out = (torch.zeros if n_new is not None else torch.empty)((B, Hq, T, c.D), dtype=bf, device=q.device)
+        q_out = torch.zeros((B, Hq, T, c.D), dtype=bf, device=q.device)   # rows that are not there stay zeros
         oa = _arg4("q_out", q_out, q_out.shape, bf)
     if workspace is None and need:
         workspace = _bytes(need, k)
@@ -1174,7 +1175,8 @@ def kv_attn(cache: KvCache, q, past, *, n_new=None, scale=None, window=0, o=None
     these T tokens behind past[b] earlier ones (linrec_kv_attn).  scale:
     1/sqrt(D) by default; window: the last `window` tokens only (<= 0 or >=
     MAX_T: all).  lse: fp32 [B,Hq,T] to be filled, or None.  Returns o; rows
-    that n_new excludes are left as they were (zeros in a new o)."""
+    that are not there (behind n_new, of a sequence with a negative past) are
+    left as they were (zeros in a new o)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         _fail("q: must be a [B,Hq,T,D] tensor")
     B, Hq, T, _ = q.shape
@@ -1197,7 +1199,7 @@ def kv_attn(cache: KvCache, q, past, *, n_new=None, scale=None, window=0, o=None
     dev = _same_device(q, ("past", past), ("n_new", n_new), ("o", o), ("lse", lse), ("workspace", workspace),
                        *zip(KvCache._fields, cache))
     if o is None:
-        o = (torch.zeros if n_new is not None else torch.empty)(shape, dtype=bf, device=q.device)
+        o = torch.zeros(shape, dtype=bf, device=q.device)   # rows that are not there stay zeros
         oa = _arg4("o", o, shape, bf)
     if workspace is None and need:
         workspace = _bytes(need, q)

@@ -58,3 +58,22 @@ def test_windows_with_a_lower_bound(recorder, window):
     q = torch.zeros(2, 4, 3, 64).bfloat16()
     linrec.kv_attn(small_cache(), q, torch.zeros(2, dtype=torch.int32), window=window)
     assert ctypes.c_int32(recorder.calls["linrec_kv_attn"][ATTN_WINDOW]).value == window
+
+
+# ----------------------------------------------------------------- new outputs
+
+@pytest.fixture
+def dirty_memory(monkeypatch):
+    """Memory that is not asked to be cleared comes full of NaN."""
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: empty(*a, **kw).fill_(float("nan")))
+
+
+@pytest.mark.parametrize("n_new", [None, [2, 3]])
+def test_rows_that_are_not_there_are_zeros_in_new_outputs(recorder, dirty_memory, n_new):
+    """The calls write no row of a sequence with a negative past, n_new or not."""
+    q, k = torch.zeros(2, 4, 3, 64).bfloat16(), torch.zeros(2, 2, 3, 64).bfloat16()
+    past = torch.full((2,), -1, dtype=torch.int32)
+    n = None if n_new is None else torch.tensor(n_new, dtype=torch.int32)
+    assert (linrec.kv_attn(small_cache(), q, past, n_new=n) == 0).all()
+    assert (linrec.kv_append(small_cache(), k, k, past, n_new=n, q=q) == 0).all()

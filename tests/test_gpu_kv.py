@@ -463,3 +463,26 @@ def test_piece_then_tokens():
             s = torch.exp2(torch.ceil(torch.log2(x.abs().amax() / 448)))
             lim = 2.0 ** -4 * x.abs() + 2.0 ** -9 * s + 2.0 ** -20 * x.norm(dim=-1, keepdim=True)
             assert ((got[:, :T] - x).abs() <= lim).all()
+
+
+@pytest.mark.parametrize("T", [1, 4, 70])
+@pytest.mark.parametrize("given", [False, True])
+def test_sequences_that_are_not_there(T, given):
+    """A negative past: the sequence has no new tokens, n_new or not.  Outputs the
+    calls make themselves hold zeros there, whatever their memory held before;
+    given ones, the cache and lse stay as they were; the others are as ever."""
+    g, cache, q = draw(40, 3, T, 4, 2, 64, 16, 8)
+    past, n = [-1, 30, -(1 << 31)], [0, T, 0]
+    check_attn(cache, q, past, n, n_new=given)
+    k, v = (torch.randn(3, 2, T, 64, generator=g).to(torch.bfloat16) for _ in range(2))
+    check_append(cache, k, v, past, n, freqs(16), False, q, given)
+    gpu, dq, kd, vd = to_dev(cache), q.to(DEV), k.to(DEV), v.to(DEV)
+    past_d = torch.tensor(past, dtype=torch.int32, device=DEV)
+    n_d = torch.full((3,), T, dtype=torch.int32, device=DEV) if given else None
+    for call in (lambda: linrec.kv_attn(gpu, dq, past_d, n_new=n_d),
+                 lambda: linrec.kv_append(gpu, kd, vd, past_d, n_new=n_d, q=dq)):
+        for _ in range(8):     # what the allocator hands out next is full of NaN
+            torch.full(q.shape, math.nan, dtype=torch.bfloat16, device=DEV)
+        out = call()
+        torch.cuda.synchronize()
+        assert (out[0] == 0).all() and (out[2] == 0).all() and (out[1] != 0).any()
