@@ -600,7 +600,11 @@ size_t linrec_kv_attn_workspace_bytes(const linrec_kv_cache* cache, int32_t B, i
  * (window <= 0 or >= LINREC_MAX_T: no lower bound).  lse: fp32 contiguous [B,Hq,T], the natural
  * logarithm of the sum, or NULL.  A row that sees no token gets o = 0 and
  * lse = -inf.  Cached values that a row does not see never reach it, whatever
- * they are.  Hq: a multiple of cache->H.  scale: finite.
+ * they are.  A value it sees that is NaN or infinite, or whose product with the
+ * scale reaches 2^128, leaves its feature of the row infinite or NaN; so do sums
+ * past fp32's range: they are formed with weights of up to 2^8 before the division,
+ * so values below 2^120 / (tokens seen) never get there.  Hq: a multiple of
+ * cache->H.  scale: finite.
  * The result does not depend on what else is in the batch beyond the choice of
  * the split (a function of B, T, Hq and the cache's sizes), and repeats bit for
  * bit. */

@@ -174,23 +174,31 @@ struct Range {
 
 // A tile at the border of what the rows see may hold, for some rows, values
 // they do not see.  Their weight is 0, but 0 * NaN is not 0.  Values that are
-// not finite (a NaN code, or any code under a scale that is not) are therefore
-// taken out of a border tile when it is loaded, and rows that do see one get a
-// NaN in its feature afterwards.  Both are rare, and kept off the registers of
-// the rest.
+// not finite (a NaN code, any code under a scale that is not, a code that the
+// scale takes past bf16's range) are therefore taken out of a border tile when it
+// is loaded, and rows that do see one get a NaN in its feature afterwards.  Both
+// are rare, and kept off the registers of the rest.
+
+// The codes that are not finite under `scale` are those whose low 7 bits, as a
+// number, reach some border; this is its distance from 0x80, so that adding it
+// carries into a code's top bit exactly for them.  Of a scale 2^e below 2^120 that is
+// 0x7f, the NaN code (448 * 2^119 is below 2^128); from there on the code of
+// 2^(128 - e), which is (128 - e + 7) << 3; of a scale that is not finite every code.
+__device__ __forceinline__ unsigned nonfinite_lift(float scale)
+{
+    const unsigned e = __float_as_uint(scale) >> 23 & 0xffu;   // biased by 127
+    return e == 255 ? 0x80u : e >= 247 ? 0x80u - ((262 - e) << 3) : 1u;
+}
 
 // 16 codes under `scale`: what is not finite becomes code 0; whether there was
 // any.  (finite_scale() of the scale then keeps 0 a 0.)
 __device__ __forceinline__ bool take_nonfinite(u32x4& v, float scale)
 {
     unsigned any = 0;
-    const bool inf = (__float_as_uint(scale) & 0x7f800000u) == 0x7f800000u;
+    const unsigned lift = nonfinite_lift(scale) * 0x01010101u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // 0x7f, the NaN code, is the one whose low 7 bits carry into the top one
-        unsigned n = ((v[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-        if (inf)
-            n = 0x80808080u;
+        const unsigned n = ((v[i] & 0x7f7f7f7fu) + lift) & 0x80808080u;
         v[i] &= ~((n >> 7) * 0xffu);
         any |= n;
     }
@@ -205,11 +213,11 @@ __device__ __forceinline__ float finite_scale(float scale)
 // Of 8 codes under `scale`, 1 for each that is not finite, as bf16.
 __device__ __forceinline__ Frag<bf16> nonfinite8(u32x2 w, float scale)
 {
-    const bool inf = (__float_as_uint(scale) & 0x7f800000u) == 0x7f800000u;
+    const unsigned lift = nonfinite_lift(scale) * 0x01010101u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const unsigned n = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-        w[i] = inf ? 0x38383838u : (n >> 7) * 0x38u;   // 0x38 is 1
+        const unsigned n = ((w[i] & 0x7f7f7f7fu) + lift) & 0x80808080u;
+        w[i] = (n >> 7) * 0x38u;   // 0x38 is 1
     }
     return frag(values8(w[0], w[1], 1.f));
 }

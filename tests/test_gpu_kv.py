@@ -486,3 +486,69 @@ def test_sequences_that_are_not_there(T, given):
         out = call()
         torch.cuda.synchronize()
         assert (out[0] == 0).all() and (out[2] == 0).all() and (out[1] != 0).any()
+
+
+LARGE = [(64, 1, 2, 16), (64, 6, 8, 64), (128, 1, 4, 32), (128, 90, 2, 16), (64, 90, 2, 128), (128, 90, 2, 64), (128, 6, 8, 16)]
+
+
+@pytest.mark.parametrize("D,T,Hq,page", LARGE)
+@pytest.mark.parametrize("exponent", [119, 120, 124, 127])
+def test_attention_hidden_values_under_the_largest_scales(D, T, Hq, page, exponent):
+    """A code times a scale may pass bf16's range (2^120 * 256, which the append stores
+    for the largest bf16 values; 2^127 * 448).  Rows that do not see it are as ever: a page
+    behind the last token in the same tile, and tokens behind it in the same page, where
+    the first visible one holds 2^118 (times a weight of at most 2^8 that is in range)."""
+    _, cache, q = draw(41, 2, T, Hq, 2, D, page, 256 // page)
+    past = [37, 100]
+    for b in range(2):
+        end = past[b] + T                    # the first hidden token
+        blk, off = end // page, end % page
+        last = (end | 63) // page            # the tile's last page
+        for p in range(blk, min(last, cache.table.shape[1] - 1) + 1):
+            p_id = int(cache.table[b, p])
+            cache.v_scale[p_id] = 2.0 ** exponent
+            lo = off if p == blk else 0
+            cache.v.view(torch.uint8)[p_id, :, :, :lo] = 0
+            cache.v[p_id, :, :, :min(lo, 1)] = torch.tensor(2.0 ** (118 - exponent)).to(F8)
+            cache.v.view(torch.uint8)[p_id, :, :, lo:] = 0x7e if b == 0 else 0xfe      # +-448
+    check_attn(cache, q, past, [T] * 2)
+    check_attn(cache, q, past, [T] * 2, window=21)
+
+
+@pytest.mark.parametrize("D,T,Hq,page", [c for c in LARGE if c[1] > 1])
+@pytest.mark.parametrize("exponent,code", [(120, 0x78), (120, 0xfe), (127, 0x40), (125, 0xd0)])
+def test_attention_values_past_bf16_reach_only_rows_that_see_them(D, T, Hq, page, exponent, code):
+    """Such a value within the rows' own tokens: rows before it are as ever, and those
+    that see it get no finite number in its feature, as from an infinity."""
+    _, cache, q = draw(42, 1, T, Hq, 1, D, page, 256 // page)
+    past, at, f = 37, 37 + T // 2, 9
+    p = int(cache.table[0, at // page])
+    cache.v_scale[p] = 2.0 ** exponent
+    cache.v.view(torch.uint8)[p] = 0
+    cache.v[p, :, :, 0] = torch.tensor(2.0 ** (118 - exponent)).to(F8)
+    cache.v.view(torch.uint8)[p, :, f, at % page] = code
+    shown = linrec.KvCache(*(t.clone() for t in cache))
+    shown.v.view(torch.uint8)[p, :, f, at % page] = 0x7f         # a NaN: the reference's mark
+    ref, mag, _ = attn_reference(shown, q, [past], [T], D ** -0.5, 0)
+    o = linrec.kv_attn(to_dev(cache), q.to(DEV), torch.tensor([past], dtype=torch.int32, device=DEV)).double().cpu()
+    seen = torch.isnan(ref)
+    assert seen[:, :, T // 2:, f].all() and not seen[:, :, :T // 2].any()
+    assert torch.equal(torch.isfinite(o), ~seen)
+    assert ((o - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * mag + 2.0 ** -8 * ref.abs())[~seen].all()
+
+
+@pytest.mark.parametrize("D,T,Hq,page", LARGE)
+@pytest.mark.parametrize("exponent", [119, 120, 124, 127])
+def test_attention_sums_past_fp32_are_not_finite(D, T, Hq, page, exponent):
+    """Visible values of 2^123 and more, whose weighted sums may pass fp32's range before
+    they are divided: what comes out finite is right."""
+    _, cache, q = draw(41, 2, T, Hq, 2, D, page, 256 // page)
+    past = [37, 100]
+    for b in range(2):
+        p = int(cache.table[b, (past[b] + T) // page])
+        cache.v_scale[p] = 2.0 ** exponent
+        cache.v[p] = (cache.v[p].float().sign() * 2.0 ** min(126 - exponent, 4)).to(F8)
+    ref, mag, _ = attn_reference(cache, q, past, [T] * 2, D ** -0.5, 0)
+    o = linrec.kv_attn(to_dev(cache), q.to(DEV), torch.tensor(past, dtype=torch.int32, device=DEV)).double().cpu()
+    near = (o - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * mag + 2.0 ** -8 * ref.abs()
+    assert (near | ~torch.isfinite(o)).all()
