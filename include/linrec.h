@@ -603,8 +603,9 @@ size_t linrec_kv_attn_workspace_bytes(const linrec_kv_cache* cache, int32_t B, i
  * they are.  A value it sees that is NaN or infinite, or whose product with the
  * scale reaches 2^128, leaves its feature of the row infinite or NaN; so do sums
  * past fp32's range: they are formed with weights of up to 2^8 before the division,
- * so values below 2^120 / (tokens seen) never get there.  Hq: a multiple of
- * cache->H.  scale: finite.
+ * so values below 2^120 / (tokens seen) never get there.  A row whose largest
+ * score, times scale * log2(e), reaches +-2^128 is NaN, as is its lse.  Hq: a
+ * multiple of cache->H.  scale: finite.
  * The result does not depend on what else is in the batch beyond the choice of
  * the split (a function of B, T, Hq and the cache's sizes), and repeats bit for
  * bit. */

@@ -299,18 +299,22 @@ __device__ __forceinline__ void attend(RowState<D> (&st)[NR], floatx4 (&x)[NR][4
         read_ahead<NR, D / 8>();
 }
 
-// A row's place in o and lse.
+// A row's place in o and lse.  No weight at all means that the row sees nothing
+// (zeros and -inf).  Where there is a maximum, that or an infinite sum means that
+// the maximum passes fp32's range with the scale and took every exponent with it:
+// NaN, not an empty row.
 template <int D>
 __device__ __forceinline__ void write_row(const AttnArgs& a, int b, int h, int row, int f, const floatx4& y, float m,
                                           float l)
 {
     const int tok = row / a.group, hq = h * a.group + row % a.group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool sums = l != 0.f && l != INFINITY, empty = m == -INFINITY;
+    const float inv = sums ? 1.f / l : empty ? 0.f : __builtin_nanf("");
     *reinterpret_cast<bf16x4*>(a.o.head(b, hq) + (int64_t)tok * a.o.st + f) =
         bf16x4{(bf16)(y[0] * inv), (bf16)(y[1] * inv), (bf16)(y[2] * inv), (bf16)(y[3] * inv)};
     if (a.lse && f == 0)
         a.lse[((int64_t)b * a.Hq + hq) * a.T + tok] =
-            l == 0.f ? -INFINITY : (m * a.c2 + __log2f(l)) * 0.6931471805599453f;
+            sums ? (m * a.c2 + __log2f(l)) * 0.6931471805599453f : empty ? -INFINITY : __builtin_nanf("");
 }
 
 // A row's sums, and its maximum and total, in a split's part.

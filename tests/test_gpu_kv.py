@@ -552,3 +552,24 @@ def test_attention_sums_past_fp32_are_not_finite(D, T, Hq, page, exponent):
     o = linrec.kv_attn(to_dev(cache), q.to(DEV), torch.tensor(past, dtype=torch.int32, device=DEV)).double().cpu()
     near = (o - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * mag + 2.0 ** -8 * ref.abs()
     assert (near | ~torch.isfinite(o)).all()
+
+
+@pytest.mark.parametrize("T,Hq,max_pages", [(1, 4, 8), (1, 2, 60), (6, 8, 8), (90, 2, 8), (90, 2, 60)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_scores_past_fp32_are_no_empty_rows(T, Hq, max_pages, sign):
+    """A row whose largest scaled score passes fp32's range, upwards or downwards, comes as
+    NaN, not as the zeros and -inf of a row that sees nothing; a row of zero scores beside
+    it is as ever."""
+    _, cache, q = draw(43, 1, T, Hq, 2, 64, 16, max_pages)
+    q = q.abs()
+    cache.k.view(torch.uint8).bitwise_and_(0x7f).bitwise_or_(0x80 if sign < 0 else 0)   # scores of one sign
+    q[:, 0] = 0
+    past = max_pages * 16 - T - 3
+    q_d, past_d = q.to(DEV), torch.tensor([past], dtype=torch.int32, device=DEV)
+    lse = torch.empty(1, Hq, T, device=DEV)
+    o = linrec.kv_attn(to_dev(cache), q_d, past_d, scale=2.0 ** 127, lse=lse).double().cpu()
+    ref, mag, ref_lse = attn_reference(cache, q, [past], [T], 2.0 ** 127, 0)
+    assert (sign * ref_lse[:, 1:] > 2.0 ** 128).all()
+    assert torch.isnan(o[:, 1:]).all() and torch.isnan(lse[:, 1:]).all()
+    assert ((o - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * mag + 2.0 ** -8 * ref.abs())[:, 0].all()
+    assert ((lse.double().cpu() - ref_lse).abs() <= 2.0 ** -12 * (1 + ref_lse.abs()))[:, 0].all()
