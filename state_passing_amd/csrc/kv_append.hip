@@ -169,7 +169,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int j, int h, i
 {
     constexpr int U = D / 16, KR = 256 / U, KI = (P + KR - 1) / KR;           // units a row, rows a pass, passes
     constexpr int VV = D / 8, VU = P / 4 * VV, VI = (VU + 255) / 256;         // V: vectors a row, units, passes
-    __shared__ uint8_t turned[D][P + 16];
+    __shared__ __align__(16) uint8_t turned[D][P + 16];
     __shared__ float red[2][4];
     const int tid = threadIdx.x;
     const Span sp(a.past, a.n_new, b, a.T);

@@ -15,7 +15,7 @@ struct AttnArgs {
     Act<const bf16> q;
     Act<bf16> o;
     float* lse;
-    float* part;         // per split: rows of D unnormalised sums, then (max, sum) of every row
+    float* part;         // per split: rows of D unnormalised sums, then (max, sum) of every row (part_floats)
     const int* past;
     const int* n_new;
     int B, T, Hq, group, window, nsplit;
@@ -317,19 +317,23 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int b, int h, int r
             sums ? (m * a.c2 + __log2f(l)) * 0.6931471805599453f : empty ? -INFINITY : __builtin_nanf("");
 }
 
+// From one split's part to the next, for n rows: D sums and two statistics each,
+// up to whole 16-byte vectors (of an odd n they end 8 bytes into one).
+constexpr __host__ __device__ int64_t part_floats(int64_t n, int D) { return (n * (D + 2) + 3) / 4 * 4; }
+
 // A row's sums, and its maximum and total, in a split's part.
 template <int D>
 __device__ __forceinline__ float* part_row(const AttnArgs& a, int split, int b, int h, int row)
 {
     const int64_t n = (int64_t)a.B * a.c.H * a.rows;
-    return a.part + split * n * (D + 2) + (((int64_t)b * a.c.H + h) * a.rows + row) * D;
+    return a.part + split * part_floats(n, D) + (((int64_t)b * a.c.H + h) * a.rows + row) * D;
 }
 
 template <int D>
 __device__ __forceinline__ float* part_stat(const AttnArgs& a, int split, int b, int h, int row)
 {
     const int64_t n = (int64_t)a.B * a.c.H * a.rows;
-    return a.part + split * n * (D + 2) + n * D + (((int64_t)b * a.c.H + h) * a.rows + row) * 2;
+    return a.part + split * part_floats(n, D) + n * D + (((int64_t)b * a.c.H + h) * a.rows + row) * 2;
 }
 
 // ---- few rows: generation -----------------------------------------------
@@ -346,7 +350,7 @@ template <int D, int NR, bool PAGED>
 __global__ __launch_bounds__(256, D * NR == 256 ? 1 : 2) void kv_attn_token_kernel(AttnArgs a)
 {
     constexpr int KS = D / 64, DT = D / 16;
-    __shared__ float red[4][16][D + 4];
+    __shared__ __align__(16) float red[4][16][D + 4];
     __shared__ float ms[4][16 * NR], ls[4][16 * NR];
     const int tile = blockIdx.x % a.row_tiles, split = blockIdx.x / a.row_tiles, h = blockIdx.y, b = blockIdx.z;
     const Span sp(a.past, a.n_new, b, a.T);
@@ -533,7 +537,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
     const int lane = lane_id(), grp = lane / LPR, f4 = lane % LPR;
     const float2 stat = *reinterpret_cast<const float2*>(part_stat<D>(a, min(lane, a.nsplit - 1), b, h, row));
     const float* y = part_row<D>(a, 0, b, h, row) + 4 * f4;
-    const int64_t next = (int64_t)a.B * a.c.H * a.rows * (D + 2);   // from one split to the next
+    const int64_t next = part_floats((int64_t)a.B * a.c.H * a.rows, D);   // from one split to the next
     constexpr int U = 4;
     floatx4 first[U];
 #pragma unroll
@@ -593,7 +597,8 @@ __global__ __launch_bounds__(256, 2) void kv_attn_piece_kernel(AttnArgs a)
 {
     constexpr int NR = 2, ROWS = 64 * NR, DT = D / 16, KP = D + 16, VP = 64 + 16;
     constexpr int KV = 64 * D / 16 / 256;   // 16-byte vectors of K, and of V, a thread stages
-    __shared__ bf16 kt[2][64 * KP], vt[2][D * VP];
+    __shared__ __align__(16) bf16 kt[2][64 * KP];
+    __shared__ __align__(16) bf16 vt[2][D * VP];
     __shared__ int there[2][4];              // whether the page of each 16-key group is there
     __shared__ int bad[2];                   // border tile: values were taken out
     const int nbh = a.c.H * a.B;
@@ -869,7 +874,7 @@ size_t linrec_kv_attn_workspace_bytes(const linrec_kv_cache* cache, int32_t B, i
         return 0;
     const Plan p = plan_of(cache, B, T, Hq);
     return p.nsplit == 1 ? 0
-                         : (size_t)p.nsplit * B * cache->H * p.rows * (size_t)(cache->D + 2) * sizeof(float);
+                         : (size_t)p.nsplit * part_floats((int64_t)B * cache->H * p.rows, cache->D) * sizeof(float);
 }
 
 linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int32_t B, int32_t T, int32_t Hq,

@@ -266,3 +266,14 @@ def test_cache_binding():
     ]:
         with pytest.raises(exc, match=match):
             att(**kw)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,group,T", [(1, 1, 1, 1), (1, 1, 1, 3), (3, 1, 5, 1), (1, 3, 1, 129), (1, 1, 2, 1)])
+def test_attn_workspace_holds_aligned_splits(D, B, H, group, T):
+    """Two splits of an odd number of rows: each has whole 16-byte vectors, so that the
+    second one's are aligned as the first one's are."""
+    c = cache(max_pages=16 if T > 64 else 8, H=H, D=D)      # 8 tiles of keys (16 for a piece): two splits
+    w = linrec._lib().linrec_kv_attn_workspace_bytes(ctypes.byref(c), B, T, H * group)
+    rows = B * H * group * T
+    assert w % 32 == 0 and 0 <= w - 2 * rows * (D + 2) * 4 < 32

@@ -573,3 +573,24 @@ def test_attention_scores_past_fp32_are_no_empty_rows(T, Hq, max_pages, sign):
     assert torch.isnan(o[:, 1:]).all() and torch.isnan(lse[:, 1:]).all()
     assert ((o - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * mag + 2.0 ** -8 * ref.abs())[:, 0].all()
     assert ((lse.double().cpu() - ref_lse).abs() <= 2.0 ** -12 * (1 + ref_lse.abs()))[:, 0].all()
+
+
+# (B, T, Hq, H, D, page, max_pages, past): odd numbers of rows, several splits
+ODD = [(1, 1, 1, 1, 128, 64, 64, [4000]), (1, 1, 1, 1, 64, 16, 64, [1000]), (1, 3, 1, 1, 128, 32, 40, [1200]),
+       (3, 1, 5, 1, 64, 128, 16, [2000, 0, 700]), (1, 129, 3, 3, 128, 64, 20, [1100]), (1, 67, 1, 1, 64, 16, 90, [1300])]
+
+
+@pytest.mark.parametrize("case", ODD, ids=[str(i) for i in range(len(ODD))])
+def test_attention_splits_of_an_odd_number_of_rows(case):
+    """The parts of every split lie on 16-byte boundaries; the workspace is used to its end
+    and no further."""
+    B, T, Hq, H, D, page, max_pages, past = case
+    _, cache, q = draw(44, B, T, Hq, H, D, page, max_pages)
+    c = linrec._kv_desc(cache, B)
+    need = linrec._lib().linrec_kv_attn_workspace_bytes(linrec.ctypes.byref(c), B, T, Hq)
+    rows = B * T * Hq
+    per = -(-rows * (D + 2) // 4) * 16
+    assert need % per == 0 and need // per > 1
+    work = torch.full((need + 256,), 0x5a, dtype=torch.uint8, device=DEV)
+    check_attn(cache, q, past, [T] * B, workspace=work)
+    assert (work[need:] == 0x5a).all() and (work[:need - 16] != 0x5a).any()
