@@ -599,8 +599,10 @@ size_t linrec_kv_attn_workspace_bytes(const linrec_kv_cache* cache, int32_t B, i
  * over the cached tokens j with past[b] + i - window < j <= past[b] + i
  * (window <= 0 or >= LINREC_MAX_T: no lower bound).  lse: fp32 contiguous [B,Hq,T], the natural
  * logarithm of the sum, or NULL.  A row that sees no token gets o = 0 and
- * lse = -inf.  Cached values that a row does not see never reach it, whatever
- * they are.  A value it sees that is NaN or infinite, or whose product with the
+ * lse = -inf.  Scores, weights and sums are formed in fp32; a weight enters the
+ * product with v as bf16, off by at most 2^-8 of itself (their total is of the
+ * weights before that).  Cached values that a row does not see never reach it,
+ * whatever they are.  A value it sees that is NaN or infinite, or whose product with the
  * scale reaches 2^128, leaves its feature of the row infinite or NaN; so do sums
  * past fp32's range: they are formed with weights of up to 2^8 before the division,
  * so values below 2^120 / (tokens seen) never get there.  A row whose largest

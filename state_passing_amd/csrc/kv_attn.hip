@@ -95,6 +95,15 @@ __device__ __forceinline__ float quad_sum(float x)
 
 // One tile's scores x (lane (g, t): product i, element r) become the weights'
 // fragments p (k32 step s from products 2s, 2s + 1).
+//
+// The weights enter the second product as bf16, V's type there (exact for its
+// codes): each is off by at most 2^-8 of itself, so o by 2^-8 sum_j p_j |v_j|
+// before its own rounding.  Of outputs whose rounding alone puts them 0.0017 off
+// (relative, root mean square), that makes 0.0019 (one user of 4096 tokens) to 0.0023
+// (4096 tokens behind 12K).  Pairs of bf16 would halve the second product's rate,
+// on the unit that bounds pieces.  The total l is of the weights before the rounding:
+// adding up the rounded ones would take a conversion back for each, so what a row
+// really gives its values adds up to 1 within 2^-8.
 template <int D>
 __device__ __forceinline__ void softmax_tile(RowState<D>& st, floatx4 (&x)[4], Frag<bf16> (&p)[2], float c2)
 {
@@ -586,7 +595,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnArgs a)
 //
 // Bound by the matrix and vector units (4 D flops a score, and about 6 vector
 // instructions with one exp), which two waves a SIMD (237 registers) overlap in
-// part: 4096 tokens behind 12K, 16 / 4 heads of 128, take 475 us (1010 TFLOP/s; a
+// part: 4096 tokens behind 12K, 16 / 4 heads of 128, take 478-484 us (1000 TFLOP/s; a
 // library's large product reaches 1210).  Four waves of 32 rows each share every
 // tile of 64 keys: the codes are converted once, on the way into LDS ([key][feature]
 // and, for V, [feature][key]), two buffers deep, while the loads of the next
@@ -824,10 +833,14 @@ Plan plan_of(const linrec_kv_cache* c, int B, int T, int Hq)
     p.row_tiles = (p.rows + tile_rows - 1) / tile_rows;
     const int64_t blocks = (int64_t)B * c->H * p.row_tiles;
     const int64_t key_tiles = ((int64_t)c->max_pages * c->page + 63) / 64;
-    // Splits fill the 256 CUs with one round of workgroups (two a CU); each gets
-    // at least one tile a wave (token kernel) or 8 tiles (piece kernel).  Rounds of
-    // 512, 768, 1024, 2048, 4096 workgroups: 180, 194, 180, 182, 194 us at 32
-    // sequences of 16K, 15.6, 19.2, 20.8, 23.1, 23.1 at 16 windows of 2048.
+    // Splits bring the workgroups to at least 512, two a CU (of the token kernel with
+    // two row tiles at D = 128, whose registers leave one a CU, that is two rounds);
+    // whole splits overshoot that, up to 1022 (511 blocks in two).  Their number is
+    // bounded by the table's capacity: one tile a wave (token kernel) or 8 tiles
+    // (piece kernel) of a sequence that fills it; a shorter one's splits hold fewer,
+    // down to 4 tiles (token kernel) or one.  Aiming at 512, 768, 1024, 2048, 4096
+    // workgroups: 180, 194, 180, 182, 194 us at 32 sequences of 16K, 15.6, 19.2,
+    // 20.8, 23.1, 23.1 at 16 windows of 2048.
     const int64_t want = (512 + blocks - 1) / blocks;
     const int64_t most = std::max<int64_t>(1, key_tiles / (p.token ? 4 : 8));
     p.nsplit = (int)std::min<int64_t>(std::min(want, most), MAX_SPLITS);
