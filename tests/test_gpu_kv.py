@@ -594,3 +594,30 @@ def test_attention_splits_of_an_odd_number_of_rows(case):
     work = torch.full((need + 256,), 0x5a, dtype=torch.uint8, device=DEV)
     check_attn(cache, q, past, [T] * B, workspace=work)
     assert (work[need:] == 0x5a).all() and (work[:need - 16] != 0x5a).any()
+
+
+def test_captured_calls_that_make_their_outputs():
+    """Outputs made within a capture are cleared by every replay, whatever was left in
+    their memory, between eager calls that make theirs."""
+    g, cache, q = draw(45, 3, 2, 4, 2, 64, 16, 8)
+    k, v = (torch.randn(3, 2, 2, 64, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    gpu, dq, past = to_dev(cache), q.to(DEV), torch.tensor([-1, 30, 5], dtype=torch.int32, device=DEV)
+
+    freq = freqs(16).to(DEV)
+
+    def both():
+        qr = linrec.kv_append(gpu, k, v, past, q=dq, inv_freq=freq)
+        return qr, linrec.kv_attn(gpu, qr, past)
+
+    want = both()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for _ in range(4):
+        for t in out:
+            t.fill_(math.nan)
+        graph.replay()
+        again = both()
+        torch.cuda.synchronize()
+        for a, b, c in zip(out, want, again):
+            assert torch.equal(a, b) and torch.equal(c, b) and (a[0] == 0).all()
