@@ -616,6 +616,150 @@ linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int3
                              const int32_t* n_new, float scale, int32_t window, linrec_tensor o,
                              float* lse, void* workspace, void* stream);
 
+/* ------------------------------------------------- short causal convolution
+ * Per batch b and channel c, over a sub-sequence of T tokens:
+ *
+ *     p_t = bias + sum_{k < K} w_k x_{t-K+1+k},   y_t = p_t   (LINREC_ACT_NONE)
+ *                                        y_t = p_t / (1 + exp(-p_t))  (LINREC_ACT_SILU)
+ *
+ * the convolution in front of a state-space scan, or of q, k and v of a
+ * delta-rule layer.  The K-1 inputs before the piece are its state: they enter
+ * as state_in, and the last K-1 inputs leave as state_out, so pieces chain as
+ * for the layer (in fp32, which holds an input exactly).
+ *
+ * Layouts: x, y, dy, dx are [B, T, C] as for the elementwise recurrence (rows
+ * 16-byte aligned, channels contiguous); w: fp32 [C, K], bias: fp32 [C] or NULL
+ * (zeros); states: fp32 [B, K-1, C], the oldest input first; all contiguous.
+ * K in {2, 3, 4}; 1 <= B <= 32767, 1 <= C <= 2^20, 0 <= T <= LINREC_MAX_T.
+ * Inputs share `dtype`, outputs `out_dtype` (LINREC_F32 when dtype is); sums are
+ * formed in fp32.
+ *   n_new: int32 [B] in device memory, the first n_new[b] of the T tokens
+ *   (clamped to [0, T]) are there, or NULL: all.  Rows behind them are neither
+ *   read nor written; the state that leaves is that of the last token there. */
+typedef enum { LINREC_ACT_NONE = 0, LINREC_ACT_SILU = 1 } linrec_act;
+
+typedef struct {
+    int32_t B, T, C, K;
+    int32_t act;              /* linrec_act */
+    int32_t dtype;            /* linrec_dtype of x, dy */
+    int32_t out_dtype;        /* linrec_dtype of y, dx */
+} linrec_conv_desc;
+
+/* Forward.  state_in: NULL means zeros.  state_out: required, may alias
+ * state_in.  T == 0 copies state_in to state_out and does nothing else. */
+linrec_status linrec_conv_fwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec_tensor x,
+                              const float* w, const float* bias, const float* state_in,
+                              const int32_t* n_new, linrec_tensor y, float* state_out, void* stream);
+
+/* Bytes of workspace linrec_conv_bwd needs (0 if `d` is invalid or T == 0):
+ * the taps' gradients of every workgroup, and dstate_in. */
+size_t linrec_conv_bwd_workspace_bytes(const linrec_conv_desc* d);
+
+/* Backward, for L = <dy, y> + <dstate_out, state_out>, with dp = dy y'(p):
+ *     dx_t = sum_k w_k dp_{t+K-1-k},  dw_k = sum_{b,t} dp_t x_{t-K+1+k},
+ *     dbias = sum_{b,t} dp_t,
+ * and dstate_in the gradient of the K-1 inputs before the piece.  dstate_out:
+ * NULL means zeros.  dw: fp32 [C, K], dbias: fp32 [C] or NULL (not wanted), both
+ * of this piece alone and summed in a fixed order.  dstate_in: required, may
+ * alias dstate_out.  T == 0: zeros for dw and dbias, dstate_out to dstate_in. */
+linrec_status linrec_conv_bwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec_tensor x,
+                              const float* w, const float* bias, const float* state_in,
+                              const int32_t* n_new, linrec_tensor dy, const float* dstate_out,
+                              linrec_tensor dx, float* dw, float* dbias, float* dstate_in,
+                              void* workspace, void* stream);
+
+/* One or a few tokens, the states updated in place in a pool, fp32 contiguous
+ * [nslots, K-1, C], as linrec_step: entry b uses state slots[b] (int32 [B] in
+ * device memory), or state b if slots is NULL; an entry whose slot is outside
+ * the pool, or occurs at an earlier entry, is skipped (y = 0). */
+linrec_status linrec_conv_step(linrec_ctx* ctx, const linrec_conv_desc* d, linrec_tensor x,
+                               const float* w, const float* bias, float* S, const int32_t* slots,
+                               int32_t nslots, linrec_tensor y, void* stream);
+
+/* --------------------------------------------------- selective state-space scan
+ * Per batch b and channel c, with N states a channel, over T tokens:
+ *
+ *     d_t = dt_t + dt_bias, or softplus of that (`softplus` != 0)
+ *     h_0 = h_in,  h_t[n] = exp(d_t A[n]) h_{t-1}[n] + d_t x_t b_t[n],  h_out = h_T
+ *     y_t = (sum_n c_t[n] h_t[n] + D x_t) g_t,   g_t = 1, or z_t / (1 + exp(-z_t))
+ *
+ * the recurrence of a state-space layer whose step d and projections b and c
+ * depend on the token: a gate per state, where the layer above has one per head
+ * and the elementwise recurrence one per channel.  Pieces chain through h_out ->
+ * h_in and, backward, dh_in -> dh_out, as for the layer.
+ *
+ * Layouts: x, dt, z, y and their gradients are [B, T, C] as for the elementwise
+ * recurrence; b, c, db, dc are [B, G, T, N] (strides sb, sh over the groups, st;
+ * n contiguous; rows 16-byte aligned): channel c uses group c / (C / G).  A: fp32
+ * [C, N], D and dt_bias: fp32 [C] or NULL (zeros); h_in, h_out, dh_out, dh_in:
+ * fp32 [B, C, N]; all contiguous.  z.ptr == NULL: no gate.
+ * N in {8, 16, 32, 64}; G divides C, and with G > 1 the C / G channels of a group
+ * fill whole 16-byte vectors of x and of y; 1 <= B <= 32767, 1 <= C <= 2^20,
+ * 0 <= T <= LINREC_MAX_T.  Inputs share `dtype`, outputs `out_dtype` (LINREC_F32
+ * when dtype is); states, sums and parameters are fp32.  n_new as for the
+ * convolution. */
+typedef struct {
+    int32_t B, T, C, N, G;
+    int32_t softplus;         /* 0 or 1 */
+    int32_t dtype;            /* linrec_dtype of x, dt, b, c, z, dy */
+    int32_t out_dtype;        /* linrec_dtype of y and the gradients of x, dt, b, c, z */
+} linrec_scan_desc;
+
+/* What every call of the scan reads. */
+typedef struct {
+    linrec_tensor x, dt, b, c, z;
+    const float* A;
+    const float* D;           /* or NULL */
+    const float* dt_bias;     /* or NULL */
+} linrec_scan_inputs;
+
+/* Bytes linrec_scan_fwd writes to `saved` for the backward: the states that
+ * enter every block of tokens, fp32.  Bytes of workspace of the two calls.  0 if
+ * `d` is invalid or T == 0, or none is needed. */
+size_t linrec_scan_saved_bytes(const linrec_scan_desc* d);
+size_t linrec_scan_fwd_workspace_bytes(const linrec_scan_desc* d);
+size_t linrec_scan_bwd_workspace_bytes(const linrec_scan_desc* d);
+
+/* Forward.  h_in: NULL means zeros.  h_out: required, may alias h_in.  saved:
+ * NULL, or linrec_scan_saved_bytes(d) bytes, 16-byte aligned, that the backward
+ * of this piece reads.  T == 0 copies h_in to h_out and does nothing else. */
+linrec_status linrec_scan_fwd(linrec_ctx* ctx, const linrec_scan_desc* d, const linrec_scan_inputs* in,
+                              const float* h_in, const int32_t* n_new, linrec_tensor y, float* h_out,
+                              void* saved, void* workspace, void* stream);
+
+/* The gradients linrec_scan_bwd writes.  dz is written when the inputs have a z.
+ * dA: fp32 [C, N], required; dD, ddt_bias: fp32 [C], or NULL (not wanted). */
+typedef struct {
+    linrec_tensor dx, ddt, db, dc, dz;
+    float* dA;
+    float* dD;
+    float* ddt_bias;
+    float* dh_in;             /* fp32 [B, C, N], required, may alias dh_out */
+} linrec_scan_grads;
+
+/* Backward, for L = <dy, y> + <dh_out, h_out>, from the forward's `saved`.  With
+ * e_t = dy_t g_t:
+ *     G_t = c_t e_t + a_{t+1} G_{t+1}   (dh_out enters at t = T),  a_t = exp(d_t A),
+ *     dc_t[n] = sum_c e_t h_t[n],  db_t[n] = sum_c G_t[n] d_t x_t  (over the channels
+ *     of the group),  q_t = a_t G_t h_{t-1},  dA = sum_{b,t} q_t d_t,
+ *     dd_t = sum_n q_t A + x_t sum_n G_t b_t,  dx_t = e_t D + d_t sum_n G_t b_t,
+ *     ddt_t = dd_t (times the softplus' slope),  dD = sum_{b,t} e_t x_t,
+ *     ddt_bias = sum_{b,t} ddt_t,  dh_in = a_1 G_1,  dz_t = dy_t (y_t / g_t) g'(z_t).
+ * The states are formed again in fp32 from the saved ones.  dh_out: NULL means
+ * zeros.  Sums over batch, tokens and channels run in a fixed order, so results
+ * repeat bit for bit.  T == 0: zeros for dA, dD and ddt_bias, dh_out to dh_in. */
+linrec_status linrec_scan_bwd(linrec_ctx* ctx, const linrec_scan_desc* d, const linrec_scan_inputs* in,
+                              const void* saved, const int32_t* n_new, linrec_tensor dy,
+                              const float* dh_out, const linrec_scan_grads* out, void* workspace,
+                              void* stream);
+
+/* One or a few tokens, the states updated in place in a pool, fp32 contiguous
+ * [nslots, C, N], 16-byte aligned; slots as linrec_conv_step (a skipped entry:
+ * y = 0). */
+linrec_status linrec_scan_step(linrec_ctx* ctx, const linrec_scan_desc* d, const linrec_scan_inputs* in,
+                               float* S, const int32_t* slots, int32_t nslots, linrec_tensor y,
+                               void* stream);
+
 /* Kernel kinds for linrec_ctx_kernel_times(). */
 enum {
     LINREC_KERNEL_FWD_SUM = 0,    /* forward segment sums (parallel)           */
@@ -632,7 +776,13 @@ enum {
     LINREC_KERNEL_STEP = 11,      /* token step                                */
     LINREC_KERNEL_KV_APPEND = 12, /* append to the paged cache                 */
     LINREC_KERNEL_KV_ATTN = 13,   /* attention over the paged cache (each call's kernels) */
-    LINREC_KERNEL_KINDS = 14
+    LINREC_KERNEL_CONV_FWD = 14,  /* causal convolution forward                */
+    LINREC_KERNEL_CONV_BWD = 15,  /* causal convolution backward (each call's kernels) */
+    LINREC_KERNEL_CONV_STEP = 16, /* causal convolution, token step            */
+    LINREC_KERNEL_SCAN_FWD = 17,  /* selective scan forward (each call's kernels)  */
+    LINREC_KERNEL_SCAN_BWD = 18,  /* selective scan backward (each call's kernels) */
+    LINREC_KERNEL_SCAN_STEP = 19, /* selective scan, token step                */
+    LINREC_KERNEL_KINDS = 20
 };
 
 /* Per-kernel timing (instrumentation, off by default).  While enabled, every

@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblinrec.so")
 SOURCES = ["api.hip", "kernels.hip", "delta.hip", "diag.hip", "step.hip", "kv_append.hip",
-           "kv_attn.hip"]
+           "kv_attn.hip", "conv.hip", "scan.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -1,0 +1,964 @@
+// scan.hip -- the selective state-space scan (linrec_scan_fwd / _bwd / _step):
+//   d = dt + dt_bias or its softplus,  h_t = exp(d_t A) h_{t-1} + d_t x_t b_t,
+//   y_t = (c_t . h_t + D x_t) silu(z_t),
+// N states a channel, b and c shared by the channels of a group.
+//
+// A lane owns 4 states of a channel, N / 4 lanes a channel, so a workgroup of
+// four waves walks 4 * 64 / (N / 4) channels token by token with their states in
+// registers.  Token rows are read 16 bytes at a time by a mapping of their own,
+// a tile of 32 tokens ahead: each value that belongs to a token and channel (the
+// step d, the input d x, the gates) is formed once there and passed through LDS.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ctx.hpp"
+#include "device.hpp"
+#include "rows.hpp"
+
+namespace linrec {
+namespace {
+
+constexpr int NT = 256;      // threads a workgroup
+constexpr int NS = 4;        // states a lane
+constexpr int TILE = 32;     // tokens a tile
+constexpr int BLOCK = 8;     // tokens between two saved states
+constexpr float LOG2E = 1.44269504088896341f;
+
+template <int N>
+struct Geo {
+    static constexpr int L = N / NS;        // lanes a channel
+    static constexpr int CPW = 64 / L;      // channels a wave
+    static constexpr int CW = NT / 64 * CPW;   // channels a workgroup
+};
+
+template <typename T>
+struct In {
+    Act<const T> x, dt, b, c, z;
+    const float *A, *D, *dt_bias;
+    int softplus;
+};
+
+// The sequence and the channels of a workgroup.
+struct Where {
+    int b, g, c0, cend, n;   // sequence, group, first channel, end of the group's channels, tokens there
+};
+
+template <int N>
+__device__ __forceinline__ Where where(const int* n_new, int T_, int C, int G, int blocks)
+{
+    const int cg = C / G;
+    Where w;
+    w.b = blockIdx.z;
+    w.g = blockIdx.x / blocks;
+    w.c0 = w.g * cg + (int)(blockIdx.x % blocks) * Geo<N>::CW;
+    w.cend = (w.g + 1) * cg;
+    w.n = n_new ? min(max(n_new[w.b], 0), T_) : T_;
+    return w;
+}
+
+__device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf(1.f + __expf(-p)); }
+
+// log(1 + e^v) = max(v, 0) + 2 artanh(e / (2 + e)), e = exp(-|v|): the series in
+// s = e / (2 + e) <= 1/3 keeps the relative precision of small steps; its first
+// dropped term, s^14 / 15, is 1.4e-8 of the sum.  slope: the derivative.
+__device__ __forceinline__ float softplus(float v, float& slope)
+{
+    const float e = __expf(-fabsf(v)), s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
+    const float r = __builtin_amdgcn_rcpf(1.f + e);
+    slope = v >= 0.f ? r : e * r;
+    float p = 1.f / 13;
+    p = __builtin_fmaf(p, q, 1.f / 11);
+    p = __builtin_fmaf(p, q, 1.f / 9);
+    p = __builtin_fmaf(p, q, 1.f / 7);
+    p = __builtin_fmaf(p, q, 1.f / 5);
+    p = __builtin_fmaf(p, q, 1.f / 3);
+    p = __builtin_fmaf(p, q, 1.f);
+    return __builtin_fmaf(2.f * s, p, fmaxf(v, 0.f));
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v)
+{
+    return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over the L lanes of a channel, in all of them.
+template <int L>
+__device__ __forceinline__ float channel_sum(float v)
+{
+    v = dpp_add<0xb1>(v);                       // lane ^ 1
+    if constexpr (L >= 4)
+        v = dpp_add<0x4e>(v);                   // lane ^ 2
+    if constexpr (L >= 8)
+        v = dpp_add<0x141>(v);                  // the other half of 8 lanes
+    if constexpr (L >= 16)
+        v = dpp_add<0x140>(v);                  // the other half of 16 lanes
+    return v;
+}
+
+// Sum over the channels of a wave (lanes L apart), in all of them.
+template <int L>
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int off = L; off < 64; off <<= 1)
+        v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// ---- the mapping that reads token rows ---------------------------------------
+//
+// A tile is TILE rows of CW channels; a thread takes PV of its 16-byte vectors,
+// all of the same channels.
+template <typename T, int N>
+struct Rows {
+    static constexpr int VN = Vec<T>::N, VPR = Geo<N>::CW / VN, COUNT = TILE * VPR, PV = (COUNT + NT - 1) / NT;
+    static_assert(NT % VPR == 0 && (COUNT % NT == 0 || COUNT < NT), "whole rounds of one thread's channels");
+    int c, nc, row;   // first channel, channels that exist, first row
+    __device__ __forceinline__ Rows(const Where& w)
+    {
+        const int v = threadIdx.x % VPR;
+        c = w.c0 + v * VN;
+        nc = (int)threadIdx.x < COUNT ? w.cend - c : 0;
+        row = threadIdx.x / VPR;
+    }
+    __device__ __forceinline__ int token(int i) const { return row + i * (NT / VPR); }
+    __device__ __forceinline__ int col() const { return (threadIdx.x % VPR) * VN; }
+    // rows t0 .. of sequence b; rows from `n` on come as zeros
+    __device__ __forceinline__ void load(u32x4 (&v)[PV], const Act<const T>& a, int b, int t0, int n) const
+    {
+#pragma unroll
+        for (int i = 0; i < PV; ++i) {
+            const int t = t0 + token(i);
+            v[i] = t < n && nc > 0 ? load_vec(a.ptr + b * a.sb + (int64_t)t * a.st + c, nc) : u32x4{0u, 0u, 0u, 0u};
+        }
+    }
+};
+
+// b and c of a tile: a thread takes PB of the 16-byte vectors of both.
+template <typename T, int N>
+struct Projections {
+    static constexpr int VN = Vec<T>::N, VPR = N / VN, ONE = TILE * VPR, COUNT = 2 * ONE, PB = (COUNT + NT - 1) / NT;
+    u32x4 v[PB];
+    __device__ __forceinline__ void load(const In<T>& in, const Where& w, int t0)
+    {
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            const int k = threadIdx.x + i * NT, r = k % ONE, t = t0 + r / VPR;
+            v[i] = u32x4{0u, 0u, 0u, 0u};
+            if (k < COUNT && t < w.n) {
+                const Act<const T>& a = k < ONE ? in.b : in.c;
+                v[i] = *reinterpret_cast<const u32x4*>(a.head(w.b, w.g) + (int64_t)t * a.st + r % VPR * VN);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float (*bc)[TILE][N]) const
+    {
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            const int k = threadIdx.x + i * NT, r = k % ONE;
+            if (k < COUNT) {
+                float* p = &bc[k / ONE][r / VPR][r % VPR * VN];
+#pragma unroll
+                for (int j = 0; j < VN; j += 4)
+                    *reinterpret_cast<floatx4*>(p + j) =
+                        floatx4{vec_get<T>(v[i], j), vec_get<T>(v[i], j + 1), vec_get<T>(v[i], j + 2), vec_get<T>(v[i], j + 3)};
+            }
+        }
+    }
+};
+
+// Where a lane's states lie.
+template <int N>
+struct Lane {
+    int q, col, c;   // state quad, channel of the workgroup's, channel
+    bool ok;
+    __device__ __forceinline__ Lane(const Where& w)
+    {
+        const int lane = threadIdx.x & 63;
+        q = lane % Geo<N>::L;
+        col = (threadIdx.x >> 6) * Geo<N>::CPW + lane / Geo<N>::L;
+        c = w.c0 + col;
+        ok = c < w.cend;
+    }
+    __device__ __forceinline__ floatx4 load(const float* p) const   // p: [C][N]
+    {
+        if (!p || !ok)
+            return zero4();
+        p += (int64_t)c * N + q * NS;
+        return floatx4{p[0], p[1], p[2], p[3]};
+    }
+    __device__ __forceinline__ void store(float* p, const floatx4& v) const
+    {
+        if (ok) {
+            p += (int64_t)c * N + q * NS;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                p[j] = v[j];
+        }
+    }
+};
+
+__device__ __forceinline__ floatx4 exp2_4(const floatx4& v)
+{
+    return floatx4{__builtin_amdgcn_exp2f(v[0]), __builtin_amdgcn_exp2f(v[1]), __builtin_amdgcn_exp2f(v[2]),
+                   __builtin_amdgcn_exp2f(v[3])};
+}
+
+__device__ __forceinline__ float dot4(const floatx4& a, const floatx4& b)
+{
+    float s = a[0] * b[0];
+#pragma unroll
+    for (int j = 1; j < 4; ++j)
+        s = __builtin_fmaf(a[j], b[j], s);
+    return s;
+}
+
+// Segments of a piece: seg tokens each; state: [B][nseg][C][N], total: [B][nseg][C].
+struct Segments {
+    int nseg, seg;
+    float *state, *total;
+};
+
+// ---- forward -----------------------------------------------------------------
+//
+// SUM: the state that a segment makes of zeros, and its sum of steps (whose
+// exponential with A is what the segment makes of the state that enters it).
+template <typename T, typename OT, int N, bool SUM>
+__global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_in, const int* n_new, Act<OT> y, float* h_out,
+                                                      float* saved, Segments sg, int T_, int C, int G, int blocks)
+{
+    typedef Rows<T, N> R;
+    constexpr int CW = Geo<N>::CW, L = Geo<N>::L, VN = R::VN, PV = R::PV;
+    __shared__ float2 step[TILE][CW];   // d, d x
+    __shared__ float ysum[SUM ? 1 : TILE][CW];
+    __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
+    const Where w = where<N>(n_new, T_, C, G, blocks);
+    const R rows(w);
+    const Lane<N> lane(w);
+    const int seg = blockIdx.y;
+    const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
+    floatx4 A2 = lane.load(in.A), h = zero4();
+    A2 *= LOG2E;
+    if constexpr (!SUM)
+        h = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
+                        : lane.load(h_in ? h_in + (int64_t)w.b * C * N : nullptr);
+    float total = 0.f;
+    float bias[VN], skip[VN];
+    load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
+    load_floats<VN>(skip, in.D ? in.D + rows.c : nullptr, rows.nc);
+    u32x4 xv[PV], dv[PV], zv[PV];
+    Projections<T, N> proj;
+    auto fetch = [&](int t0) {
+        rows.load(xv, in.x, w.b, t0, end);
+        rows.load(dv, in.dt, w.b, t0, end);
+        if constexpr (!SUM)
+            if (in.z.ptr)
+                rows.load(zv, in.z, w.b, t0, end);
+        proj.load(in, w, t0);
+    };
+    if (begin < end)
+        fetch(begin);
+    for (int t0 = begin; t0 < end; t0 += TILE) {
+        u32x4 xc[PV], zc[PV];
+#pragma unroll
+        for (int i = 0; i < PV; ++i) {
+            xc[i] = xv[i];
+            zc[i] = zv[i];
+            const int r = rows.token(i);
+            if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT) {
+#pragma unroll
+                for (int j = 0; j < VN; ++j) {
+                    float d = vec_get<T>(dv[i], j) + bias[j], slope;
+                    if (in.softplus)
+                        d = softplus(d, slope);
+                    const bool there = t0 + r < end;   // a token that is not there leaves the state as it is
+                    step[r][rows.col() + j] = float2{there ? d : 0.f, there ? d * vec_get<T>(xv[i], j) : 0.f};
+                }
+            }
+        }
+        proj.store(bc);
+        if (t0 + TILE < end)
+            fetch(t0 + TILE);
+        __syncthreads();
+        float* sp = saved ? saved + ((int64_t)w.b * ((T_ + BLOCK - 1) / BLOCK) + t0 / BLOCK) * C * N : nullptr;
+#pragma unroll 8
+        for (int t = 0; t < TILE; ++t) {
+            if constexpr (!SUM)
+                if (sp && t % BLOCK == 0 && t0 + t < end)
+                    lane.store(sp + (int64_t)(t / BLOCK) * C * N, h);
+            const float2 s = step[t][lane.col];
+            const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][t][lane.q * NS]);
+            h = exp2_4(s.x * A2) * h + s.y * bv;
+            if constexpr (SUM) {
+                total += s.x;
+            } else {
+                const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][t][lane.q * NS]);
+                const float o = channel_sum<L>(dot4(cv, h));
+                if (lane.q == 0)
+                    ysum[t][lane.col] = o;
+            }
+        }
+        __syncthreads();
+        if constexpr (!SUM) {
+#pragma unroll
+            for (int i = 0; i < PV; ++i) {
+                const int r = rows.token(i);
+                if (t0 + r < end && rows.nc > 0) {
+                    float out[VN];
+#pragma unroll
+                    for (int j = 0; j < VN; ++j) {
+                        float o = __builtin_fmaf(skip[j], vec_get<T>(xc[i], j), ysum[r][rows.col() + j]);
+                        if (in.z.ptr) {
+                            const float z = vec_get<T>(zc[i], j);
+                            o *= z * sigmoid(z);
+                        }
+                        out[j] = o;
+                    }
+                    store_vec<OT, VN>(y.ptr + w.b * y.sb + (int64_t)(t0 + r) * y.st + rows.c, out, rows.nc);
+                }
+            }
+        }
+    }
+    if constexpr (SUM) {
+        const int64_t at = (int64_t)w.b * sg.nseg + seg;
+        lane.store(sg.state + at * C * N, h);
+        if (lane.ok && lane.q == 0)
+            sg.total[at * C + lane.c] = total;
+    } else if (seg == sg.nseg - 1) {
+        lane.store(h_out + (int64_t)w.b * C * N, h);
+    }
+}
+
+// The states that enter the segments (REVERSE: the gradients that enter them from
+// behind), in the place of what the segments make of zeros.
+template <bool REVERSE>
+__global__ __launch_bounds__(NT) void scan_fold_kernel(const float* A, const float* carry, Segments sg, int C, int N)
+{
+    const int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x, cn = (int64_t)C * N;
+    const int b = blockIdx.y;
+    if (i >= cn)
+        return;
+    const float A2 = A[i] * LOG2E;
+    float s = carry ? carry[b * cn + i] : 0.f;
+    for (int k = 0; k < sg.nseg; ++k) {
+        const int64_t at = (int64_t)b * sg.nseg + (REVERSE ? sg.nseg - 1 - k : k);
+        float* p = sg.state + at * cn + i;
+        if (k == sg.nseg - 1) {   // nothing asks what the last one makes of it
+            *p = s;
+            break;
+        }
+        const float own = *p, keep = __builtin_amdgcn_exp2f(sg.total[at * C + i / N] * A2);
+        *p = s;
+        s = __builtin_fmaf(keep, s, own);
+    }
+}
+
+// ---- backward ----------------------------------------------------------------
+
+template <typename OT>
+struct Grads {
+    Act<OT> dx, ddt, db, dc, dz;
+    float* dh_in;
+    float* params;   // [B * nseg][C N + 2 C]: dA, dD, ddt_bias of a workgroup
+    float* proj;     // [G * blocks][B][T][2 N]: db, dc of a workgroup's channels
+};
+
+// SUM: the gradient that a segment passes on of zeros behind it, and its sum of steps.
+template <typename T, typename OT, int N, bool SUM>
+__global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* saved, const int* n_new, Act<const T> dy,
+                                                      const float* dh_out, Grads<OT> out, Segments sg, int T_, int C, int G,
+                                                      int blocks)
+{
+    typedef Rows<T, N> R;
+    constexpr int CW = Geo<N>::CW, L = Geo<N>::L, VN = R::VN, PV = R::PV;
+    __shared__ floatx4 slot[TILE][CW];   // d, d x, e, c . h; then the sums of dd and of G b in the places of d and d x
+    __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
+    __shared__ __attribute__((aligned(16))) float part[SUM ? 1 : NT / 64][SUM ? 1 : TILE][SUM ? 4 : 2 * N];
+    const Where w = where<N>(n_new, T_, C, G, blocks);
+    const R rows(w);
+    const Lane<N> lane(w);
+    const int seg = blockIdx.y + (SUM ? 1 : 0);   // what the first segment passes on is not asked for
+    const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
+    const floatx4 A = lane.load(in.A), A2 = A * LOG2E;
+    floatx4 g = zero4(), dA = zero4();
+    if constexpr (!SUM)
+        g = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
+                        : lane.load(dh_out ? dh_out + (int64_t)w.b * C * N : nullptr);
+    float total = 0.f;
+    float bias[VN], skip[VN], dD[VN], dbias[VN];
+    load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
+    load_floats<VN>(skip, in.D ? in.D + rows.c : nullptr, rows.nc);
+#pragma unroll
+    for (int j = 0; j < VN; ++j)
+        dD[j] = dbias[j] = 0.f;
+    u32x4 xv[PV], dv[PV], zv[PV], gv[PV];
+    Projections<T, N> proj;
+    auto fetch = [&](int t0) {
+        rows.load(xv, in.x, w.b, t0, end);
+        rows.load(dv, in.dt, w.b, t0, end);
+        if (in.z.ptr)
+            rows.load(zv, in.z, w.b, t0, end);
+        rows.load(gv, dy, w.b, t0, end);
+        proj.load(in, w, t0);
+    };
+    const int last = begin + (end - 1 - begin) / TILE * TILE;
+    if (begin < end)
+        fetch(last);
+    for (int t0 = last; t0 >= begin && begin < end; t0 -= TILE) {
+        u32x4 xc[PV];
+        float dd[PV][VN], ee[PV][VN], ds[PV][VN], dg[PV][VN];   // step, e, slope of the step, dy times the slope of the gate
+#pragma unroll
+        for (int i = 0; i < PV; ++i) {
+            xc[i] = xv[i];
+            const int r = rows.token(i);
+            const bool there = t0 + r < end;
+#pragma unroll
+            for (int j = 0; j < VN; ++j) {
+                float d = vec_get<T>(dv[i], j) + bias[j];
+                ds[i][j] = 1.f;
+                if (in.softplus)
+                    d = softplus(d, ds[i][j]);
+                d = there ? d : 0.f;
+                float e = vec_get<T>(gv[i], j);
+                dg[i][j] = e;
+                if (in.z.ptr) {
+                    const float z = vec_get<T>(zv[i], j), q = sigmoid(z);
+                    dg[i][j] = e * __builtin_fmaf(z * q, 1.f - q, q);
+                    e *= z * q;
+                }
+                e = there ? e : 0.f;
+                dd[i][j] = d;
+                ee[i][j] = e;
+                if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT)
+                    slot[r][rows.col() + j] = floatx4{d, there ? d * vec_get<T>(xc[i], j) : 0.f, e, 0.f};
+            }
+        }
+        proj.store(bc);
+        if (t0 > begin)
+            fetch(t0 - TILE);
+        __syncthreads();
+        if constexpr (SUM) {
+#pragma unroll 8
+            for (int t = TILE - 1; t >= 0; --t) {
+                const floatx4 s = slot[t][lane.col];
+                const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][t][lane.q * NS]);
+                g = exp2_4(s[0] * A2) * (g + s[2] * cv);
+                total += s[0];
+            }
+        } else {
+            const float* sp = saved + ((int64_t)w.b * ((T_ + BLOCK - 1) / BLOCK) + t0 / BLOCK) * C * N;
+            for (int k = TILE / BLOCK - 1; k >= 0; --k) {
+                const int tk = k * BLOCK;
+                if (t0 + tk >= end)   // nothing there
+                    continue;
+                const floatx4 h0 = lane.load(sp + (int64_t)k * C * N);
+                floatx4 h = h0, hs[BLOCK], as[BLOCK];
+#pragma unroll
+                for (int t = 0; t < BLOCK; ++t) {
+                    const floatx4 s = slot[tk + t][lane.col];
+                    const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
+                    as[t] = exp2_4(s[0] * A2);
+                    hs[t] = h = as[t] * h + s[1] * bv;
+                }
+#pragma unroll
+                for (int t = BLOCK - 1; t >= 0; --t) {
+                    const floatx4 s = slot[tk + t][lane.col];
+                    const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
+                    const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][tk + t][lane.q * NS]);
+                    const floatx4 Gt = g + s[2] * cv;
+                    const float o = channel_sum<L>(dot4(cv, hs[t]));
+                    const float du = channel_sum<L>(dot4(Gt, bv));
+                    floatx4 pc = s[2] * hs[t], pb = s[1] * Gt;
+                    g = as[t] * Gt;
+                    const floatx4 qv = g * (t ? hs[t - 1] : h0);
+                    dA += s[0] * qv;
+                    const float da = channel_sum<L>(dot4(qv, A));
+                    if (lane.q == 0)
+                        slot[tk + t][lane.col] = floatx4{da, du, 0.f, o};
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        pb[j] = wave_sum<L>(pb[j]);
+                        pc[j] = wave_sum<L>(pc[j]);
+                    }
+                    if ((threadIdx.x & 63) < L) {
+                        float* p = &part[threadIdx.x >> 6][tk + t][lane.q * NS];
+                        *reinterpret_cast<floatx4*>(p) = pb;
+                        *reinterpret_cast<floatx4*>(p + N) = pc;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (!SUM) {
+            // db, dc of this workgroup's channels
+            float* pp = out.proj + (((int64_t)blockIdx.x * gridDim.z + w.b) * T_ + t0) * 2 * N;
+            for (int i = threadIdx.x; i < TILE * 2 * N; i += NT)
+                if (t0 + i / (2 * N) < end) {
+                    float s = part[0][i / (2 * N)][i % (2 * N)];
+#pragma unroll
+                    for (int k = 1; k < NT / 64; ++k)
+                        s += part[k][i / (2 * N)][i % (2 * N)];
+                    pp[i] = s;
+                }
+#pragma unroll
+            for (int i = 0; i < PV; ++i) {
+                const int r = rows.token(i);
+                if (t0 + r < end && rows.nc > 0) {
+                    float dx[VN], ddt[VN], dz[VN];
+#pragma unroll
+                    for (int j = 0; j < VN; ++j) {
+                        const floatx4 s = slot[r][rows.col() + j];
+                        const float x = vec_get<T>(xc[i], j);
+                        dx[j] = __builtin_fmaf(ee[i][j], skip[j], s[1] * dd[i][j]);
+                        ddt[j] = __builtin_fmaf(s[1], x, s[0]) * ds[i][j];
+                        dz[j] = dg[i][j] * __builtin_fmaf(skip[j], x, s[3]);
+                        dD[j] = __builtin_fmaf(ee[i][j], x, dD[j]);
+                        dbias[j] += ddt[j];
+                    }
+                    const int64_t t = t0 + r;
+                    store_vec<OT, VN>(out.dx.ptr + w.b * out.dx.sb + t * out.dx.st + rows.c, dx, rows.nc);
+                    store_vec<OT, VN>(out.ddt.ptr + w.b * out.ddt.sb + t * out.ddt.st + rows.c, ddt, rows.nc);
+                    if (in.z.ptr)
+                        store_vec<OT, VN>(out.dz.ptr + w.b * out.dz.sb + t * out.dz.st + rows.c, dz, rows.nc);
+                }
+            }
+            __syncthreads();   // before the next tile's values
+        }
+    }
+    if constexpr (SUM) {
+        const int64_t at = (int64_t)w.b * sg.nseg + seg;
+        lane.store(sg.state + at * C * N, g);
+        if (lane.ok && lane.q == 0)
+            sg.total[at * C + lane.c] = total;
+    } else {
+        if (seg == 0)
+            lane.store(out.dh_in + (int64_t)w.b * C * N, g);
+        float* pp = out.params + ((int64_t)w.b * sg.nseg + seg) * ((int64_t)C * N + 2 * C);
+        lane.store(pp, dA);
+        // dD and ddt_bias over the rows of a channel
+        constexpr int ROWS = R::COUNT < NT ? TILE : NT / R::VPR;
+        float* red = reinterpret_cast<float*>(slot);   // [2][ROWS][CW]
+        static_assert(2 * ROWS <= 4 * TILE, "the sums fit the slots");
+        __syncthreads();
+        if ((int)threadIdx.x < R::COUNT)
+#pragma unroll
+            for (int j = 0; j < VN; ++j) {
+                red[rows.row * CW + rows.col() + j] = dD[j];
+                red[(ROWS + rows.row) * CW + rows.col() + j] = dbias[j];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * CW; i += NT)
+            if (w.c0 + i % CW < w.cend) {
+                float s = 0.f;
+                for (int r = 0; r < ROWS; ++r)
+                    s += red[((i / CW) * ROWS + r) * CW + i % CW];
+                pp[(int64_t)C * N + (i / CW) * C + w.c0 + i % CW] = s;
+            }
+    }
+}
+
+// dA, dD and ddt_bias from the workgroups' sums: 64 columns and 16 slices of the
+// sums a workgroup.
+__global__ __launch_bounds__(1024) void scan_params_kernel(const float* part, int parts, float* dA, float* dD, float* dbias,
+                                                           int64_t cn, int C)
+{
+    __shared__ float sums[16][64];
+    const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    const int64_t i = blockIdx.x * 64ll + col, ld = cn + 2 * C;
+    float s = 0.f;
+    if (i < ld)
+#pragma unroll 8
+        for (int q = slice; q < parts; q += 16)
+            s += part[q * ld + i];
+    sums[slice][col] = s;
+    __syncthreads();
+    if (slice == 0 && i < ld) {
+        for (int q = 1; q < 16; ++q)
+            s += sums[q][col];
+        if (i < cn)
+            dA[i] = s;
+        else if (i < cn + C) {
+            if (dD)
+                dD[i - cn] = s;
+        } else if (dbias) {
+            dbias[i - cn - C] = s;
+        }
+    }
+}
+
+// db and dc over the workgroups of a group's channels, 4 values a thread.
+template <typename OT, int N>
+__global__ __launch_bounds__(NT) void scan_proj_kernel(const float* part, const int* n_new, Act<OT> db, Act<OT> dc, int B,
+                                                       int T_, int blocks)
+{
+    const int b = blockIdx.z, g = blockIdx.y, n = n_new ? min(max(n_new[b], 0), T_) : T_;
+    const int64_t count = (int64_t)n * (2 * N / 4), ld = (int64_t)B * T_ * 2 * N;
+    for (int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x; i < count; i += (int64_t)gridDim.x * NT) {
+        const float* p = part + ((int64_t)g * blocks * B + b) * T_ * 2 * N + i * 4;
+        floatx4 s = zero4();
+#pragma unroll 4
+        for (int k = 0; k < blocks; ++k)
+            s += *reinterpret_cast<const floatx4*>(p + k * ld);
+        const int64_t t = i / (2 * N / 4);
+        const int at = (int)(i % (2 * N / 4)) * 4;
+        const Act<OT>& o = at < N ? db : dc;
+        const float v[4] = {s[0], s[1], s[2], s[3]};
+        store_vec<OT, 4>(o.head(b, g) + t * o.st + at % N, v, 4);
+    }
+}
+
+// ---- token step --------------------------------------------------------------
+
+template <typename T, typename OT, int N>
+__global__ __launch_bounds__(NT) void scan_step_kernel(In<T> in, float* S, const int* slots, int nslots, Act<OT> y, int T_,
+                                                       int C, int G)
+{
+    constexpr int CW = Geo<N>::CW, L = Geo<N>::L;
+    const Where w{(int)blockIdx.y, 0, (int)blockIdx.x * CW, C, T_};
+    const Lane<N> lane(w);
+    int slot = w.b;
+    OT* yp = y.ptr + w.b * y.sb + lane.c;
+    if (slots) {
+        slot = slots[w.b];
+        int skip = slot < 0 || slot >= nslots;
+        for (int i = threadIdx.x; i < w.b; i += NT)
+            skip |= slots[i] == slot;
+        if (__syncthreads_or(skip)) {
+            if (lane.ok && lane.q == 0)
+                for (int t = 0; t < T_; ++t)
+                    yp[(int64_t)t * y.st] = (OT)0.f;
+            return;
+        }
+    }
+    if (!lane.ok)
+        return;
+    const int g = lane.c / (C / G);
+    floatx4* Sp = reinterpret_cast<floatx4*>(S + ((int64_t)slot * C + lane.c) * N + lane.q * NS);
+    floatx4 h = *Sp;
+    const floatx4 A2 = lane.load(in.A) * LOG2E;
+    const float bias = in.dt_bias ? in.dt_bias[lane.c] : 0.f, skip = in.D ? in.D[lane.c] : 0.f;
+    const T* bp = in.b.head(w.b, g) + lane.q * NS;
+    const T* cp = in.c.head(w.b, g) + lane.q * NS;
+    for (int t = 0; t < T_; ++t) {
+        const float x = (float)in.x.ptr[w.b * in.x.sb + (int64_t)t * in.x.st + lane.c];
+        float d = (float)in.dt.ptr[w.b * in.dt.sb + (int64_t)t * in.dt.st + lane.c] + bias, slope;
+        if (in.softplus)
+            d = softplus(d, slope);
+        floatx4 bv, cv;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            bv[j] = (float)bp[(int64_t)t * in.b.st + j];
+            cv[j] = (float)cp[(int64_t)t * in.c.st + j];
+        }
+        h = exp2_4(d * A2) * h + (d * x) * bv;
+        float o = __builtin_fmaf(skip, x, channel_sum<L>(dot4(cv, h)));
+        if (in.z.ptr) {
+            const float z = (float)in.z.ptr[w.b * in.z.sb + (int64_t)t * in.z.st + lane.c];
+            o *= z * sigmoid(z);
+        }
+        if (lane.q == 0)
+            yp[(int64_t)t * y.st] = (OT)o;
+    }
+    *Sp = h;
+}
+
+// ---- host --------------------------------------------------------------------
+
+int channels_per_block(int N) { return NT / 64 * 64 / (N / NS); }
+
+// How a piece is split: `blocks` workgroups over the channels of a group, nseg
+// segments of seg tokens.
+struct Plan {
+    int blocks, nseg, seg;
+    Plan(const linrec_scan_desc* d)
+    {
+        const int cw = channels_per_block(d->N);
+        blocks = (d->C / d->G + cw - 1) / cw;
+        const int64_t wgs = (int64_t)blocks * d->G * d->B;
+        const int64_t want = wgs >= 256 ? 1 : std::min<int64_t>((511 + wgs) / wgs, (d->T + 127) / 128);
+        const int64_t len = (d->T + want - 1) / want;
+        seg = (int)((len + TILE - 1) / TILE * TILE);
+        nseg = (int)((d->T + (int64_t)seg - 1) / seg);
+    }
+};
+
+linrec_status check_scan_desc(const linrec_scan_desc* d)
+{
+    if (!d)
+        return LINREC_E_NULL;
+    if ((d->dtype != LINREC_BF16 && d->dtype != LINREC_F32) ||
+        (d->out_dtype != LINREC_BF16 && d->out_dtype != LINREC_F32) ||
+        (d->dtype == LINREC_F32 && d->out_dtype != LINREC_F32))
+        return LINREC_E_DTYPE;
+    if (d->B < 1 || d->B > 32767 || d->C < 1 || d->C > (1 << 20) || d->T < 0 || d->T > LINREC_MAX_T)
+        return LINREC_E_SHAPE;
+    if (d->N != 8 && d->N != 16 && d->N != 32 && d->N != 64)
+        return LINREC_E_SHAPE;
+    if (d->G < 1 || d->G > 65535 || d->C % d->G || (d->G > 1 && (d->C / d->G * elem_size(d->dtype)) % 16))
+        return LINREC_E_SHAPE;
+    if (d->softplus != 0 && d->softplus != 1)
+        return LINREC_E_LAYOUT;
+    return LINREC_OK;
+}
+
+linrec_status check_rows(const linrec_scan_desc* d, const linrec_tensor& t, int dtype, bool out)
+{
+    return check_view(linrec_tensor{t.ptr, t.sb, 0, t.st}, d->B, 1, d->T, d->C, elem_size(dtype), out);
+}
+
+linrec_status check_proj(const linrec_scan_desc* d, const linrec_tensor& t, int dtype, bool out)
+{
+    return check_view(t, d->B, d->G, d->T, d->N, elem_size(dtype), out);
+}
+
+linrec_status check_inputs(const linrec_scan_desc* d, const linrec_scan_inputs* in)
+{
+    linrec_status st;
+    if (!in)
+        return LINREC_E_NULL;
+    if ((st = check_rows(d, in->x, d->dtype, false)) != LINREC_OK || (st = check_rows(d, in->dt, d->dtype, false)) != LINREC_OK ||
+        (st = check_proj(d, in->b, d->dtype, false)) != LINREC_OK || (st = check_proj(d, in->c, d->dtype, false)) != LINREC_OK ||
+        (in->z.ptr && (st = check_rows(d, in->z, d->dtype, false)) != LINREC_OK) ||
+        (st = check_state_ptr(in->A, true)) != LINREC_OK || (st = check_state_ptr(in->D, false)) != LINREC_OK ||
+        (st = check_state_ptr(in->dt_bias, false)) != LINREC_OK)
+        return st;
+    return LINREC_OK;
+}
+
+template <typename T>
+Act<const T> chead(const linrec_tensor& a) { return Act<const T>{(const T*)a.ptr, a.sb, a.sh, a.st}; }
+template <typename T>
+Act<T> mhead(const linrec_tensor& a) { return Act<T>{(T*)a.ptr, a.sb, a.sh, a.st}; }
+
+template <typename T>
+In<T> inputs(const linrec_scan_desc* d, const linrec_scan_inputs* in)
+{
+    return In<T>{cact<T>(in->x), cact<T>(in->dt), chead<T>(in->b), chead<T>(in->c), cact<T>(in->z),
+                 in->A, in->D, in->dt_bias, d->softplus};
+}
+
+// Calls f with (input type, output type, states) of the description.
+template <typename F>
+hipError_t dispatch(const linrec_scan_desc* d, F&& f)
+{
+    auto states = [&](auto t, auto o) {
+        switch (d->N) {
+        case 8: return f(t, o, std::integral_constant<int, 8>{});
+        case 16: return f(t, o, std::integral_constant<int, 16>{});
+        case 32: return f(t, o, std::integral_constant<int, 32>{});
+        default: return f(t, o, std::integral_constant<int, 64>{});
+        }
+    };
+    if (d->dtype == LINREC_F32)
+        return states(float{}, float{});
+    return d->out_dtype == LINREC_F32 ? states(bf16{}, float{}) : states(bf16{}, bf16{});
+}
+
+int64_t round4(int64_t n) { return (n + 3) / 4 * 4; }
+
+int64_t state_floats(const linrec_scan_desc* d) { return (int64_t)d->B * d->C * d->N; }
+
+// The segments' part of a workspace.
+int64_t segment_floats(const linrec_scan_desc* d, const Plan& p)
+{
+    return p.nseg > 1 ? p.nseg * state_floats(d) + round4((int64_t)d->B * p.nseg * d->C) : 0;
+}
+
+Segments segments(const linrec_scan_desc* d, const Plan& p, void* workspace)
+{
+    float* w = (float*)workspace;
+    return p.nseg > 1 ? Segments{p.nseg, p.seg, w, w + p.nseg * state_floats(d)} : Segments{1, p.seg, nullptr, nullptr};
+}
+
+int64_t params_floats(const linrec_scan_desc* d, const Plan& p)
+{
+    return round4((int64_t)d->B * p.nseg * ((int64_t)d->C * d->N + 2 * d->C));
+}
+
+linrec_status pass(const linrec_scan_desc* d, const float* in, float* out, hipStream_t s)
+{
+    if (in == out)
+        return LINREC_OK;
+    LAUNCH(launch_carry_copy(in, out, state_floats(d), s));
+    return LINREC_OK;
+}
+
+}  // namespace
+}  // namespace linrec
+
+using namespace linrec;
+
+extern "C" {
+
+size_t linrec_scan_saved_bytes(const linrec_scan_desc* d)
+{
+    if (check_scan_desc(d) != LINREC_OK)
+        return 0;
+    return (size_t)(((int64_t)d->T + BLOCK - 1) / BLOCK) * (size_t)state_floats(d) * sizeof(float);
+}
+
+size_t linrec_scan_fwd_workspace_bytes(const linrec_scan_desc* d)
+{
+    if (check_scan_desc(d) != LINREC_OK || d->T == 0)
+        return 0;
+    return (size_t)segment_floats(d, Plan(d)) * sizeof(float);
+}
+
+size_t linrec_scan_bwd_workspace_bytes(const linrec_scan_desc* d)
+{
+    if (check_scan_desc(d) != LINREC_OK || d->T == 0)
+        return 0;
+    const Plan p(d);
+    return (size_t)(segment_floats(d, p) + params_floats(d, p) + (int64_t)d->G * p.blocks * d->B * d->T * 2 * d->N) *
+           sizeof(float);
+}
+
+linrec_status linrec_scan_fwd(linrec_ctx* ctx, const linrec_scan_desc* d, const linrec_scan_inputs* in, const float* h_in,
+                              const int32_t* n_new, linrec_tensor y, float* h_out, void* saved, void* workspace, void* stream)
+{
+    linrec_status st;
+    if ((st = check_scan_desc(d)) != LINREC_OK || (st = check_state_ptr(h_in, false)) != LINREC_OK ||
+        (st = check_state_ptr(h_out, true)) != LINREC_OK)
+        return st;
+    if (d->T > 0) {
+        if ((st = check_inputs(d, in)) != LINREC_OK || (st = check_rows(d, y, d->out_dtype, true)) != LINREC_OK)
+            return st;
+        if (!aligned(n_new, 4))
+            return LINREC_E_ALIGN;
+        if ((saved && (st = check_buffer(saved)) != LINREC_OK) ||
+            (linrec_scan_fwd_workspace_bytes(d) && (st = check_buffer(workspace)) != LINREC_OK))
+            return st;
+    }
+    if ((st = check_ctx(ctx)) != LINREC_OK)
+        return st;
+    hipStream_t s = (hipStream_t)stream;
+    if (d->T == 0)
+        return pass(d, h_in, h_out, s);
+    LAUNCH(timed_launch(ctx, LINREC_KERNEL_SCAN_FWD, s, [&] {
+        return dispatch(d, [&](auto t, auto o, auto n) {
+            using T = decltype(t);
+            using OT = decltype(o);
+            constexpr int N = decltype(n)::value;
+            const Plan p(d);
+            const Segments sg = segments(d, p, workspace);
+            const In<T> a = inputs<T>(d, in);
+            const unsigned wgs = (unsigned)p.blocks * d->G;
+            if (p.nseg > 1) {
+                launch_kernel(scan_fwd_kernel<T, OT, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, h_in, n_new,
+                              mact<OT>(y), h_out, (float*)nullptr, sg, d->T, d->C, d->G, p.blocks);
+                launch_kernel(scan_fold_kernel<false>, dim3((unsigned)(((int64_t)d->C * N + NT - 1) / NT), d->B), dim3(NT), s,
+                              in->A, h_in, sg, d->C, N);
+            }
+            launch_kernel(scan_fwd_kernel<T, OT, N, false>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, h_in, n_new, mact<OT>(y),
+                          h_out, (float*)saved, sg, d->T, d->C, d->G, p.blocks);
+            return hipGetLastError();
+        });
+    }));
+    return LINREC_OK;
+}
+
+linrec_status linrec_scan_bwd(linrec_ctx* ctx, const linrec_scan_desc* d, const linrec_scan_inputs* in, const void* saved,
+                              const int32_t* n_new, linrec_tensor dy, const float* dh_out, const linrec_scan_grads* out,
+                              void* workspace, void* stream)
+{
+    linrec_status st;
+    if ((st = check_scan_desc(d)) != LINREC_OK || (st = check_state_ptr(dh_out, false)) != LINREC_OK)
+        return st;
+    if (!out)
+        return LINREC_E_NULL;
+    if ((st = check_state_ptr(out->dh_in, true)) != LINREC_OK || (st = check_state_ptr(out->dA, true)) != LINREC_OK ||
+        (st = check_state_ptr(out->dD, false)) != LINREC_OK || (st = check_state_ptr(out->ddt_bias, false)) != LINREC_OK)
+        return st;
+    if (d->T > 0) {
+        if ((st = check_inputs(d, in)) != LINREC_OK || (st = check_rows(d, dy, d->dtype, false)) != LINREC_OK ||
+            (st = check_rows(d, out->dx, d->out_dtype, true)) != LINREC_OK ||
+            (st = check_rows(d, out->ddt, d->out_dtype, true)) != LINREC_OK ||
+            (st = check_proj(d, out->db, d->out_dtype, true)) != LINREC_OK ||
+            (st = check_proj(d, out->dc, d->out_dtype, true)) != LINREC_OK ||
+            (in->z.ptr && (st = check_rows(d, out->dz, d->out_dtype, true)) != LINREC_OK))
+            return st;
+        if (!aligned(n_new, 4))
+            return LINREC_E_ALIGN;
+        if ((st = check_buffer(saved)) != LINREC_OK || (st = check_buffer(workspace)) != LINREC_OK)
+            return st;
+    }
+    if ((st = check_ctx(ctx)) != LINREC_OK)
+        return st;
+    hipStream_t s = (hipStream_t)stream;
+    if (d->T == 0) {
+        LAUNCH(launch_carry_copy(nullptr, out->dA, (int64_t)d->C * d->N, s));
+        if (out->dD)
+            LAUNCH(launch_carry_copy(nullptr, out->dD, d->C, s));
+        if (out->ddt_bias)
+            LAUNCH(launch_carry_copy(nullptr, out->ddt_bias, d->C, s));
+        return pass(d, dh_out, out->dh_in, s);
+    }
+    LAUNCH(timed_launch(ctx, LINREC_KERNEL_SCAN_BWD, s, [&] {
+        return dispatch(d, [&](auto t, auto o, auto n) {
+            using T = decltype(t);
+            using OT = decltype(o);
+            constexpr int N = decltype(n)::value;
+            const Plan p(d);
+            const Segments sg = segments(d, p, workspace);
+            const In<T> a = inputs<T>(d, in);
+            float* params = (float*)workspace + segment_floats(d, p);
+            const Grads<OT> gr{mact<OT>(out->dx), mact<OT>(out->ddt), mhead<OT>(out->db), mhead<OT>(out->dc),
+                               mact<OT>(out->dz), out->dh_in, params, params + params_floats(d, p)};
+            const unsigned wgs = (unsigned)p.blocks * d->G;
+            const int64_t cn = (int64_t)d->C * N;
+            if (p.nseg > 1) {
+                launch_kernel(scan_bwd_kernel<T, OT, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a,
+                              (const float*)nullptr, n_new, cact<T>(dy), dh_out, gr, sg, d->T, d->C, d->G, p.blocks);
+                launch_kernel(scan_fold_kernel<true>, dim3((unsigned)((cn + NT - 1) / NT), d->B), dim3(NT), s, in->A, dh_out,
+                              sg, d->C, N);
+            }
+            launch_kernel(scan_bwd_kernel<T, OT, N, false>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, (const float*)saved,
+                          n_new, cact<T>(dy), dh_out, gr, sg, d->T, d->C, d->G, p.blocks);
+            launch_kernel(scan_params_kernel, dim3((unsigned)((cn + 2 * d->C + 63) / 64)), dim3(1024), s, (const float*)gr.params,
+                          d->B * p.nseg, out->dA, out->dD, out->ddt_bias, cn, d->C);
+            const int64_t rounds = ((int64_t)d->T * (2 * N / 4) + NT - 1) / NT;
+            launch_kernel(scan_proj_kernel<OT, N>, dim3((unsigned)std::min<int64_t>(rounds, 4096), d->G, d->B), dim3(NT), s,
+                          (const float*)gr.proj, n_new, gr.db, gr.dc, d->B, d->T, p.blocks);
+            return hipGetLastError();
+        });
+    }));
+    return LINREC_OK;
+}
+
+linrec_status linrec_scan_step(linrec_ctx* ctx, const linrec_scan_desc* d, const linrec_scan_inputs* in, float* S,
+                               const int32_t* slots, int32_t nslots, linrec_tensor y, void* stream)
+{
+    linrec_status st;
+    if ((st = check_scan_desc(d)) != LINREC_OK)
+        return st;
+    if (d->T > 0) {
+        if (!S)
+            return LINREC_E_NULL;
+        if (nslots < 1 || (!slots && nslots < d->B))
+            return LINREC_E_SHAPE;
+        if ((st = check_inputs(d, in)) != LINREC_OK || (st = check_rows(d, y, d->out_dtype, true)) != LINREC_OK)
+            return st;
+        if (!aligned(S, 16) || !aligned(slots, 4))
+            return LINREC_E_ALIGN;
+    }
+    if ((st = check_ctx(ctx)) != LINREC_OK)
+        return st;
+    if (d->T == 0)
+        return LINREC_OK;
+    hipStream_t s = (hipStream_t)stream;
+    LAUNCH(timed_launch(ctx, LINREC_KERNEL_SCAN_STEP, s, [&] {
+        return dispatch(d, [&](auto t, auto o, auto n) {
+            using T = decltype(t);
+            using OT = decltype(o);
+            constexpr int N = decltype(n)::value;
+            launch_kernel(scan_step_kernel<T, OT, N>, dim3((d->C + Geo<N>::CW - 1) / Geo<N>::CW, d->B), dim3(NT), s,
+                          inputs<T>(d, in), S, slots, nslots, mact<OT>(y), d->T, d->C, d->G);
+            return hipGetLastError();
+        });
+    }));
+    return LINREC_OK;
+}
+
+}  // extern "C"

@@ -52,14 +52,20 @@ EXPORTS = (
     "linrec_diag_states_bytes", "linrec_diag_workspace_bytes", "linrec_diag_fwd", "linrec_diag_bwd",
     "linrec_step", "linrec_kv_append_workspace_bytes", "linrec_kv_append",
     "linrec_kv_attn_workspace_bytes", "linrec_kv_attn",
+    "linrec_conv_fwd", "linrec_conv_bwd_workspace_bytes", "linrec_conv_bwd", "linrec_conv_step",
+    "linrec_scan_saved_bytes", "linrec_scan_fwd_workspace_bytes", "linrec_scan_bwd_workspace_bytes",
+    "linrec_scan_fwd", "linrec_scan_bwd", "linrec_scan_step",
 )
 
 KERNEL_KINDS = {0: "fwd_sum", 1: "fwd_fold", 2: "fwd_seg", 3: "bwd_sum", 4: "bwd_fold",
                 5: "bwd_seg", 6: "da_finish", 7: "delta_fwd", 8: "delta_bwd", 9: "diag_fwd",
-                10: "diag_bwd", 11: "step", 12: "kv_append", 13: "kv_attn"}
+                10: "diag_bwd", 11: "step", 12: "kv_append", 13: "kv_attn", 14: "conv_fwd",
+                15: "conv_bwd", 16: "conv_step", 17: "scan_fwd", 18: "scan_bwd", 19: "scan_step"}
 
 # Forms of the elementwise recurrence (linrec_diag_form).
 DIAG_FORMS = {"plain": 0, "mix": 1}
+# Activations of the causal convolution (linrec_act).
+ACTS = {None: 0, "silu": 1}
 
 
 class LinrecError(RuntimeError):
@@ -87,6 +93,28 @@ class DiagDesc(ctypes.Structure):
                 ("form", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
+class ConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("G", ctypes.c_int32), ("softplus", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class ScanInputs(ctypes.Structure):
+    _fields_ = [("x", Tensor), ("dt", Tensor), ("b", Tensor), ("c", Tensor), ("z", Tensor),
+                ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class ScanGradsDesc(ctypes.Structure):
+    _fields_ = [("dx", Tensor), ("ddt", Tensor), ("db", Tensor), ("dc", Tensor), ("dz", Tensor),
+                ("dA", ctypes.c_void_p), ("dD", ctypes.c_void_p), ("ddt_bias", ctypes.c_void_p),
+                ("dh_in", ctypes.c_void_p)]
+
+
 class KvCacheDesc(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
@@ -107,6 +135,7 @@ def _lib():
     lib = ctypes.CDLL(LIB_PATH)
     P, T, D = ctypes.c_void_p, Tensor, ctypes.POINTER(Desc)
     I32, DD, KC = ctypes.c_int32, ctypes.POINTER(DiagDesc), ctypes.POINTER(KvCacheDesc)
+    CD, SD, SI = ctypes.POINTER(ConvDesc), ctypes.POINTER(ScanDesc), ctypes.POINTER(ScanInputs)
     sig = {
         "linrec_ctx_create": ([ctypes.POINTER(P), ctypes.c_int], ctypes.c_int),
         "linrec_ctx_destroy": ([P], ctypes.c_int),
@@ -144,6 +173,16 @@ def _lib():
         "linrec_kv_attn_workspace_bytes": ([KC, I32, I32, I32], ctypes.c_size_t),
         "linrec_kv_attn": ([P, KC, I32, I32, I32, T, P, P, ctypes.c_float, I32, T, P, P, P],
                            ctypes.c_int),
+        "linrec_conv_fwd": ([P, CD, T, P, P, P, P, T, P, P], ctypes.c_int),
+        "linrec_conv_bwd_workspace_bytes": ([CD], ctypes.c_size_t),
+        "linrec_conv_bwd": ([P, CD, T, P, P, P, P, T, P, T, P, P, P, P, P], ctypes.c_int),
+        "linrec_conv_step": ([P, CD, T, P, P, P, P, I32, T, P], ctypes.c_int),
+        "linrec_scan_saved_bytes": ([SD], ctypes.c_size_t),
+        "linrec_scan_fwd_workspace_bytes": ([SD], ctypes.c_size_t),
+        "linrec_scan_bwd_workspace_bytes": ([SD], ctypes.c_size_t),
+        "linrec_scan_fwd": ([P, SD, SI, P, P, T, P, P, P, P], ctypes.c_int),
+        "linrec_scan_bwd": ([P, SD, SI, P, P, T, P, ctypes.POINTER(ScanGradsDesc), P, P], ctypes.c_int),
+        "linrec_scan_step": ([P, SD, SI, P, P, I32, T, P], ctypes.c_int),
         "linrec_status_str": ([ctypes.c_int], ctypes.c_char_p),
         "linrec_last_hip_error": ([], ctypes.c_int),
         "linrec_version": ([], ctypes.c_int),
@@ -1023,6 +1062,308 @@ def diag_bwd(g, x, states, dh, dh_out=None, *, form="plain", dg=None, dx=None, d
                                 dga, dxa, in_ptr, _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_diag_bwd")
     return dg, dx, dh_in
+
+
+# ----------------------------------------------------------------- state-space layer
+
+def _out_code(dt, out_dtype, *outs):
+    """The output type of a call and its code: of the given outputs, else out_dtype, else dt."""
+    odt = dt if out_dtype is None else out_dtype
+    given = [t.dtype for t in outs if isinstance(t, torch.Tensor)]
+    if given:
+        odt = given[0]
+        if len(set(given)) > 1:
+            _fail(f"outputs must share one dtype, got {sorted(map(str, set(given)))}", TypeError)
+    code = _CODE.get(odt)
+    if code is None:
+        _fail(f"unsupported output dtype {odt}", TypeError)
+    return odt, code
+
+
+def _new_rows_of(like, dtype, ragged):
+    """A new [B,T,C] output as _new_rows; zeros where rows may not be written."""
+    t = _new_rows(like, dtype)
+    return t.zero_() if ragged else t
+
+
+def _conv_setup(x, w, bias, act, out_dtype, *outs):
+    """The shape, description and output type of a convolution, with its parameters' addresses."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        _fail("x: must be a [B,T,C] tensor")
+    code = _CODE.get(x.dtype)
+    if code is None:
+        _fail(f"unsupported activation dtype {x.dtype}", TypeError)
+    kind = ACTS.get(act)
+    if kind is None:
+        _fail(f"act: {act!r} is none of {list(ACTS)}")
+    odt, out = _out_code(x.dtype, out_dtype, *outs)
+    B, T, C = shape = x.shape
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        _fail("w: must be a float32 [C,K] tensor")
+    K = w.shape[1]
+    if (B | T | C | K) >> 31:
+        _too_large(B, T, C, K)
+    w_ptr = _state_ptr("w", w, (C, K))
+    return shape, ConvDesc(B, T, C, K, kind, code, out), odt, w_ptr, _state_ptr("bias", bias, (C,))
+
+
+def conv_fwd(x, w, bias=None, state_in=None, *, act="silu", n_new=None, y=None, state_out=None,
+             out_dtype=None):
+    """Short causal convolution over one piece (linrec_conv_fwd):
+    y_t = act(bias + sum_k w[:,k] x_{t-K+1+k}) per channel; x: [B,T,C]; w: fp32
+    [C,K], K = 2, 3 or 4; bias: fp32 [C] or None; act: "silu" or None; state_in,
+    state_out: fp32 [B,K-1,C], the K-1 inputs before the piece and its last ones.
+    n_new: int32 [B] on the device, the first n_new[b] tokens are there (rows
+    behind them are left as they were, zeros in a new y).  Returns (y, state_out)."""
+    shape, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, y)
+    carry = (shape[0], d.K - 1, shape[2])
+    xa = _arg3("x", x, shape, x.dtype)
+    ya = None if y is None else _arg3("y", y, shape, odt)
+    in_ptr, out_ptr = _state_ptr("state_in", state_in, carry), _state_ptr("state_out", state_out, carry)
+    n_ptr = _int_ptr("n_new", n_new, (shape[0],))
+    dev = _same_device(x, ("w", w), ("bias", bias), ("state_in", state_in), ("n_new", n_new), ("y", y),
+                       ("state_out", state_out))
+    if y is None:
+        y = _new_rows_of(x, odt, n_new is not None)
+        ya = _arg3("y", y, shape, odt)
+    if state_out is None:
+        state_out = torch.empty(carry, dtype=torch.float32, device=x.device)
+        out_ptr = state_out.data_ptr()
+    rc = _lib().linrec_conv_fwd(context(dev), ctypes.byref(d), xa, w_ptr, b_ptr, in_ptr, n_ptr, ya, out_ptr,
+                                _raw_stream(dev))
+    _check(rc, "linrec_conv_fwd")
+    return y, state_out
+
+
+def conv_bwd(x, w, bias, state_in, dy, dstate_out=None, *, act="silu", n_new=None, dx=None, dw=None,
+             dbias=None, dstate_in=None, workspace=None, out_dtype=None):
+    """Backward of conv_fwd over one piece (linrec_conv_bwd), for the loss
+    <dy, y> + <dstate_out, state_out>.  Returns (dx, dw, dbias, dstate_in);
+    dbias is None without a bias.  dw and dbias are this piece's alone."""
+    shape, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, dx)
+    C, K = shape[2], d.K
+    carry = (shape[0], K - 1, C)
+    xa, da = _arg3("x", x, shape, x.dtype), _arg3("dy", dy, shape, x.dtype)
+    dxa = None if dx is None else _arg3("dx", dx, shape, odt)
+    in_ptr, dout_ptr = _state_ptr("state_in", state_in, carry), _state_ptr("dstate_out", dstate_out, carry)
+    din_ptr = _state_ptr("dstate_in", dstate_in, carry)
+    dw_ptr, db_ptr = _state_ptr("dw", dw, (C, K)), _state_ptr("dbias", dbias, (C,))
+    n_ptr = _int_ptr("n_new", n_new, (shape[0],))
+    need = int(_lib().linrec_conv_bwd_workspace_bytes(ctypes.byref(d)))
+    if workspace is not None:
+        _check_buffer("workspace", workspace, need)
+    dev = _same_device(x, ("w", w), ("bias", bias), ("state_in", state_in), ("n_new", n_new), ("dy", dy),
+                       ("dstate_out", dstate_out), ("dx", dx), ("dw", dw), ("dbias", dbias),
+                       ("dstate_in", dstate_in), ("workspace", workspace))
+    if dx is None:
+        dx = _new_rows_of(x, odt, n_new is not None)
+        dxa = _arg3("dx", dx, shape, odt)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    if dw is None:
+        dw = torch.empty(C, K, **f32)
+        dw_ptr = dw.data_ptr()
+    if dbias is None and bias is not None:
+        dbias = torch.empty(C, **f32)
+        db_ptr = dbias.data_ptr()
+    if dstate_in is None:
+        dstate_in = torch.empty(carry, **f32)
+        din_ptr = dstate_in.data_ptr()
+    if workspace is None and need:
+        workspace = _bytes(need, x)
+    rc = _lib().linrec_conv_bwd(context(dev), ctypes.byref(d), xa, w_ptr, b_ptr, in_ptr, n_ptr, da, dout_ptr, dxa,
+                                dw_ptr, db_ptr, din_ptr, _ptr(workspace), _raw_stream(dev))
+    _check(rc, "linrec_conv_bwd")
+    return dx, dw, dbias, dstate_in
+
+
+def _pool(name, S, rest, B, slots):
+    """The address and size of a pool of fp32 states [n, *rest]."""
+    if not isinstance(S, torch.Tensor) or S.dim() != 1 + len(rest):
+        _fail(f"{name}: must be a float32 [n,{','.join(map(str, rest))}] tensor")
+    n = S.shape[0]
+    if n >> 31:
+        _too_large(n)
+    ptr = _state_ptr(name, S, (n, *rest))
+    if slots is None and n < B:
+        _fail(f"{name}: {n} states for {B} entries")
+    return ptr, n
+
+
+def conv_step(x, w, bias, S, *, act="silu", slots=None, y=None, out_dtype=None):
+    """One or a few tokens of conv_fwd (linrec_conv_step), the states updated in
+    place.  x: [B,T,C]; S: fp32 [n,K-1,C], entry b at slots[b] (int32 [B] on the
+    device) or at b.  An entry whose slot is outside the pool, or taken by an
+    earlier entry, is skipped (y = 0).  Returns y."""
+    shape, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, y)
+    B, T, C = shape
+    xa = _arg3("x", x, shape, x.dtype)
+    ya = None if y is None else _arg3("y", y, shape, odt)
+    S_ptr, n = _pool("S", S, (d.K - 1, C), B, slots)
+    slot_ptr = _int_ptr("slots", slots, (B,))
+    dev = _same_device(x, ("w", w), ("bias", bias), ("S", S), ("slots", slots), ("y", y))
+    if y is None:
+        y = _new_rows(x, odt)
+        ya = _arg3("y", y, shape, odt)
+    rc = _lib().linrec_conv_step(context(dev), ctypes.byref(d), xa, w_ptr, b_ptr, S_ptr, slot_ptr, n, ya,
+                                 _raw_stream(dev))
+    _check(rc, "linrec_conv_step")
+    return y
+
+
+def _scan_setup(x, dt, A, B, C, D, z, dt_bias, softplus, out_dtype, *outs):
+    """The shapes, description, inputs and output type of a scan."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        _fail("x: must be a [B,T,C] tensor")
+    t = x.dtype
+    code = _CODE.get(t)
+    if code is None:
+        _fail(f"unsupported activation dtype {t}", TypeError)
+    odt, out = _out_code(t, out_dtype, *outs)
+    n, T, ch = shape = x.shape
+    if not isinstance(B, torch.Tensor) or B.dim() != 4:
+        _fail("B: must be a [B,G,T,N] tensor")
+    G, N = B.shape[1], B.shape[3]
+    proj = (n, G, T, N)
+    if (n | T | ch | N | G) >> 31:
+        _too_large(n, T, ch, N, G)
+    if A is None:
+        _fail("A: expected a tensor", TypeError)
+    inputs = ScanInputs(_arg3("x", x, shape, t), _arg3("dt", dt, shape, t), _arg4("B", B, proj, t),
+                        _arg4("C", C, proj, t), _NONE if z is None else _arg3("z", z, shape, t),
+                        _state_ptr("A", A, (ch, N)), _state_ptr("D", D, (ch,)),
+                        _state_ptr("dt_bias", dt_bias, (ch,)))
+    return shape, proj, ScanDesc(n, T, ch, N, G, 1 if softplus else 0, code, out), inputs, odt
+
+
+def scan_saved_bytes(d: ScanDesc) -> int:
+    return int(_lib().linrec_scan_saved_bytes(ctypes.byref(d)))
+
+
+def scan_fwd(x, dt, A, B, C, h_in=None, *, D=None, z=None, dt_bias=None, softplus=True, n_new=None,
+             y=None, h_out=None, saved=None, save=False, workspace=None, out_dtype=None):
+    """Selective state-space scan over one piece (linrec_scan_fwd): with
+    d = softplus(dt + dt_bias) (softplus=False: dt + dt_bias),
+    h_t = exp(d_t A) h_{t-1} + d_t x_t B_t,  y_t = (C_t . h_t + D x_t) silu(z_t).
+    x, dt, z: [B,T,C]; A: fp32 [C,N]; B, C: [B,G,T,N], G groups of channels; D,
+    dt_bias: fp32 [C] or None; z: None means no gate; h_in, h_out: fp32 [B,C,N].
+    n_new: int32 [B] on the device, the first n_new[b] tokens are there (rows
+    behind them are left as they were, zeros in a new y).  With save=True (or a
+    `saved` buffer) the states that scan_bwd needs are kept.
+    Returns (y, h_out, saved or None)."""
+    shape, proj, d, inputs, odt = _scan_setup(x, dt, A, B, C, D, z, dt_bias, softplus, out_dtype, y)
+    carry = (shape[0], shape[2], proj[3])
+    ya = None if y is None else _arg3("y", y, shape, odt)
+    in_ptr, out_ptr = _state_ptr("h_in", h_in, carry), _state_ptr("h_out", h_out, carry)
+    n_ptr = _int_ptr("n_new", n_new, (shape[0],))
+    need = int(_lib().linrec_scan_fwd_workspace_bytes(ctypes.byref(d)))
+    if workspace is not None:
+        _check_buffer("workspace", workspace, need)
+    if saved is not None:
+        _check_buffer("saved", saved, scan_saved_bytes(d))
+    dev = _same_device(x, ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
+                       ("h_in", h_in), ("n_new", n_new), ("y", y), ("h_out", h_out), ("saved", saved),
+                       ("workspace", workspace))
+    if y is None:
+        y = _new_rows_of(x, odt, n_new is not None)
+        ya = _arg3("y", y, shape, odt)
+    if h_out is None:
+        h_out = torch.empty(carry, dtype=torch.float32, device=x.device)
+        out_ptr = h_out.data_ptr()
+    if saved is None and save:
+        saved = _bytes(max(scan_saved_bytes(d), 16), x)
+    if workspace is None and need:
+        workspace = _bytes(need, x)
+    rc = _lib().linrec_scan_fwd(context(dev), ctypes.byref(d), ctypes.byref(inputs), in_ptr, n_ptr, ya, out_ptr,
+                                _ptr(saved), _ptr(workspace), _raw_stream(dev))
+    _check(rc, "linrec_scan_fwd")
+    return y, h_out, saved
+
+
+class ScanGrads(NamedTuple):
+    """What scan_bwd returns; dD, dz and ddt_bias are None without D, z and dt_bias."""
+    dx: torch.Tensor
+    ddt: torch.Tensor
+    dA: torch.Tensor
+    dB: torch.Tensor
+    dC: torch.Tensor
+    dh_in: torch.Tensor
+    dD: Optional[torch.Tensor]
+    dz: Optional[torch.Tensor]
+    ddt_bias: Optional[torch.Tensor]
+
+
+def scan_bwd(x, dt, A, B, C, saved, dy, dh_out=None, *, D=None, z=None, dt_bias=None, softplus=True,
+             n_new=None, dx=None, ddt=None, dA=None, dB=None, dC=None, dh_in=None, dD=None, dz=None,
+             ddt_bias=None, workspace=None, out_dtype=None) -> ScanGrads:
+    """Backward of scan_fwd over one piece (linrec_scan_bwd), from its `saved`
+    buffer, for the loss <dy, y> + <dh_out, h_out>.  Gradients of parameters and
+    of B and C are sums over what shares them, of this piece alone."""
+    shape, proj, d, inputs, odt = _scan_setup(x, dt, A, B, C, D, z, dt_bias, softplus, out_dtype, dx, ddt, dB, dC, dz)
+    ch = shape[2]
+    carry = (shape[0], ch, proj[3])
+    da = _arg3("dy", dy, shape, x.dtype)
+    dout_ptr = _state_ptr("dh_out", dh_out, carry)
+    if dz is not None and z is None:
+        _fail("dz: there is no z")
+    n_ptr = _int_ptr("n_new", n_new, (shape[0],))
+    need = int(_lib().linrec_scan_bwd_workspace_bytes(ctypes.byref(d)))
+    _check_buffer("saved", saved, scan_saved_bytes(d))
+    if workspace is not None:
+        _check_buffer("workspace", workspace, need)
+    rows = {k: t if t is None else _arg3(k, t, shape, odt) for k, t in (("dx", dx), ("ddt", ddt), ("dz", dz))}
+    deep = {k: t if t is None else _arg4(k, t, proj, odt) for k, t in (("dB", dB), ("dC", dC))}
+    flat = {"dA": (dA, (ch, proj[3])), "dD": (dD, (ch,)), "ddt_bias": (ddt_bias, (ch,)), "dh_in": (dh_in, carry)}
+    for k, (t, s) in flat.items():
+        _state_ptr(k, t, s)
+    dev = _same_device(x, ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
+                       ("saved", saved), ("n_new", n_new), ("dy", dy), ("dh_out", dh_out), ("dx", dx), ("ddt", ddt),
+                       ("dB", dB), ("dC", dC), ("dz", dz), ("workspace", workspace),
+                       *((k, t) for k, (t, _) in flat.items()))
+    f32 = dict(dtype=torch.float32, device=x.device)
+    ragged = n_new is not None
+    dx = _new_rows_of(x, odt, ragged) if dx is None else dx
+    ddt = _new_rows_of(x, odt, ragged) if ddt is None else ddt
+    if z is not None and dz is None:
+        dz = _new_rows_of(x, odt, ragged)
+    new = torch.zeros if ragged else torch.empty
+    dB = new(proj, dtype=odt, device=x.device) if dB is None else dB
+    dC = new(proj, dtype=odt, device=x.device) if dC is None else dC
+    dA = torch.empty(ch, proj[3], **f32) if dA is None else dA
+    dh_in = torch.empty(carry, **f32) if dh_in is None else dh_in
+    if dD is None and D is not None:
+        dD = torch.empty(ch, **f32)
+    if ddt_bias is None and dt_bias is not None:
+        ddt_bias = torch.empty(ch, **f32)
+    if workspace is None and need:
+        workspace = _bytes(need, x)
+    out = ScanGradsDesc(rows["dx"] or _arg3("dx", dx, shape, odt), rows["ddt"] or _arg3("ddt", ddt, shape, odt),
+                        deep["dB"] or _arg4("dB", dB, proj, odt), deep["dC"] or _arg4("dC", dC, proj, odt),
+                        _NONE if dz is None else rows["dz"] or _arg3("dz", dz, shape, odt),
+                        _ptr(dA), _ptr(dD), _ptr(ddt_bias), _ptr(dh_in))
+    rc = _lib().linrec_scan_bwd(context(dev), ctypes.byref(d), ctypes.byref(inputs), _ptr(saved), n_ptr, da, dout_ptr,
+                                ctypes.byref(out), _ptr(workspace), _raw_stream(dev))
+    _check(rc, "linrec_scan_bwd")
+    return ScanGrads(dx, ddt, dA, dB, dC, dh_in, dD, dz, ddt_bias)
+
+
+def scan_step(x, dt, A, B, C, S, *, D=None, z=None, dt_bias=None, softplus=True, slots=None, y=None,
+              out_dtype=None):
+    """One or a few tokens of scan_fwd (linrec_scan_step), the states updated in
+    place.  S: fp32 [n,C,N], entry b at slots[b] (int32 [B] on the device) or at
+    b; slots as conv_step.  Returns y."""
+    shape, proj, d, inputs, odt = _scan_setup(x, dt, A, B, C, D, z, dt_bias, softplus, out_dtype, y)
+    ya = None if y is None else _arg3("y", y, shape, odt)
+    S_ptr, n = _pool("S", S, (shape[2], proj[3]), shape[0], slots)
+    slot_ptr = _int_ptr("slots", slots, (shape[0],))
+    dev = _same_device(x, ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
+                       ("S", S), ("slots", slots), ("y", y))
+    if y is None:
+        y = _new_rows(x, odt)
+        ya = _arg3("y", y, shape, odt)
+    rc = _lib().linrec_scan_step(context(dev), ctypes.byref(d), ctypes.byref(inputs), S_ptr, slot_ptr, n, ya,
+                                 _raw_stream(dev))
+    _check(rc, "linrec_scan_step")
+    return y
 
 
 # ----------------------------------------------------------------- generation
