@@ -77,6 +77,28 @@ __device__ __forceinline__ float softplus(float v, float& slope)
     return __builtin_fmaf(2.f * s, p, fmaxf(v, 0.f));
 }
 
+// The steps of a vector of channels (and their slopes).
+template <typename T, int VN>
+__device__ __forceinline__ void steps(float (&d)[VN], float (&slope)[VN], const u32x4& v, const float (&bias)[VN], int sp)
+{
+#pragma unroll
+    for (int j = 0; j < VN; ++j) {
+        d[j] = vec_get<T>(v, j) + bias[j];
+        slope[j] = 1.f;
+    }
+    if (sp)   // one branch for the vector: its channels' chains run side by side
+#pragma unroll
+        for (int j = 0; j < VN; ++j)
+            d[j] = softplus(d[j], slope[j]);
+}
+
+template <typename T, int VN>
+__device__ __forceinline__ void steps(float (&d)[VN], const u32x4& v, const float (&bias)[VN], int sp)
+{
+    float slope[VN];
+    steps<T, VN>(d, slope, v, bias, sp);
+}
+
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v)
 {
@@ -97,15 +119,85 @@ __device__ __forceinline__ float channel_sum(float v)
     return v;
 }
 
-// Sum over the channels of a wave (lanes L apart), in all of them.
+// Sums of 8 values of every lane over the channels of a wave (the lanes of one
+// state quad), left COUNT a lane: a step that adds lanes 32 or 16 apart adds two
+// values at once, one in each half of the lanes, so 8 values over 16 channels take
+// 17 instructions where adding them one by one takes 32.  r[i] is value of(i) of
+// the lane's quad.
 template <int L>
-__device__ __forceinline__ float wave_sum(float v)
-{
-#pragma unroll
-    for (int off = L; off < 64; off <<= 1)
-        v += __shfl_xor(v, off, 64);
-    return v;
-}
+struct WaveSums {
+    static constexpr int COUNT = L == 16 ? 2 : 1;
+    static __device__ __forceinline__ int of(int i)
+    {
+        const int lane = threadIdx.x & 63, row = lane >> 4;
+        const int half = L == 16 ? i : (lane >> 3) & 1;
+        return 4 * half + 2 * (row & 1) + (row >> 1);
+    }
+    static __device__ __forceinline__ float halves(float a, float b)   // a in lanes 0-31, b in 32-63
+    {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    static __device__ __forceinline__ float rows(float a, float b)     // a in even rows of 16, b in odd
+    {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    static __device__ __forceinline__ float row(float a)   // over the channels of a row
+    {
+        a = dpp_add<0x128>(a);                             // lanes 8 apart
+        if constexpr (L <= 4)
+            a = dpp_add<0x124>(a);                         // 4 apart
+        if constexpr (L <= 2)
+            a = dpp_add<0x122>(a);                         // 2 apart
+        return a;
+    }
+    static __device__ __forceinline__ void sum(float (&r)[COUNT], const floatx4& v, const floatx4& w)
+    {
+        const float a = rows(halves(v[0], v[1]), halves(v[2], v[3]));
+        const float b = rows(halves(w[0], w[1]), halves(w[2], w[3]));
+        if constexpr (L == 16) {
+            r[0] = a;
+            r[1] = b;
+        } else {
+            const float p = row(a), q = row(b);
+            r[0] = threadIdx.x & 8 ? q : p;
+        }
+    }
+};
+
+// Sums over the lanes of a channel of 4 values, the lane with quad q the sum of
+// value q & 3 (L == 2: of values q and q + 2).
+template <int L>
+struct ChannelSums {
+    static constexpr int COUNT = L == 2 ? 2 : 1;
+    template <int CTRL>
+    static __device__ __forceinline__ float pick(float a, float b, bool second)   // a's sum, or the second lane's b's
+    {
+        const float keep = second ? b : a, give = second ? a : b;
+        return keep + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(give), CTRL, 0xf, 0xf, true));
+    }
+    static __device__ __forceinline__ void sum(float (&r)[COUNT], const float (&v)[4])
+    {
+        const bool one = threadIdx.x & 1, two = threadIdx.x & 2;
+        const float a = pick<0xb1>(v[0], v[1], one), b = pick<0xb1>(v[2], v[3], one);
+        if constexpr (L == 2) {
+            r[0] = a;
+            r[1] = b;
+        } else {
+            float s = pick<0x4e>(a, b, two);
+            // the 4 (12) lanes beside hold other parts of the same values
+            if constexpr (L == 8) {
+                unsigned o = __builtin_amdgcn_update_dpp(0u, __float_as_uint(s), 0x124, 0xf, 0xa, false);   // 4 lanes before
+                o = __builtin_amdgcn_update_dpp(o, __float_as_uint(s), 0x12c, 0xf, 0x5, false);             // 4 lanes behind
+                s += __uint_as_float(o);
+            }
+            if constexpr (L == 16)
+                s = dpp_add<0x124>(dpp_add<0x128>(s));
+            r[0] = s;
+        }
+    }
+};
 
 // ---- the mapping that reads token rows ---------------------------------------
 //
@@ -231,7 +323,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
 {
     typedef Rows<T, N> R;
     constexpr int CW = Geo<N>::CW, L = Geo<N>::L, VN = R::VN, PV = R::PV;
-    __shared__ float2 step[TILE][CW];   // d, d x
+    __shared__ __attribute__((aligned(16))) float2 step[TILE][CW];   // d, d x
     __shared__ float ysum[SUM ? 1 : TILE][CW];
     __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
     const Where w = where<N>(n_new, T_, C, G, blocks);
@@ -267,14 +359,14 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
             xc[i] = xv[i];
             zc[i] = zv[i];
             const int r = rows.token(i);
+            float d[VN];
+            steps<T, VN>(d, dv[i], bias, in.softplus);
             if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT) {
+                const bool there = t0 + r < end;   // a token that is not there leaves the state as it is
 #pragma unroll
-                for (int j = 0; j < VN; ++j) {
-                    float d = vec_get<T>(dv[i], j) + bias[j], slope;
-                    if (in.softplus)
-                        d = softplus(d, slope);
-                    const bool there = t0 + r < end;   // a token that is not there leaves the state as it is
-                    step[r][rows.col() + j] = float2{there ? d : 0.f, there ? d * vec_get<T>(xv[i], j) : 0.f};
+                for (int j = 0; j < VN; j += 2) {
+                    const floatx4 v = {d[j], d[j] * vec_get<T>(xv[i], j), d[j + 1], d[j + 1] * vec_get<T>(xv[i], j + 1)};
+                    *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) = there ? v : zero4();
                 }
             }
         }
@@ -283,22 +375,30 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
             fetch(t0 + TILE);
         __syncthreads();
         float* sp = saved ? saved + ((int64_t)w.b * ((T_ + BLOCK - 1) / BLOCK) + t0 / BLOCK) * C * N : nullptr;
-#pragma unroll 8
-        for (int t = 0; t < TILE; ++t) {
+        for (int k = 0; k < TILE; k += BLOCK) {
             if constexpr (!SUM)
-                if (sp && t % BLOCK == 0 && t0 + t < end)
-                    lane.store(sp + (int64_t)(t / BLOCK) * C * N, h);
-            const float2 s = step[t][lane.col];
-            const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][t][lane.q * NS]);
-            h = exp2_4(s.x * A2) * h + s.y * bv;
-            if constexpr (SUM) {
-                total += s.x;
-            } else {
-                const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][t][lane.q * NS]);
-                const float o = channel_sum<L>(dot4(cv, h));
-                if (lane.q == 0)
-                    ysum[t][lane.col] = o;
+                if (sp && t0 + k < end)
+                    lane.store(sp + (int64_t)(k / BLOCK) * C * N, h);
+            float o[BLOCK];
+#pragma unroll
+            for (int t = 0; t < BLOCK; ++t) {
+                const float2 s = step[k + t][lane.col];
+                const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][k + t][lane.q * NS]);
+                h = exp2_4(s.x * A2) * h + s.y * bv;
+                if constexpr (SUM)
+                    total += s.x;
+                else
+                    o[t] = dot4(*reinterpret_cast<const floatx4*>(&bc[1][k + t][lane.q * NS]), h);
             }
+            if constexpr (!SUM)
+#pragma unroll
+                for (int t = 0; t < BLOCK; t += 4) {   // every lane writes a token's sum: no branch in the walk
+                    float r[ChannelSums<L>::COUNT];
+                    ChannelSums<L>::sum(r, {o[t], o[t + 1], o[t + 2], o[t + 3]});
+#pragma unroll
+                    for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
+                        ysum[k + t + 2 * i + (lane.q & (L == 2 ? 1 : 3))][lane.col] = r[i];
+                }
         }
         __syncthreads();
         if constexpr (!SUM) {
@@ -308,14 +408,14 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
                 if (t0 + r < end && rows.nc > 0) {
                     float out[VN];
 #pragma unroll
-                    for (int j = 0; j < VN; ++j) {
-                        float o = __builtin_fmaf(skip[j], vec_get<T>(xc[i], j), ysum[r][rows.col() + j]);
-                        if (in.z.ptr) {
+                    for (int j = 0; j < VN; ++j)
+                        out[j] = __builtin_fmaf(skip[j], vec_get<T>(xc[i], j), ysum[r][rows.col() + j]);
+                    if (in.z.ptr)
+#pragma unroll
+                        for (int j = 0; j < VN; ++j) {
                             const float z = vec_get<T>(zc[i], j);
-                            o *= z * sigmoid(z);
+                            out[j] *= z * sigmoid(z);
                         }
-                        out[j] = o;
-                    }
                     store_vec<OT, VN>(y.ptr + w.b * y.sb + (int64_t)(t0 + r) * y.st + rows.c, out, rows.nc);
                 }
             }
@@ -386,6 +486,11 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
     if constexpr (!SUM)
         g = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
                         : lane.load(dh_out ? dh_out + (int64_t)w.b * C * N : nullptr);
+    typedef WaveSums<L> Sums;
+    int sums_at[Sums::COUNT];   // where this lane's sums lie among the 2 N of a token
+#pragma unroll
+    for (int i = 0; i < Sums::COUNT; ++i)
+        sums_at[i] = Sums::of(i) / NS * N + lane.q * NS + Sums::of(i) % NS;
     float total = 0.f;
     float bias[VN], skip[VN], dD[VN], dbias[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
@@ -414,26 +519,22 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
             xc[i] = xv[i];
             const int r = rows.token(i);
             const bool there = t0 + r < end;
+            steps<T, VN>(dd[i], ds[i], dv[i], bias, in.softplus);
 #pragma unroll
-            for (int j = 0; j < VN; ++j) {
-                float d = vec_get<T>(dv[i], j) + bias[j];
-                ds[i][j] = 1.f;
-                if (in.softplus)
-                    d = softplus(d, ds[i][j]);
-                d = there ? d : 0.f;
-                float e = vec_get<T>(gv[i], j);
-                dg[i][j] = e;
-                if (in.z.ptr) {
+            for (int j = 0; j < VN; ++j)
+                ee[i][j] = dg[i][j] = vec_get<T>(gv[i], j);
+            if (in.z.ptr)
+#pragma unroll
+                for (int j = 0; j < VN; ++j) {
                     const float z = vec_get<T>(zv[i], j), q = sigmoid(z);
-                    dg[i][j] = e * __builtin_fmaf(z * q, 1.f - q, q);
-                    e *= z * q;
+                    dg[i][j] *= __builtin_fmaf(z * q, 1.f - q, q);
+                    ee[i][j] *= z * q;
                 }
-                e = there ? e : 0.f;
-                dd[i][j] = d;
-                ee[i][j] = e;
-                if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT)
-                    slot[r][rows.col() + j] = floatx4{d, there ? d * vec_get<T>(xc[i], j) : 0.f, e, 0.f};
-            }
+            if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT)
+#pragma unroll
+                for (int j = 0; j < VN; ++j)
+                    slot[r][rows.col() + j] =
+                        there ? floatx4{dd[i][j], dd[i][j] * vec_get<T>(xc[i], j), ee[i][j], 0.f} : zero4();
         }
         proj.store(bc);
         if (t0 > begin)
@@ -468,25 +569,21 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
                     const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
                     const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][tk + t][lane.q * NS]);
                     const floatx4 Gt = g + s[2] * cv;
-                    const float o = channel_sum<L>(dot4(cv, hs[t]));
-                    const float du = channel_sum<L>(dot4(Gt, bv));
                     floatx4 pc = s[2] * hs[t], pb = s[1] * Gt;
                     g = as[t] * Gt;
                     const floatx4 qv = g * (t ? hs[t - 1] : h0);
                     dA += s[0] * qv;
-                    const float da = channel_sum<L>(dot4(qv, A));
-                    if (lane.q == 0)
-                        slot[tk + t][lane.col] = floatx4{da, du, 0.f, o};
+                    // the channel's lanes write its sums together, and no lane branches
+                    float own[ChannelSums<L>::COUNT], r[Sums::COUNT];
+                    ChannelSums<L>::sum(own, {dot4(qv, A), dot4(Gt, bv), 0.f, dot4(cv, hs[t])});
+                    float* at = reinterpret_cast<float*>(&slot[tk + t][lane.col]);
 #pragma unroll
-                    for (int j = 0; j < NS; ++j) {
-                        pb[j] = wave_sum<L>(pb[j]);
-                        pc[j] = wave_sum<L>(pc[j]);
-                    }
-                    if ((threadIdx.x & 63) < L) {
-                        float* p = &part[threadIdx.x >> 6][tk + t][lane.q * NS];
-                        *reinterpret_cast<floatx4*>(p) = pb;
-                        *reinterpret_cast<floatx4*>(p + N) = pc;
-                    }
+                    for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
+                        at[2 * i + (lane.q & (L == 2 ? 1 : 3))] = own[i];
+                    Sums::sum(r, pb, pc);
+#pragma unroll
+                    for (int i = 0; i < Sums::COUNT; ++i)
+                        part[threadIdx.x >> 6][tk + t][sums_at[i]] = r[i];
                 }
             }
         }
