@@ -6,7 +6,7 @@
 // A lane owns 4 states of a channel, N / 4 lanes a channel, so a workgroup of
 // four waves walks 4 * 64 / (N / 4) channels token by token with their states in
 // registers.  Token rows are read 16 bytes at a time by a mapping of their own,
-// a tile of 32 tokens ahead: each value that belongs to a token and channel (the
+// a tile of tokens ahead: each value that belongs to a token and channel (the
 // step d, the input d x, the gates) is formed once there and passed through LDS.
 #include <hip/hip_runtime.h>
 
@@ -21,15 +21,16 @@ namespace {
 
 constexpr int NT = 256;      // threads a workgroup
 constexpr int NS = 4;        // states a lane
-constexpr int TILE = 32;     // tokens a tile
+constexpr int SEG = 32;      // tokens: segments are multiples of this, and of every tile
 constexpr int BLOCK = 8;     // tokens between two saved states
-constexpr float LOG2E = 1.44269504088896341f;
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
 
 template <int N>
 struct Geo {
     static constexpr int L = N / NS;        // lanes a channel
     static constexpr int CPW = 64 / L;      // channels a wave
     static constexpr int CW = NT / 64 * CPW;   // channels a workgroup
+    static constexpr int TILE = N == 16 || N == 32 ? 32 : 16;   // tokens a tile: two workgroups' tiles fit a CU's LDS
 };
 
 template <typename T>
@@ -59,22 +60,21 @@ __device__ __forceinline__ Where where(const int* n_new, int T_, int C, int G, i
 
 __device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf(1.f + __expf(-p)); }
 
-// log(1 + e^v) = max(v, 0) + 2 artanh(e / (2 + e)), e = exp(-|v|): the series in
-// s = e / (2 + e) <= 1/3 keeps the relative precision of small steps; its first
-// dropped term, s^14 / 15, is 1.4e-8 of the sum.  slope: the derivative.
+// log(1 + e^v) = max(v, 0) + log(w), w = 1 + e, e = exp(-|v|).  What w loses of e
+// is added back, which keeps the relative precision of small steps (log(w) is c / w
+// short, and w = 1 up to rounding where c counts).  slope: the derivative.
+__device__ __forceinline__ float softplus(float v)
+{
+    const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(v)), w = 1.f + e, c = e - (w - 1.f);
+    return __builtin_fmaf(0.5f, v + fabsf(v), __builtin_fmaf(__builtin_amdgcn_logf(w), LN2, c));
+}
+
 __device__ __forceinline__ float softplus(float v, float& slope)
 {
-    const float e = __expf(-fabsf(v)), s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-    const float r = __builtin_amdgcn_rcpf(1.f + e);
+    const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(v)), w = 1.f + e, c = e - (w - 1.f);
+    const float r = __builtin_amdgcn_rcpf(w);
     slope = v >= 0.f ? r : e * r;
-    float p = 1.f / 13;
-    p = __builtin_fmaf(p, q, 1.f / 11);
-    p = __builtin_fmaf(p, q, 1.f / 9);
-    p = __builtin_fmaf(p, q, 1.f / 7);
-    p = __builtin_fmaf(p, q, 1.f / 5);
-    p = __builtin_fmaf(p, q, 1.f / 3);
-    p = __builtin_fmaf(p, q, 1.f);
-    return __builtin_fmaf(2.f * s, p, fmaxf(v, 0.f));
+    return __builtin_fmaf(0.5f, v + fabsf(v), __builtin_fmaf(__builtin_amdgcn_logf(w), LN2, c));
 }
 
 // The steps of a vector of channels (and their slopes).
@@ -95,8 +95,13 @@ __device__ __forceinline__ void steps(float (&d)[VN], float (&slope)[VN], const 
 template <typename T, int VN>
 __device__ __forceinline__ void steps(float (&d)[VN], const u32x4& v, const float (&bias)[VN], int sp)
 {
-    float slope[VN];
-    steps<T, VN>(d, slope, v, bias, sp);
+#pragma unroll
+    for (int j = 0; j < VN; ++j)
+        d[j] = vec_get<T>(v, j) + bias[j];
+    if (sp)
+#pragma unroll
+        for (int j = 0; j < VN; ++j)
+            d[j] = softplus(d[j]);
 }
 
 template <int CTRL>
@@ -119,19 +124,38 @@ __device__ __forceinline__ float channel_sum(float v)
     return v;
 }
 
-// Sums of 8 values of every lane over the channels of a wave (the lanes of one
-// state quad), left COUNT a lane: a step that adds lanes 32 or 16 apart adds two
-// values at once, one in each half of the lanes, so 8 values over 16 channels take
-// 17 instructions where adding them one by one takes 32.  r[i] is value of(i) of
-// the lane's quad.
+// Sums of 4 values of every lane over the channels of a wave (the lanes of one
+// state quad): a step that adds lanes 32 or 16 apart adds two values at once, one
+// in each half of the lanes, so 4 values over 16 channels take 8 instructions
+// where adding them one by one takes 16.  Every lane of row r of 16 lanes has the
+// sum of value of(); the two sets of sums of TOKENS tokens (db's and dc's) differ
+// by lane, so that a write stores 64 of them (L == 16: two writes).
 template <int L>
 struct WaveSums {
-    static constexpr int COUNT = L == 16 ? 2 : 1;
-    static __device__ __forceinline__ int of(int i)
+    static constexpr int TOKENS = L == 2 ? 4 : L == 4 ? 2 : 1, COUNT = L == 16 ? 2 : 1;
+    static __device__ __forceinline__ int of() { return 2 * ((threadIdx.x >> 4) & 1) + ((threadIdx.x >> 5) & 1); }
+    static __device__ __forceinline__ int set() { return L == 16 ? 0 : (threadIdx.x >> 3) & 1; }
+    static __device__ __forceinline__ int token() { return L == 2 ? (threadIdx.x >> 1) & 3 : L == 4 ? (threadIdx.x >> 2) & 1 : 0; }
+    static __device__ __forceinline__ void pick(float (&r)[COUNT], const float (&b)[TOKENS], const float (&c)[TOKENS])
     {
-        const int lane = threadIdx.x & 63, row = lane >> 4;
-        const int half = L == 16 ? i : (lane >> 3) & 1;
-        return 4 * half + 2 * (row & 1) + (row >> 1);
+        if constexpr (L == 16) {
+            r[0] = b[0];
+            r[1] = c[0];
+        } else {
+            float v[TOKENS];
+#pragma unroll
+            for (int i = 0; i < TOKENS; ++i)
+                v[i] = threadIdx.x & 8 ? c[i] : b[i];
+            if constexpr (L == 2) {
+                const bool one = threadIdx.x & 2;
+                const float p = one ? v[1] : v[0], q = one ? v[3] : v[2];
+                r[0] = threadIdx.x & 4 ? q : p;
+            } else if constexpr (L == 4) {
+                r[0] = threadIdx.x & 4 ? v[1] : v[0];
+            } else {
+                r[0] = v[0];
+            }
+        }
     }
     static __device__ __forceinline__ float halves(float a, float b)   // a in lanes 0-31, b in 32-63
     {
@@ -145,24 +169,17 @@ struct WaveSums {
     }
     static __device__ __forceinline__ float row(float a)   // over the channels of a row
     {
-        a = dpp_add<0x128>(a);                             // lanes 8 apart
+        if constexpr (L <= 8)
+            a = dpp_add<0x128>(a);                         // lanes 8 apart
         if constexpr (L <= 4)
             a = dpp_add<0x124>(a);                         // 4 apart
         if constexpr (L <= 2)
             a = dpp_add<0x122>(a);                         // 2 apart
         return a;
     }
-    static __device__ __forceinline__ void sum(float (&r)[COUNT], const floatx4& v, const floatx4& w)
+    static __device__ __forceinline__ float sum(const floatx4& v)   // values 0-3 in the rows of 16 lanes
     {
-        const float a = rows(halves(v[0], v[1]), halves(v[2], v[3]));
-        const float b = rows(halves(w[0], w[1]), halves(w[2], w[3]));
-        if constexpr (L == 16) {
-            r[0] = a;
-            r[1] = b;
-        } else {
-            const float p = row(a), q = row(b);
-            r[0] = threadIdx.x & 8 ? q : p;
-        }
+        return row(rows(halves(v[0], v[1]), halves(v[2], v[3])));
     }
 };
 
@@ -177,10 +194,15 @@ struct ChannelSums {
         const float keep = second ? b : a, give = second ? a : b;
         return keep + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(give), CTRL, 0xf, 0xf, true));
     }
-    static __device__ __forceinline__ void sum(float (&r)[COUNT], const float (&v)[4])
+    static __device__ __forceinline__ float both(float a)
+    {
+        return dpp_add<0xb1>(a);
+    }
+    // 4 values, or 3: value 2 is value 3 too
+    static __device__ __forceinline__ void sum(float (&r)[COUNT], const float (&v)[4], bool three = false)
     {
         const bool one = threadIdx.x & 1, two = threadIdx.x & 2;
-        const float a = pick<0xb1>(v[0], v[1], one), b = pick<0xb1>(v[2], v[3], one);
+        const float a = pick<0xb1>(v[0], v[1], one), b = three ? both(v[3]) : pick<0xb1>(v[2], v[3], one);
         if constexpr (L == 2) {
             r[0] = a;
             r[1] = b;
@@ -205,6 +227,7 @@ struct ChannelSums {
 // all of the same channels.
 template <typename T, int N>
 struct Rows {
+    static constexpr int TILE = Geo<N>::TILE;
     static constexpr int VN = Vec<T>::N, VPR = Geo<N>::CW / VN, COUNT = TILE * VPR, PV = (COUNT + NT - 1) / NT;
     static_assert(NT % VPR == 0 && (COUNT % NT == 0 || COUNT < NT), "whole rounds of one thread's channels");
     int c, nc, row;   // first channel, channels that exist, first row
@@ -217,20 +240,32 @@ struct Rows {
     }
     __device__ __forceinline__ int token(int i) const { return row + i * (NT / VPR); }
     __device__ __forceinline__ int col() const { return (threadIdx.x % VPR) * VN; }
-    // rows t0 .. of sequence b; rows from `n` on come as zeros
-    __device__ __forceinline__ void load(u32x4 (&v)[PV], const Act<const T>& a, int b, int t0, int n) const
+};
+
+// This thread's rows of one tensor, tile after tile.
+template <typename T, typename R>
+struct Stream {
+    T* p;
+    int64_t st;
+    __device__ __forceinline__ Stream(const Act<T>& a, const Where& w, const R& rows, int t0)
+        : p(a.ptr + w.b * a.sb + (int64_t)(t0 + rows.row) * a.st + rows.c), st(a.st)
+    {
+    }
+    __device__ __forceinline__ void move(int tokens) { p += tokens * st; }
+    __device__ __forceinline__ T* at(int i) const { return p + i * (NT / R::VPR) * st; }
+    // the tile's first `left` rows; the others come as zeros
+    __device__ __forceinline__ void load(u32x4 (&v)[R::PV], const R& rows, int left) const
     {
 #pragma unroll
-        for (int i = 0; i < PV; ++i) {
-            const int t = t0 + token(i);
-            v[i] = t < n && nc > 0 ? load_vec(a.ptr + b * a.sb + (int64_t)t * a.st + c, nc) : u32x4{0u, 0u, 0u, 0u};
-        }
+        for (int i = 0; i < R::PV; ++i)
+            v[i] = rows.token(i) < left && rows.nc > 0 ? load_vec(at(i), rows.nc) : u32x4{0u, 0u, 0u, 0u};
     }
 };
 
 // b and c of a tile: a thread takes PB of the 16-byte vectors of both.
 template <typename T, int N>
 struct Projections {
+    static constexpr int TILE = Geo<N>::TILE;
     static constexpr int VN = Vec<T>::N, VPR = N / VN, ONE = TILE * VPR, COUNT = 2 * ONE, PB = (COUNT + NT - 1) / NT;
     u32x4 v[PB];
     __device__ __forceinline__ void load(const In<T>& in, const Where& w, int t0)
@@ -322,9 +357,9 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
                                                       float* saved, Segments sg, int T_, int C, int G, int blocks)
 {
     typedef Rows<T, N> R;
-    constexpr int CW = Geo<N>::CW, L = Geo<N>::L, VN = R::VN, PV = R::PV;
-    __shared__ __attribute__((aligned(16))) float2 step[TILE][CW];   // d, d x
-    __shared__ float ysum[SUM ? 1 : TILE][CW];
+    constexpr int CW = Geo<N>::CW, L = Geo<N>::L, TILE = Geo<N>::TILE, VN = R::VN, PV = R::PV;
+    __shared__ __attribute__((aligned(16))) float2 step[TILE][CW + 2];   // d, d x (rows 4 banks apart, as those below)
+    __shared__ __attribute__((aligned(16))) float ysum[SUM ? 1 : TILE][CW + 4];
     __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
     const Where w = where<N>(n_new, T_, C, G, blocks);
     const R rows(w);
@@ -342,13 +377,18 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
     load_floats<VN>(skip, in.D ? in.D + rows.c : nullptr, rows.nc);
     u32x4 xv[PV], dv[PV], zv[PV];
     Projections<T, N> proj;
+    Stream<const T, R> xs(in.x, w, rows, begin), ds(in.dt, w, rows, begin), zs(in.z, w, rows, begin);
+    Stream<OT, R> ys(y, w, rows, begin);
     auto fetch = [&](int t0) {
-        rows.load(xv, in.x, w.b, t0, end);
-        rows.load(dv, in.dt, w.b, t0, end);
+        xs.load(xv, rows, end - t0);
+        ds.load(dv, rows, end - t0);
         if constexpr (!SUM)
             if (in.z.ptr)
-                rows.load(zv, in.z, w.b, t0, end);
+                zs.load(zv, rows, end - t0);
         proj.load(in, w, t0);
+        xs.move(TILE);
+        ds.move(TILE);
+        zs.move(TILE);
     };
     if (begin < end)
         fetch(begin);
@@ -362,12 +402,14 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
             float d[VN];
             steps<T, VN>(d, dv[i], bias, in.softplus);
             if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT) {
-                const bool there = t0 + r < end;   // a token that is not there leaves the state as it is
+                if (t0 + TILE > end && t0 + r >= end)   // a token that is not there leaves the state as it is
 #pragma unroll
-                for (int j = 0; j < VN; j += 2) {
-                    const floatx4 v = {d[j], d[j] * vec_get<T>(xv[i], j), d[j + 1], d[j + 1] * vec_get<T>(xv[i], j + 1)};
-                    *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) = there ? v : zero4();
-                }
+                    for (int j = 0; j < VN; ++j)
+                        d[j] = 0.f;
+#pragma unroll
+                for (int j = 0; j < VN; j += 2)
+                    *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) =
+                        floatx4{d[j], d[j] * vec_get<T>(xv[i], j), d[j + 1], d[j + 1] * vec_get<T>(xv[i], j + 1)};
             }
         }
         proj.store(bc);
@@ -416,9 +458,10 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
                             const float z = vec_get<T>(zc[i], j);
                             out[j] *= z * sigmoid(z);
                         }
-                    store_vec<OT, VN>(y.ptr + w.b * y.sb + (int64_t)(t0 + r) * y.st + rows.c, out, rows.nc);
+                    store_vec<OT, VN>(ys.at(i), out, rows.nc);
                 }
             }
+            ys.move(TILE);
         }
     }
     if constexpr (SUM) {
@@ -467,13 +510,16 @@ struct Grads {
 
 // SUM: the gradient that a segment passes on of zeros behind it, and its sum of steps.
 template <typename T, typename OT, int N, bool SUM>
-__global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* saved, const int* n_new, Act<const T> dy,
+__global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* saved, const int* n_new, Act<const T> dy,
                                                       const float* dh_out, Grads<OT> out, Segments sg, int T_, int C, int G,
                                                       int blocks)
 {
     typedef Rows<T, N> R;
-    constexpr int CW = Geo<N>::CW, L = Geo<N>::L, VN = R::VN, PV = R::PV;
-    __shared__ floatx4 slot[TILE][CW];   // d, d x, e, c . h; then the sums of dd and of G b in the places of d and d x
+    constexpr int CW = Geo<N>::CW, L = Geo<N>::L, TILE = Geo<N>::TILE, VN = R::VN, PV = R::PV;
+    // a row: d, d x, e, c . h of the channels (G . b in d x's place after the walk), then the sums of q A;
+    // rows are 4 banks apart
+    constexpr int PITCH = 4 * (CW + 1) + CW;
+    __shared__ __attribute__((aligned(16))) float slot[TILE][PITCH];
     __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
     __shared__ __attribute__((aligned(16))) float part[SUM ? 1 : NT / 64][SUM ? 1 : TILE][SUM ? 4 : 2 * N];
     const Where w = where<N>(n_new, T_, C, G, blocks);
@@ -481,16 +527,16 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
     const Lane<N> lane(w);
     const int seg = blockIdx.y + (SUM ? 1 : 0);   // what the first segment passes on is not asked for
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
-    const floatx4 A = lane.load(in.A), A2 = A * LOG2E;
+    const floatx4 A2 = lane.load(in.A) * LOG2E;
     floatx4 g = zero4(), dA = zero4();
     if constexpr (!SUM)
         g = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
                         : lane.load(dh_out ? dh_out + (int64_t)w.b * C * N : nullptr);
     typedef WaveSums<L> Sums;
-    int sums_at[Sums::COUNT];   // where this lane's sums lie among the 2 N of a token
-#pragma unroll
-    for (int i = 0; i < Sums::COUNT; ++i)
-        sums_at[i] = Sums::of(i) / NS * N + lane.q * NS + Sums::of(i) % NS;
+    // where this lane's sums lie in the rows of its channel and of the tokens
+    float* const own_at = lane.q & 3 ? &slot[0][4 * lane.col + (lane.q & 2 ? 3 : 1)] : &slot[0][4 * (CW + 1) + lane.col];
+    const int own_o = (int)(&slot[0][4 * lane.col + 3] - own_at);   // (L == 2 writes c . h apart)
+    float* const part_at = SUM ? nullptr : &part[threadIdx.x >> 6][Sums::token()][Sums::set() * N + lane.q * NS + Sums::of()];
     float total = 0.f;
     float bias[VN], skip[VN], dD[VN], dbias[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
@@ -500,41 +546,51 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
         dD[j] = dbias[j] = 0.f;
     u32x4 xv[PV], dv[PV], zv[PV], gv[PV];
     Projections<T, N> proj;
-    auto fetch = [&](int t0) {
-        rows.load(xv, in.x, w.b, t0, end);
-        rows.load(dv, in.dt, w.b, t0, end);
-        if (in.z.ptr)
-            rows.load(zv, in.z, w.b, t0, end);
-        rows.load(gv, dy, w.b, t0, end);
-        proj.load(in, w, t0);
-    };
     const int last = begin + (end - 1 - begin) / TILE * TILE;
+    Stream<const T, R> xs(in.x, w, rows, last), ts(in.dt, w, rows, last), zs(in.z, w, rows, last), gs(dy, w, rows, last);
+    Stream<OT, R> dxs(out.dx, w, rows, last), dts(out.ddt, w, rows, last), dzs(out.dz, w, rows, last);
+    auto fetch = [&](int t0) {
+        xs.load(xv, rows, end - t0);
+        ts.load(dv, rows, end - t0);
+        if (in.z.ptr)
+            zs.load(zv, rows, end - t0);
+        gs.load(gv, rows, end - t0);
+        proj.load(in, w, t0);
+        xs.move(-TILE);
+        ts.move(-TILE);
+        zs.move(-TILE);
+        gs.move(-TILE);
+    };
     if (begin < end)
         fetch(last);
     for (int t0 = last; t0 >= begin && begin < end; t0 -= TILE) {
         u32x4 xc[PV];
-        float dd[PV][VN], ee[PV][VN], ds[PV][VN], dg[PV][VN];   // step, e, slope of the step, dy times the slope of the gate
+        float ds[PV][VN], dg[PV][VN];   // slope of the step, dy times the slope of the gate
 #pragma unroll
         for (int i = 0; i < PV; ++i) {
             xc[i] = xv[i];
             const int r = rows.token(i);
-            const bool there = t0 + r < end;
-            steps<T, VN>(dd[i], ds[i], dv[i], bias, in.softplus);
+            float d[VN], e[VN];
+            steps<T, VN>(d, ds[i], dv[i], bias, in.softplus);
 #pragma unroll
             for (int j = 0; j < VN; ++j)
-                ee[i][j] = dg[i][j] = vec_get<T>(gv[i], j);
+                e[j] = dg[i][j] = vec_get<T>(gv[i], j);
             if (in.z.ptr)
 #pragma unroll
                 for (int j = 0; j < VN; ++j) {
-                    const float z = vec_get<T>(zv[i], j), q = sigmoid(z);
-                    dg[i][j] *= __builtin_fmaf(z * q, 1.f - q, q);
-                    ee[i][j] *= z * q;
+                    const float z = vec_get<T>(zv[i], j), q = sigmoid(z), y = z * q;
+                    dg[i][j] *= __builtin_fmaf(y, 1.f - q, q);
+                    e[j] *= y;
                 }
+            if (t0 + TILE > end && t0 + r >= end)   // a token that is not there passes the gradient on (its x and dy are zeros)
+#pragma unroll
+                for (int j = 0; j < VN; ++j)
+                    d[j] = 0.f;
             if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT)
 #pragma unroll
                 for (int j = 0; j < VN; ++j)
-                    slot[r][rows.col() + j] =
-                        there ? floatx4{dd[i][j], dd[i][j] * vec_get<T>(xc[i], j), ee[i][j], 0.f} : zero4();
+                    *reinterpret_cast<floatx4*>(&slot[r][4 * (rows.col() + j)]) =
+                        floatx4{d[j], d[j] * vec_get<T>(xc[i], j), e[j], 0.f};
         }
         proj.store(bc);
         if (t0 > begin)
@@ -543,7 +599,7 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
         if constexpr (SUM) {
 #pragma unroll 8
             for (int t = TILE - 1; t >= 0; --t) {
-                const floatx4 s = slot[t][lane.col];
+                const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[t][4 * lane.col]);
                 const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][t][lane.q * NS]);
                 g = exp2_4(s[0] * A2) * (g + s[2] * cv);
                 total += s[0];
@@ -558,14 +614,15 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
                 floatx4 h = h0, hs[BLOCK], as[BLOCK];
 #pragma unroll
                 for (int t = 0; t < BLOCK; ++t) {
-                    const floatx4 s = slot[tk + t][lane.col];
+                    const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
                     const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
                     as[t] = exp2_4(s[0] * A2);
                     hs[t] = h = as[t] * h + s[1] * bv;
                 }
+                float sb[Sums::TOKENS], sc[Sums::TOKENS];
 #pragma unroll
                 for (int t = BLOCK - 1; t >= 0; --t) {
-                    const floatx4 s = slot[tk + t][lane.col];
+                    const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
                     const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
                     const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][tk + t][lane.q * NS]);
                     const floatx4 Gt = g + s[2] * cv;
@@ -574,16 +631,21 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
                     const floatx4 qv = g * (t ? hs[t - 1] : h0);
                     dA += s[0] * qv;
                     // the channel's lanes write its sums together, and no lane branches
-                    float own[ChannelSums<L>::COUNT], r[Sums::COUNT];
-                    ChannelSums<L>::sum(own, {dot4(qv, A), dot4(Gt, bv), 0.f, dot4(cv, hs[t])});
-                    float* at = reinterpret_cast<float*>(&slot[tk + t][lane.col]);
+                    float own[ChannelSums<L>::COUNT];
+                    const float o = dot4(cv, hs[t]);
+                    ChannelSums<L>::sum(own, {dot4(qv, A2), dot4(Gt, bv), o, o}, L > 2);
 #pragma unroll
                     for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
-                        at[2 * i + (lane.q & (L == 2 ? 1 : 3))] = own[i];
-                    Sums::sum(r, pb, pc);
+                        own_at[(tk + t) * PITCH + (i ? own_o : 0)] = own[i];
+                    sb[t % Sums::TOKENS] = Sums::sum(pb);
+                    sc[t % Sums::TOKENS] = Sums::sum(pc);
+                    if (t % Sums::TOKENS == 0) {
+                        float r[Sums::COUNT];
+                        Sums::pick(r, sb, sc);
 #pragma unroll
-                    for (int i = 0; i < Sums::COUNT; ++i)
-                        part[threadIdx.x >> 6][tk + t][sums_at[i]] = r[i];
+                        for (int i = 0; i < Sums::COUNT; ++i)
+                            part_at[(tk + t) * 2 * N + i * N] = r[i];
+                    }
                 }
             }
         }
@@ -591,13 +653,14 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
         if constexpr (!SUM) {
             // db, dc of this workgroup's channels
             float* pp = out.proj + (((int64_t)blockIdx.x * gridDim.z + w.b) * T_ + t0) * 2 * N;
-            for (int i = threadIdx.x; i < TILE * 2 * N; i += NT)
-                if (t0 + i / (2 * N) < end) {
-                    float s = part[0][i / (2 * N)][i % (2 * N)];
 #pragma unroll
-                    for (int k = 1; k < NT / 64; ++k)
-                        s += part[k][i / (2 * N)][i % (2 * N)];
-                    pp[i] = s;
+            for (int i = threadIdx.x * 4; i < TILE * 2 * N; i += NT * 4)
+                if (t0 + i / (2 * N) < end) {
+                    floatx4 s = zero4();
+#pragma unroll
+                    for (int k = 0; k < NT / 64; ++k)
+                        s += *reinterpret_cast<const floatx4*>(&part[k][i / (2 * N)][i % (2 * N)]);
+                    *reinterpret_cast<floatx4*>(pp + i) = s;
                 }
 #pragma unroll
             for (int i = 0; i < PV; ++i) {
@@ -606,21 +669,23 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
                     float dx[VN], ddt[VN], dz[VN];
 #pragma unroll
                     for (int j = 0; j < VN; ++j) {
-                        const floatx4 s = slot[r][rows.col() + j];
-                        const float x = vec_get<T>(xc[i], j);
-                        dx[j] = __builtin_fmaf(ee[i][j], skip[j], s[1] * dd[i][j]);
-                        ddt[j] = __builtin_fmaf(s[1], x, s[0]) * ds[i][j];
+                        const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[r][4 * (rows.col() + j)]);   // d, G . b, e, c . h
+                        const float x = vec_get<T>(xc[i], j), da = slot[r][4 * (CW + 1) + rows.col() + j];
+                        dx[j] = __builtin_fmaf(s[2], skip[j], s[1] * s[0]);
+                        ddt[j] = __builtin_fmaf(s[1], x, da * LN2) * ds[i][j];   // (the walk sums q A in base 2)
                         dz[j] = dg[i][j] * __builtin_fmaf(skip[j], x, s[3]);
-                        dD[j] = __builtin_fmaf(ee[i][j], x, dD[j]);
+                        dD[j] = __builtin_fmaf(s[2], x, dD[j]);
                         dbias[j] += ddt[j];
                     }
-                    const int64_t t = t0 + r;
-                    store_vec<OT, VN>(out.dx.ptr + w.b * out.dx.sb + t * out.dx.st + rows.c, dx, rows.nc);
-                    store_vec<OT, VN>(out.ddt.ptr + w.b * out.ddt.sb + t * out.ddt.st + rows.c, ddt, rows.nc);
+                    store_vec<OT, VN>(dxs.at(i), dx, rows.nc);
+                    store_vec<OT, VN>(dts.at(i), ddt, rows.nc);
                     if (in.z.ptr)
-                        store_vec<OT, VN>(out.dz.ptr + w.b * out.dz.sb + t * out.dz.st + rows.c, dz, rows.nc);
+                        store_vec<OT, VN>(dzs.at(i), dz, rows.nc);
                 }
             }
+            dxs.move(-TILE);
+            dts.move(-TILE);
+            dzs.move(-TILE);
             __syncthreads();   // before the next tile's values
         }
     }
@@ -636,7 +701,7 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(In<T> in, const float* sav
         lane.store(pp, dA);
         // dD and ddt_bias over the rows of a channel
         constexpr int ROWS = R::COUNT < NT ? TILE : NT / R::VPR;
-        float* red = reinterpret_cast<float*>(slot);   // [2][ROWS][CW]
+        float* red = &slot[0][0];   // [2][ROWS][CW]
         static_assert(2 * ROWS <= 4 * TILE, "the sums fit the slots");
         __syncthreads();
         if ((int)threadIdx.x < R::COUNT)
@@ -740,9 +805,9 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(In<T> in, float* S, const
     const T* cp = in.c.head(w.b, g) + lane.q * NS;
     for (int t = 0; t < T_; ++t) {
         const float x = (float)in.x.ptr[w.b * in.x.sb + (int64_t)t * in.x.st + lane.c];
-        float d = (float)in.dt.ptr[w.b * in.dt.sb + (int64_t)t * in.dt.st + lane.c] + bias, slope;
+        float d = (float)in.dt.ptr[w.b * in.dt.sb + (int64_t)t * in.dt.st + lane.c] + bias;
         if (in.softplus)
-            d = softplus(d, slope);
+            d = softplus(d);
         floatx4 bv, cv;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -776,7 +841,7 @@ struct Plan {
         const int64_t wgs = (int64_t)blocks * d->G * d->B;
         const int64_t want = wgs >= 256 ? 1 : std::min<int64_t>((511 + wgs) / wgs, (d->T + 127) / 128);
         const int64_t len = (d->T + want - 1) / want;
-        seg = (int)((len + TILE - 1) / TILE * TILE);
+        seg = (int)((len + SEG - 1) / SEG * SEG);
         nseg = (int)((d->T + (int64_t)seg - 1) / seg);
     }
 };
