@@ -203,7 +203,7 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(Act<const T> x, const floa
                                                       const float* dstate_out, Act<OT> dx, float* dstate, float* part,
                                                       int T_, int C, int ncg, int shift)
 {
-    constexpr int N = 4, R = 8;
+    constexpr int N = 4, R = 4;
     __shared__ float sums[NT][(K + 1) * N + 1];
     const Run p(n_new, T_, C, ncg, shift, N, RUN);
     float dw[K][N], db[N];

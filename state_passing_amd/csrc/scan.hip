@@ -262,20 +262,21 @@ struct Stream {
     }
 };
 
-// b and c of a tile: a thread takes PB of the 16-byte vectors of both.
-template <typename T, int N>
+// One or two projections of a tile (rows of N): a thread takes PB of the 16-byte
+// vectors of all.
+template <typename T, int N, int MANY>
 struct Projections {
     static constexpr int TILE = Geo<N>::TILE;
-    static constexpr int VN = Vec<T>::N, VPR = N / VN, ONE = TILE * VPR, COUNT = 2 * ONE, PB = (COUNT + NT - 1) / NT;
+    static constexpr int VN = Vec<T>::N, VPR = N / VN, ONE = TILE * VPR, COUNT = MANY * ONE, PB = (COUNT + NT - 1) / NT;
     u32x4 v[PB];
-    __device__ __forceinline__ void load(const In<T>& in, const Where& w, int t0)
+    __device__ __forceinline__ void load(const Act<const T>& first, const Act<const T>& second, const Where& w, int t0)
     {
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
             const int k = threadIdx.x + i * NT, r = k % ONE, t = t0 + r / VPR;
             v[i] = u32x4{0u, 0u, 0u, 0u};
             if (k < COUNT && t < w.n) {
-                const Act<const T>& a = k < ONE ? in.b : in.c;
+                const Act<const T>& a = k < ONE ? first : second;
                 v[i] = *reinterpret_cast<const u32x4*>(a.head(w.b, w.g) + (int64_t)t * a.st + r % VPR * VN);
             }
         }
@@ -348,18 +349,134 @@ struct Segments {
     float *state, *total;
 };
 
-// ---- forward -----------------------------------------------------------------
+// ---- segments ----------------------------------------------------------------
 //
-// SUM: the state that a segment makes of zeros, and its sum of steps (whose
-// exponential with A is what the segment makes of the state that enters it).
-template <typename T, typename OT, int N, bool SUM>
+// What a segment makes of zeros: the state that leaves it (REVERSE: the gradient
+// that it passes on), and its sum of steps, whose exponential with A is what it
+// makes of the state (gradient) that enters it.
+template <typename T, int N, bool REVERSE>
+__global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const int* n_new, Act<const T> dy, Segments sg, int T_, int C,
+                                                      int G, int blocks)
+{
+    typedef Rows<T, N> R;
+    constexpr int CW = Geo<N>::CW, TILE = Geo<N>::TILE, VN = R::VN, PV = R::PV;
+    __shared__ __attribute__((aligned(16))) float2 step[TILE][CW + 2];   // d, and d x or e
+    __shared__ __attribute__((aligned(16))) float bc[1][TILE][N];
+    const Where w = where<N>(n_new, T_, C, G, blocks);
+    const R rows(w);
+    const Lane<N> lane(w);
+    const int seg = blockIdx.y + (REVERSE ? 1 : 0);   // what the last (first) one makes is not asked for
+    const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
+    const int first = REVERSE ? begin + (end - 1 - begin) / TILE * TILE : begin, move = REVERSE ? -TILE : TILE;
+    const floatx4 A2 = lane.load(in.A) * LOG2E;
+    floatx4 h = zero4();
+    float total = 0.f;
+    float bias[VN];
+    load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
+    u32x4 xv[PV], dv[PV], zv[PV];
+    Projections<T, N, 1> proj;
+    Stream<const T, R> xs(REVERSE ? dy : in.x, w, rows, first), ds(in.dt, w, rows, first), zs(in.z, w, rows, first);
+    auto fetch = [&](int t0) {
+        xs.load(xv, rows, end - t0);
+        ds.load(dv, rows, end - t0);
+        if (REVERSE && in.z.ptr)
+            zs.load(zv, rows, end - t0);
+        proj.load(REVERSE ? in.c : in.b, in.b, w, t0);
+        xs.move(move);
+        ds.move(move);
+        zs.move(move);
+    };
+    if (begin < end)
+        fetch(first);
+    for (int t0 = first; t0 >= begin && t0 < end; t0 += move) {
+#pragma unroll
+        for (int i = 0; i < PV; ++i) {
+            const int r = rows.token(i);
+            float d[VN], u[VN];
+            steps<T, VN>(d, dv[i], bias, in.softplus);
+#pragma unroll
+            for (int j = 0; j < VN; ++j)
+                u[j] = REVERSE ? vec_get<T>(xv[i], j) : d[j] * vec_get<T>(xv[i], j);
+            if (REVERSE && in.z.ptr)
+#pragma unroll
+                for (int j = 0; j < VN; ++j) {
+                    const float z = vec_get<T>(zv[i], j);
+                    u[j] *= z * sigmoid(z);
+                }
+            if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT) {
+                if (t0 + TILE > end && t0 + r >= end)
+#pragma unroll
+                    for (int j = 0; j < VN; ++j)
+                        d[j] = 0.f;
+#pragma unroll
+                for (int j = 0; j < VN; j += 2)
+                    *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) = floatx4{d[j], u[j], d[j + 1], u[j + 1]};
+            }
+        }
+        proj.store(bc);
+        if (t0 + move >= begin && t0 + move < end)
+            fetch(t0 + move);
+        __syncthreads();
+#pragma unroll 8
+        for (int k = 0; k < TILE; ++k) {
+            const int t = REVERSE ? TILE - 1 - k : k;
+            const float2 s = step[t][lane.col];
+            const floatx4 v = *reinterpret_cast<const floatx4*>(&bc[0][t][lane.q * NS]);
+            if constexpr (REVERSE)
+                h = exp2_4(s.x * A2) * (h + s.y * v);
+            else
+                h = exp2_4(s.x * A2) * h + s.y * v;
+            total += s.x;
+        }
+        __syncthreads();
+    }
+    const int64_t at = (int64_t)w.b * sg.nseg + seg;
+    lane.store(sg.state + at * C * N, h);
+    if (lane.ok && lane.q == 0)
+        sg.total[at * C + lane.c] = total;
+}
+
+// The states that enter the segments (REVERSE: the gradients that enter them from
+// behind), in the place of what the segments make of zeros.
+template <bool REVERSE>
+__global__ __launch_bounds__(NT) void scan_fold_kernel(const float* A, const float* carry, Segments sg, int C, int N)
+{
+    constexpr int W = 8;   // segments read together
+    const int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x, cn = (int64_t)C * N;
+    const int b = blockIdx.y;
+    if (i >= cn)
+        return;
+    const float A2 = A[i] * LOG2E;
+    const int64_t at = (int64_t)b * sg.nseg + (REVERSE ? sg.nseg - 1 : 0), step = REVERSE ? -1 : 1;
+    float* p = sg.state + at * cn + i;
+    const float* q = sg.total + at * C + i / N;
+    float s = carry ? carry[b * cn + i] : 0.f;
+    for (int k = 0; k < sg.nseg; k += W) {
+        float own[W], keep[W];
+#pragma unroll
+        for (int u = 0; u < W; ++u) {   // nothing asks what the last one makes of it
+            own[u] = k + u < sg.nseg - 1 ? p[(k + u) * step * cn] : 0.f;
+            keep[u] = k + u < sg.nseg - 1 ? q[(k + u) * step * C] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+            if (k + u < sg.nseg) {
+                p[(k + u) * step * cn] = s;
+                s = __builtin_fmaf(__builtin_amdgcn_exp2f(keep[u] * A2), s, own[u]);
+            }
+    }
+}
+
+// ---- forward -----------------------------------------------------------------
+
+template <typename T, typename OT, int N>
 __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_in, const int* n_new, Act<OT> y, float* h_out,
                                                       float* saved, Segments sg, int T_, int C, int G, int blocks)
 {
     typedef Rows<T, N> R;
     constexpr int CW = Geo<N>::CW, L = Geo<N>::L, TILE = Geo<N>::TILE, VN = R::VN, PV = R::PV;
     __shared__ __attribute__((aligned(16))) float2 step[TILE][CW + 2];   // d, d x (rows 4 banks apart, as those below)
-    __shared__ __attribute__((aligned(16))) float ysum[SUM ? 1 : TILE][CW + 4];
+    __shared__ __attribute__((aligned(16))) float ysum[TILE][CW + 4];
     __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
     const Where w = where<N>(n_new, T_, C, G, blocks);
     const R rows(w);
@@ -368,24 +485,21 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
     floatx4 A2 = lane.load(in.A), h = zero4();
     A2 *= LOG2E;
-    if constexpr (!SUM)
-        h = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
-                        : lane.load(h_in ? h_in + (int64_t)w.b * C * N : nullptr);
-    float total = 0.f;
+    h = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
+                    : lane.load(h_in ? h_in + (int64_t)w.b * C * N : nullptr);
     float bias[VN], skip[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
     load_floats<VN>(skip, in.D ? in.D + rows.c : nullptr, rows.nc);
     u32x4 xv[PV], dv[PV], zv[PV];
-    Projections<T, N> proj;
+    Projections<T, N, 2> proj;
     Stream<const T, R> xs(in.x, w, rows, begin), ds(in.dt, w, rows, begin), zs(in.z, w, rows, begin);
     Stream<OT, R> ys(y, w, rows, begin);
     auto fetch = [&](int t0) {
         xs.load(xv, rows, end - t0);
         ds.load(dv, rows, end - t0);
-        if constexpr (!SUM)
-            if (in.z.ptr)
-                zs.load(zv, rows, end - t0);
-        proj.load(in, w, t0);
+        if (in.z.ptr)
+            zs.load(zv, rows, end - t0);
+        proj.load(in.b, in.c, w, t0);
         xs.move(TILE);
         ds.move(TILE);
         zs.move(TILE);
@@ -418,84 +532,47 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
         __syncthreads();
         float* sp = saved ? saved + ((int64_t)w.b * ((T_ + BLOCK - 1) / BLOCK) + t0 / BLOCK) * C * N : nullptr;
         for (int k = 0; k < TILE; k += BLOCK) {
-            if constexpr (!SUM)
-                if (sp && t0 + k < end)
-                    lane.store(sp + (int64_t)(k / BLOCK) * C * N, h);
+            if (sp && t0 + k < end)
+                lane.store(sp + (int64_t)(k / BLOCK) * C * N, h);
             float o[BLOCK];
 #pragma unroll
             for (int t = 0; t < BLOCK; ++t) {
                 const float2 s = step[k + t][lane.col];
                 const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][k + t][lane.q * NS]);
                 h = exp2_4(s.x * A2) * h + s.y * bv;
-                if constexpr (SUM)
-                    total += s.x;
-                else
-                    o[t] = dot4(*reinterpret_cast<const floatx4*>(&bc[1][k + t][lane.q * NS]), h);
+                o[t] = dot4(*reinterpret_cast<const floatx4*>(&bc[1][k + t][lane.q * NS]), h);
             }
-            if constexpr (!SUM)
 #pragma unroll
-                for (int t = 0; t < BLOCK; t += 4) {   // every lane writes a token's sum: no branch in the walk
-                    float r[ChannelSums<L>::COUNT];
-                    ChannelSums<L>::sum(r, {o[t], o[t + 1], o[t + 2], o[t + 3]});
+            for (int t = 0; t < BLOCK; t += 4) {   // every lane writes a token's sum: no branch in the walk
+                float r[ChannelSums<L>::COUNT];
+                ChannelSums<L>::sum(r, {o[t], o[t + 1], o[t + 2], o[t + 3]});
 #pragma unroll
-                    for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
-                        ysum[k + t + 2 * i + (lane.q & (L == 2 ? 1 : 3))][lane.col] = r[i];
-                }
+                for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
+                    ysum[k + t + 2 * i + (lane.q & (L == 2 ? 1 : 3))][lane.col] = r[i];
+            }
         }
         __syncthreads();
-        if constexpr (!SUM) {
 #pragma unroll
-            for (int i = 0; i < PV; ++i) {
-                const int r = rows.token(i);
-                if (t0 + r < end && rows.nc > 0) {
-                    float out[VN];
+        for (int i = 0; i < PV; ++i) {
+            const int r = rows.token(i);
+            if (t0 + r < end && rows.nc > 0) {
+                float out[VN];
 #pragma unroll
-                    for (int j = 0; j < VN; ++j)
-                        out[j] = __builtin_fmaf(skip[j], vec_get<T>(xc[i], j), ysum[r][rows.col() + j]);
-                    if (in.z.ptr)
+                for (int j = 0; j < VN; ++j)
+                    out[j] = __builtin_fmaf(skip[j], vec_get<T>(xc[i], j), ysum[r][rows.col() + j]);
+                if (in.z.ptr)
 #pragma unroll
-                        for (int j = 0; j < VN; ++j) {
-                            const float z = vec_get<T>(zc[i], j);
-                            out[j] *= z * sigmoid(z);
-                        }
-                    store_vec<OT, VN>(ys.at(i), out, rows.nc);
-                }
+                    for (int j = 0; j < VN; ++j) {
+                        const float z = vec_get<T>(zc[i], j);
+                        out[j] *= z * sigmoid(z);
+                    }
+                store_vec<OT, VN>(ys.at(i), out, rows.nc);
             }
-            ys.move(TILE);
         }
+        ys.move(TILE);
     }
-    if constexpr (SUM) {
-        const int64_t at = (int64_t)w.b * sg.nseg + seg;
-        lane.store(sg.state + at * C * N, h);
-        if (lane.ok && lane.q == 0)
-            sg.total[at * C + lane.c] = total;
-    } else if (seg == sg.nseg - 1) {
+    if (seg == sg.nseg - 1)
         lane.store(h_out + (int64_t)w.b * C * N, h);
-    }
-}
-
-// The states that enter the segments (REVERSE: the gradients that enter them from
-// behind), in the place of what the segments make of zeros.
-template <bool REVERSE>
-__global__ __launch_bounds__(NT) void scan_fold_kernel(const float* A, const float* carry, Segments sg, int C, int N)
-{
-    const int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x, cn = (int64_t)C * N;
-    const int b = blockIdx.y;
-    if (i >= cn)
-        return;
-    const float A2 = A[i] * LOG2E;
-    float s = carry ? carry[b * cn + i] : 0.f;
-    for (int k = 0; k < sg.nseg; ++k) {
-        const int64_t at = (int64_t)b * sg.nseg + (REVERSE ? sg.nseg - 1 - k : k);
-        float* p = sg.state + at * cn + i;
-        if (k == sg.nseg - 1) {   // nothing asks what the last one makes of it
-            *p = s;
-            break;
-        }
-        const float own = *p, keep = __builtin_amdgcn_exp2f(sg.total[at * C + i / N] * A2);
-        *p = s;
-        s = __builtin_fmaf(keep, s, own);
-    }
 }
 
 // ---- backward ----------------------------------------------------------------
@@ -508,8 +585,7 @@ struct Grads {
     float* proj;     // [G * blocks][B][T][2 N]: db, dc of a workgroup's channels
 };
 
-// SUM: the gradient that a segment passes on of zeros behind it, and its sum of steps.
-template <typename T, typename OT, int N, bool SUM>
+template <typename T, typename OT, int N>
 __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* saved, const int* n_new, Act<const T> dy,
                                                       const float* dh_out, Grads<OT> out, Segments sg, int T_, int C, int G,
                                                       int blocks)
@@ -521,23 +597,21 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
     constexpr int PITCH = 4 * (CW + 1) + CW;
     __shared__ __attribute__((aligned(16))) float slot[TILE][PITCH];
     __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
-    __shared__ __attribute__((aligned(16))) float part[SUM ? 1 : NT / 64][SUM ? 1 : TILE][SUM ? 4 : 2 * N];
+    __shared__ __attribute__((aligned(16))) float part[NT / 64][TILE][2 * N];
     const Where w = where<N>(n_new, T_, C, G, blocks);
     const R rows(w);
     const Lane<N> lane(w);
-    const int seg = blockIdx.y + (SUM ? 1 : 0);   // what the first segment passes on is not asked for
+    const int seg = blockIdx.y;
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
     const floatx4 A2 = lane.load(in.A) * LOG2E;
-    floatx4 g = zero4(), dA = zero4();
-    if constexpr (!SUM)
-        g = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
-                        : lane.load(dh_out ? dh_out + (int64_t)w.b * C * N : nullptr);
+    floatx4 g = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
+                            : lane.load(dh_out ? dh_out + (int64_t)w.b * C * N : nullptr);
+    floatx4 dA = zero4();
     typedef WaveSums<L> Sums;
     // where this lane's sums lie in the rows of its channel and of the tokens
     float* const own_at = lane.q & 3 ? &slot[0][4 * lane.col + (lane.q & 2 ? 3 : 1)] : &slot[0][4 * (CW + 1) + lane.col];
     const int own_o = (int)(&slot[0][4 * lane.col + 3] - own_at);   // (L == 2 writes c . h apart)
-    float* const part_at = SUM ? nullptr : &part[threadIdx.x >> 6][Sums::token()][Sums::set() * N + lane.q * NS + Sums::of()];
-    float total = 0.f;
+    float* const part_at = &part[threadIdx.x >> 6][Sums::token()][Sums::set() * N + lane.q * NS + Sums::of()];
     float bias[VN], skip[VN], dD[VN], dbias[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
     load_floats<VN>(skip, in.D ? in.D + rows.c : nullptr, rows.nc);
@@ -545,7 +619,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
     for (int j = 0; j < VN; ++j)
         dD[j] = dbias[j] = 0.f;
     u32x4 xv[PV], dv[PV], zv[PV], gv[PV];
-    Projections<T, N> proj;
+    Projections<T, N, 2> proj;
     const int last = begin + (end - 1 - begin) / TILE * TILE;
     Stream<const T, R> xs(in.x, w, rows, last), ts(in.dt, w, rows, last), zs(in.z, w, rows, last), gs(dy, w, rows, last);
     Stream<OT, R> dxs(out.dx, w, rows, last), dts(out.ddt, w, rows, last), dzs(out.dz, w, rows, last);
@@ -555,14 +629,18 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
         if (in.z.ptr)
             zs.load(zv, rows, end - t0);
         gs.load(gv, rows, end - t0);
-        proj.load(in, w, t0);
+        proj.load(in.b, in.c, w, t0);
         xs.move(-TILE);
         ts.move(-TILE);
         zs.move(-TILE);
         gs.move(-TILE);
     };
-    if (begin < end)
+    const float* sp = saved + ((int64_t)w.b * ((T_ + BLOCK - 1) / BLOCK) + (end - 1) / BLOCK) * C * N;
+    floatx4 hn = zero4();
+    if (begin < end) {
         fetch(last);
+        hn = lane.load(sp);
+    }
     for (int t0 = last; t0 >= begin && begin < end; t0 -= TILE) {
         u32x4 xc[PV];
         float ds[PV][VN], dg[PV][VN];   // slope of the step, dy times the slope of the gate
@@ -596,129 +674,111 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
         if (t0 > begin)
             fetch(t0 - TILE);
         __syncthreads();
-        if constexpr (SUM) {
-#pragma unroll 8
-            for (int t = TILE - 1; t >= 0; --t) {
-                const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[t][4 * lane.col]);
-                const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][t][lane.q * NS]);
-                g = exp2_4(s[0] * A2) * (g + s[2] * cv);
-                total += s[0];
+        for (int k = (min(end - t0, TILE) - 1) / BLOCK; k >= 0; --k) {
+            const int tk = k * BLOCK;
+            const floatx4 h0 = hn;
+            if (t0 + tk > begin) {   // the block before's, a block ahead
+                sp -= (int64_t)C * N;
+                hn = lane.load(sp);
             }
-        } else {
-            const float* sp = saved + ((int64_t)w.b * ((T_ + BLOCK - 1) / BLOCK) + t0 / BLOCK) * C * N;
-            for (int k = TILE / BLOCK - 1; k >= 0; --k) {
-                const int tk = k * BLOCK;
-                if (t0 + tk >= end)   // nothing there
-                    continue;
-                const floatx4 h0 = lane.load(sp + (int64_t)k * C * N);
-                floatx4 h = h0, hs[BLOCK], as[BLOCK];
+            floatx4 h = h0, hs[BLOCK], as[BLOCK];
 #pragma unroll
-                for (int t = 0; t < BLOCK; ++t) {
-                    const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
-                    const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
-                    as[t] = exp2_4(s[0] * A2);
-                    hs[t] = h = as[t] * h + s[1] * bv;
-                }
-                float sb[Sums::TOKENS], sc[Sums::TOKENS];
+            for (int t = 0; t < BLOCK; ++t) {
+                const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
+                const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
+                as[t] = exp2_4(s[0] * A2);
+                hs[t] = h = as[t] * h + s[1] * bv;
+            }
+            float sb[Sums::TOKENS], sc[Sums::TOKENS];
 #pragma unroll
-                for (int t = BLOCK - 1; t >= 0; --t) {
-                    const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
-                    const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
-                    const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][tk + t][lane.q * NS]);
-                    const floatx4 Gt = g + s[2] * cv;
-                    floatx4 pc = s[2] * hs[t], pb = s[1] * Gt;
-                    g = as[t] * Gt;
-                    const floatx4 qv = g * (t ? hs[t - 1] : h0);
-                    dA += s[0] * qv;
-                    // the channel's lanes write its sums together, and no lane branches
-                    float own[ChannelSums<L>::COUNT];
-                    const float o = dot4(cv, hs[t]);
-                    ChannelSums<L>::sum(own, {dot4(qv, A2), dot4(Gt, bv), o, o}, L > 2);
+            for (int t = BLOCK - 1; t >= 0; --t) {
+                const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
+                const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
+                const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][tk + t][lane.q * NS]);
+                const floatx4 Gt = g + s[2] * cv;
+                floatx4 pc = s[2] * hs[t], pb = s[1] * Gt;
+                g = as[t] * Gt;
+                const floatx4 qv = g * (t ? hs[t - 1] : h0);
+                dA += s[0] * qv;
+                // the channel's lanes write its sums together, and no lane branches
+                float own[ChannelSums<L>::COUNT];
+                const float o = dot4(cv, hs[t]);
+                ChannelSums<L>::sum(own, {dot4(qv, A2), dot4(Gt, bv), o, o}, L > 2);
 #pragma unroll
-                    for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
-                        own_at[(tk + t) * PITCH + (i ? own_o : 0)] = own[i];
-                    sb[t % Sums::TOKENS] = Sums::sum(pb);
-                    sc[t % Sums::TOKENS] = Sums::sum(pc);
-                    if (t % Sums::TOKENS == 0) {
-                        float r[Sums::COUNT];
-                        Sums::pick(r, sb, sc);
+                for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
+                    own_at[(tk + t) * PITCH + (i ? own_o : 0)] = own[i];
+                sb[t % Sums::TOKENS] = Sums::sum(pb);
+                sc[t % Sums::TOKENS] = Sums::sum(pc);
+                if (t % Sums::TOKENS == 0) {
+                    float r[Sums::COUNT];
+                    Sums::pick(r, sb, sc);
 #pragma unroll
-                        for (int i = 0; i < Sums::COUNT; ++i)
-                            part_at[(tk + t) * 2 * N + i * N] = r[i];
-                    }
+                    for (int i = 0; i < Sums::COUNT; ++i)
+                        part_at[(tk + t) * 2 * N + i * N] = r[i];
                 }
             }
         }
         __syncthreads();
-        if constexpr (!SUM) {
-            // db, dc of this workgroup's channels
-            float* pp = out.proj + (((int64_t)blockIdx.x * gridDim.z + w.b) * T_ + t0) * 2 * N;
+        // db, dc of this workgroup's channels
+        float* pp = out.proj + (((int64_t)blockIdx.x * gridDim.z + w.b) * T_ + t0) * 2 * N;
 #pragma unroll
-            for (int i = threadIdx.x * 4; i < TILE * 2 * N; i += NT * 4)
-                if (t0 + i / (2 * N) < end) {
-                    floatx4 s = zero4();
+        for (int i = threadIdx.x * 4; i < TILE * 2 * N; i += NT * 4)
+            if (t0 + i / (2 * N) < end) {
+                floatx4 s = zero4();
 #pragma unroll
-                    for (int k = 0; k < NT / 64; ++k)
-                        s += *reinterpret_cast<const floatx4*>(&part[k][i / (2 * N)][i % (2 * N)]);
-                    *reinterpret_cast<floatx4*>(pp + i) = s;
-                }
-#pragma unroll
-            for (int i = 0; i < PV; ++i) {
-                const int r = rows.token(i);
-                if (t0 + r < end && rows.nc > 0) {
-                    float dx[VN], ddt[VN], dz[VN];
-#pragma unroll
-                    for (int j = 0; j < VN; ++j) {
-                        const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[r][4 * (rows.col() + j)]);   // d, G . b, e, c . h
-                        const float x = vec_get<T>(xc[i], j), da = slot[r][4 * (CW + 1) + rows.col() + j];
-                        dx[j] = __builtin_fmaf(s[2], skip[j], s[1] * s[0]);
-                        ddt[j] = __builtin_fmaf(s[1], x, da * LN2) * ds[i][j];   // (the walk sums q A in base 2)
-                        dz[j] = dg[i][j] * __builtin_fmaf(skip[j], x, s[3]);
-                        dD[j] = __builtin_fmaf(s[2], x, dD[j]);
-                        dbias[j] += ddt[j];
-                    }
-                    store_vec<OT, VN>(dxs.at(i), dx, rows.nc);
-                    store_vec<OT, VN>(dts.at(i), ddt, rows.nc);
-                    if (in.z.ptr)
-                        store_vec<OT, VN>(dzs.at(i), dz, rows.nc);
-                }
+                for (int k = 0; k < NT / 64; ++k)
+                    s += *reinterpret_cast<const floatx4*>(&part[k][i / (2 * N)][i % (2 * N)]);
+                *reinterpret_cast<floatx4*>(pp + i) = s;
             }
-            dxs.move(-TILE);
-            dts.move(-TILE);
-            dzs.move(-TILE);
-            __syncthreads();   // before the next tile's values
+#pragma unroll
+        for (int i = 0; i < PV; ++i) {
+            const int r = rows.token(i);
+            if (t0 + r < end && rows.nc > 0) {
+                float dx[VN], ddt[VN], dz[VN];
+#pragma unroll
+                for (int j = 0; j < VN; ++j) {
+                    const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[r][4 * (rows.col() + j)]);   // d, G . b, e, c . h
+                    const float x = vec_get<T>(xc[i], j), da = slot[r][4 * (CW + 1) + rows.col() + j];
+                    dx[j] = __builtin_fmaf(s[2], skip[j], s[1] * s[0]);
+                    ddt[j] = __builtin_fmaf(s[1], x, da * LN2) * ds[i][j];   // (the walk sums q A in base 2)
+                    dz[j] = dg[i][j] * __builtin_fmaf(skip[j], x, s[3]);
+                    dD[j] = __builtin_fmaf(s[2], x, dD[j]);
+                    dbias[j] += ddt[j];
+                }
+                store_vec<OT, VN>(dxs.at(i), dx, rows.nc);
+                store_vec<OT, VN>(dts.at(i), ddt, rows.nc);
+                if (in.z.ptr)
+                    store_vec<OT, VN>(dzs.at(i), dz, rows.nc);
+            }
         }
+        dxs.move(-TILE);
+        dts.move(-TILE);
+        dzs.move(-TILE);
+        __syncthreads();   // before the next tile's values
     }
-    if constexpr (SUM) {
-        const int64_t at = (int64_t)w.b * sg.nseg + seg;
-        lane.store(sg.state + at * C * N, g);
-        if (lane.ok && lane.q == 0)
-            sg.total[at * C + lane.c] = total;
-    } else {
-        if (seg == 0)
-            lane.store(out.dh_in + (int64_t)w.b * C * N, g);
-        float* pp = out.params + ((int64_t)w.b * sg.nseg + seg) * ((int64_t)C * N + 2 * C);
-        lane.store(pp, dA);
-        // dD and ddt_bias over the rows of a channel
-        constexpr int ROWS = R::COUNT < NT ? TILE : NT / R::VPR;
-        float* red = &slot[0][0];   // [2][ROWS][CW]
-        static_assert(2 * ROWS <= 4 * TILE, "the sums fit the slots");
-        __syncthreads();
-        if ((int)threadIdx.x < R::COUNT)
+    if (seg == 0)
+        lane.store(out.dh_in + (int64_t)w.b * C * N, g);
+    float* pp = out.params + ((int64_t)w.b * sg.nseg + seg) * ((int64_t)C * N + 2 * C);
+    lane.store(pp, dA);
+    // dD and ddt_bias over the rows of a channel
+    constexpr int ROWS = R::COUNT < NT ? TILE : NT / R::VPR;
+    float* red = &slot[0][0];   // [2][ROWS][CW]
+    static_assert(2 * ROWS <= 4 * TILE, "the sums fit the slots");
+    __syncthreads();
+    if ((int)threadIdx.x < R::COUNT)
 #pragma unroll
-            for (int j = 0; j < VN; ++j) {
-                red[rows.row * CW + rows.col() + j] = dD[j];
-                red[(ROWS + rows.row) * CW + rows.col() + j] = dbias[j];
-            }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * CW; i += NT)
-            if (w.c0 + i % CW < w.cend) {
-                float s = 0.f;
-                for (int r = 0; r < ROWS; ++r)
-                    s += red[((i / CW) * ROWS + r) * CW + i % CW];
-                pp[(int64_t)C * N + (i / CW) * C + w.c0 + i % CW] = s;
-            }
-    }
+        for (int j = 0; j < VN; ++j) {
+            red[rows.row * CW + rows.col() + j] = dD[j];
+            red[(ROWS + rows.row) * CW + rows.col() + j] = dbias[j];
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * CW; i += NT)
+        if (w.c0 + i % CW < w.cend) {
+            float s = 0.f;
+            for (int r = 0; r < ROWS; ++r)
+                s += red[((i / CW) * ROWS + r) * CW + i % CW];
+            pp[(int64_t)C * N + (i / CW) * C + w.c0 + i % CW] = s;
+        }
 }
 
 // dA, dD and ddt_bias from the workgroups' sums: 64 columns and 16 slices of the
@@ -1008,12 +1068,12 @@ linrec_status linrec_scan_fwd(linrec_ctx* ctx, const linrec_scan_desc* d, const 
             const In<T> a = inputs<T>(d, in);
             const unsigned wgs = (unsigned)p.blocks * d->G;
             if (p.nseg > 1) {
-                launch_kernel(scan_fwd_kernel<T, OT, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, h_in, n_new,
-                              mact<OT>(y), h_out, (float*)nullptr, sg, d->T, d->C, d->G, p.blocks);
+                launch_kernel(scan_sum_kernel<T, N, false>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, n_new, cact<T>(in->x),
+                              sg, d->T, d->C, d->G, p.blocks);
                 launch_kernel(scan_fold_kernel<false>, dim3((unsigned)(((int64_t)d->C * N + NT - 1) / NT), d->B), dim3(NT), s,
                               in->A, h_in, sg, d->C, N);
             }
-            launch_kernel(scan_fwd_kernel<T, OT, N, false>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, h_in, n_new, mact<OT>(y),
+            launch_kernel(scan_fwd_kernel<T, OT, N>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, h_in, n_new, mact<OT>(y),
                           h_out, (float*)saved, sg, d->T, d->C, d->G, p.blocks);
             return hipGetLastError();
         });
@@ -1071,12 +1131,12 @@ linrec_status linrec_scan_bwd(linrec_ctx* ctx, const linrec_scan_desc* d, const 
             const unsigned wgs = (unsigned)p.blocks * d->G;
             const int64_t cn = (int64_t)d->C * N;
             if (p.nseg > 1) {
-                launch_kernel(scan_bwd_kernel<T, OT, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a,
-                              (const float*)nullptr, n_new, cact<T>(dy), dh_out, gr, sg, d->T, d->C, d->G, p.blocks);
+                launch_kernel(scan_sum_kernel<T, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, n_new, cact<T>(dy), sg,
+                              d->T, d->C, d->G, p.blocks);
                 launch_kernel(scan_fold_kernel<true>, dim3((unsigned)((cn + NT - 1) / NT), d->B), dim3(NT), s, in->A, dh_out,
                               sg, d->C, N);
             }
-            launch_kernel(scan_bwd_kernel<T, OT, N, false>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, (const float*)saved,
+            launch_kernel(scan_bwd_kernel<T, OT, N>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, (const float*)saved,
                           n_new, cact<T>(dy), dh_out, gr, sg, d->T, d->C, d->G, p.blocks);
             launch_kernel(scan_params_kernel, dim3((unsigned)((cn + 2 * d->C + 63) / 64)), dim3(1024), s, (const float*)gr.params,
                           d->B * p.nseg, out->dA, out->dD, out->ddt_bias, cn, d->C);
