@@ -351,12 +351,14 @@ struct Segments {
 
 // ---- segments ----------------------------------------------------------------
 //
-// What a segment makes of zeros: the state that leaves it (REVERSE: the gradient
-// that it passes on), and its sum of steps, whose exponential with A is what it
-// makes of the state (gradient) that enters it.
+// What a segment makes of zeros (the first in order: of the carry): the state that
+// leaves it (REVERSE: the gradient that it passes on), and its sum of steps, whose
+// exponential with A is what it makes of the state (gradient) that enters it.  What
+// the last in order makes is not asked for: its place takes a copy of the carry,
+// which the first reads (the caller's memory may be the last one's output).
 template <typename T, int N, bool REVERSE>
-__global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const int* n_new, Act<const T> dy, Segments sg, int T_, int C,
-                                                      int G, int blocks)
+__global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* carry, const int* n_new, Act<const T> dy,
+                                                      Segments sg, int T_, int C, int G, int blocks)
 {
     typedef Rows<T, N> R;
     constexpr int CW = Geo<N>::CW, TILE = Geo<N>::TILE, VN = R::VN, PV = R::PV;
@@ -365,11 +367,15 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const int* n_new
     const Where w = where<N>(n_new, T_, C, G, blocks);
     const R rows(w);
     const Lane<N> lane(w);
-    const int seg = blockIdx.y + (REVERSE ? 1 : 0);   // what the last (first) one makes is not asked for
+    const int seg = REVERSE ? sg.nseg - 1 - blockIdx.y : blockIdx.y;
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
     const int first = REVERSE ? begin + (end - 1 - begin) / TILE * TILE : begin, move = REVERSE ? -TILE : TILE;
     const floatx4 A2 = lane.load(in.A) * LOG2E;
     floatx4 h = zero4();
+    if (blockIdx.y == 0) {
+        h = lane.load(carry ? carry + (int64_t)w.b * C * N : nullptr);
+        lane.store(sg.state + ((int64_t)w.b * sg.nseg + (REVERSE ? 0 : sg.nseg - 1)) * C * N, h);
+    }
     float total = 0.f;
     float bias[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
@@ -436,35 +442,33 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const int* n_new
         sg.total[at * C + lane.c] = total;
 }
 
-// The states that enter the segments (REVERSE: the gradients that enter them from
-// behind), in the place of what the segments make of zeros.
-template <bool REVERSE>
-__global__ __launch_bounds__(NT) void scan_fold_kernel(const float* A, const float* carry, Segments sg, int C, int N)
+// The state that enters segment `seg` (REVERSE: the gradient that enters it from
+// behind), from what those before it in order make.
+template <int N, bool REVERSE>
+__device__ __forceinline__ floatx4 enter(const Segments& sg, const Lane<N>& lane, const floatx4& A2, int b, int seg, int C)
 {
     constexpr int W = 8;   // segments read together
-    const int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x, cn = (int64_t)C * N;
-    const int b = blockIdx.y;
-    if (i >= cn)
-        return;
-    const float A2 = A[i] * LOG2E;
-    const int64_t at = (int64_t)b * sg.nseg + (REVERSE ? sg.nseg - 1 : 0), step = REVERSE ? -1 : 1;
-    float* p = sg.state + at * cn + i;
-    const float* q = sg.total + at * C + i / N;
-    float s = carry ? carry[b * cn + i] : 0.f;
-    for (int k = 0; k < sg.nseg; k += W) {
-        float own[W], keep[W];
+    const int order = REVERSE ? sg.nseg - 1 - seg : seg;
+    const int64_t at = (int64_t)b * sg.nseg + (REVERSE ? sg.nseg - 1 : 0);   // of the first in order
+    const int64_t step = REVERSE ? -1 : 1;
+    if (order == 0)
+        return lane.load(sg.state + ((int64_t)b * sg.nseg + (REVERSE ? 0 : sg.nseg - 1)) * C * N);
+    floatx4 h = lane.load(sg.state + at * C * N);
+    for (int k = 1; k < order; k += W) {
+        floatx4 own[W];
+        float d[W];
 #pragma unroll
-        for (int u = 0; u < W; ++u) {   // nothing asks what the last one makes of it
-            own[u] = k + u < sg.nseg - 1 ? p[(k + u) * step * cn] : 0.f;
-            keep[u] = k + u < sg.nseg - 1 ? q[(k + u) * step * C] : 0.f;
+        for (int u = 0; u < W; ++u) {
+            const int64_t i = at + min(k + u, order - 1) * step;
+            own[u] = lane.load(sg.state + i * C * N);
+            d[u] = lane.ok ? sg.total[i * C + lane.c] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < W; ++u)
-            if (k + u < sg.nseg) {
-                p[(k + u) * step * cn] = s;
-                s = __builtin_fmaf(__builtin_amdgcn_exp2f(keep[u] * A2), s, own[u]);
-            }
+            if (k + u < order)
+                h = exp2_4(d[u] * A2) * h + own[u];
     }
+    return h;
 }
 
 // ---- forward -----------------------------------------------------------------
@@ -485,8 +489,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
     floatx4 A2 = lane.load(in.A), h = zero4();
     A2 *= LOG2E;
-    h = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
-                    : lane.load(h_in ? h_in + (int64_t)w.b * C * N : nullptr);
+    h = sg.nseg > 1 ? enter<N, false>(sg, lane, A2, w.b, seg, C) : lane.load(h_in ? h_in + (int64_t)w.b * C * N : nullptr);
     float bias[VN], skip[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
     load_floats<VN>(skip, in.D ? in.D + rows.c : nullptr, rows.nc);
@@ -604,7 +607,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
     const int seg = blockIdx.y;
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
     const floatx4 A2 = lane.load(in.A) * LOG2E;
-    floatx4 g = sg.nseg > 1 ? lane.load(sg.state + ((int64_t)w.b * sg.nseg + seg) * C * N)
+    floatx4 g = sg.nseg > 1 ? enter<N, true>(sg, lane, A2, w.b, seg, C)
                             : lane.load(dh_out ? dh_out + (int64_t)w.b * C * N : nullptr);
     floatx4 dA = zero4();
     typedef WaveSums<L> Sums;
@@ -781,23 +784,44 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
         }
 }
 
-// dA, dD and ddt_bias from the workgroups' sums: 64 columns and 16 slices of the
-// sums a workgroup.
-__global__ __launch_bounds__(1024) void scan_params_kernel(const float* part, int parts, float* dA, float* dD, float* dbias,
-                                                           int64_t cn, int C)
+// The sums over workgroups, in order: db and dc over those of a group's channels, 4
+// values a thread, then (the last `cols` workgroups) dA, dD and ddt_bias over the
+// sequences and segments, 64 columns and 4 slices of the sums a workgroup.
+template <typename OT, int N>
+__global__ __launch_bounds__(NT) void scan_finish_kernel(Grads<OT> out, float* dA, float* dD, float* dbias, const int* n_new,
+                                                         int B, int T_, int C, int G, int blocks, int parts, int cols)
 {
-    __shared__ float sums[16][64];
+    __shared__ float sums[NT / 64][64];
+    const int rows = gridDim.x - cols;
+    if ((int)blockIdx.x < rows) {
+        const int64_t ld = (int64_t)B * T_ * 2 * N, per = (int64_t)T_ * (2 * N / 4), count = per * B * G;
+        for (int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x; i < count; i += (int64_t)rows * NT) {
+            const int64_t r = i % per, t = r / (2 * N / 4);
+            const int b = (int)(i / per % B), g = (int)(i / per / B), at = (int)(r % (2 * N / 4)) * 4;
+            if (n_new && t >= min(max(n_new[b], 0), T_))
+                continue;
+            const float* p = out.proj + ((int64_t)g * blocks * B + b) * T_ * 2 * N + r * 4;
+            floatx4 s = zero4();
+#pragma unroll 8
+            for (int k = 0; k < blocks; ++k)
+                s += *reinterpret_cast<const floatx4*>(p + k * ld);
+            const Act<OT>& o = at < N ? out.db : out.dc;
+            const float v[4] = {s[0], s[1], s[2], s[3]};
+            store_vec<OT, 4>(o.head(b, g) + t * o.st + at % N, v, 4);
+        }
+        return;
+    }
     const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
-    const int64_t i = blockIdx.x * 64ll + col, ld = cn + 2 * C;
+    const int64_t i = (blockIdx.x - rows) * 64ll + col, cn = (int64_t)C * N, ld = cn + 2 * C;
     float s = 0.f;
     if (i < ld)
 #pragma unroll 8
-        for (int q = slice; q < parts; q += 16)
-            s += part[q * ld + i];
+        for (int q = slice; q < parts; q += NT / 64)
+            s += out.params[q * ld + i];
     sums[slice][col] = s;
     __syncthreads();
     if (slice == 0 && i < ld) {
-        for (int q = 1; q < 16; ++q)
+        for (int q = 1; q < NT / 64; ++q)
             s += sums[q][col];
         if (i < cn)
             dA[i] = s;
@@ -807,27 +831,6 @@ __global__ __launch_bounds__(1024) void scan_params_kernel(const float* part, in
         } else if (dbias) {
             dbias[i - cn - C] = s;
         }
-    }
-}
-
-// db and dc over the workgroups of a group's channels, 4 values a thread.
-template <typename OT, int N>
-__global__ __launch_bounds__(NT) void scan_proj_kernel(const float* part, const int* n_new, Act<OT> db, Act<OT> dc, int B,
-                                                       int T_, int blocks)
-{
-    const int b = blockIdx.z, g = blockIdx.y, n = n_new ? min(max(n_new[b], 0), T_) : T_;
-    const int64_t count = (int64_t)n * (2 * N / 4), ld = (int64_t)B * T_ * 2 * N;
-    for (int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x; i < count; i += (int64_t)gridDim.x * NT) {
-        const float* p = part + ((int64_t)g * blocks * B + b) * T_ * 2 * N + i * 4;
-        floatx4 s = zero4();
-#pragma unroll 4
-        for (int k = 0; k < blocks; ++k)
-            s += *reinterpret_cast<const floatx4*>(p + k * ld);
-        const int64_t t = i / (2 * N / 4);
-        const int at = (int)(i % (2 * N / 4)) * 4;
-        const Act<OT>& o = at < N ? db : dc;
-        const float v[4] = {s[0], s[1], s[2], s[3]};
-        store_vec<OT, 4>(o.head(b, g) + t * o.st + at % N, v, 4);
     }
 }
 
@@ -899,7 +902,7 @@ struct Plan {
         const int cw = channels_per_block(d->N);
         blocks = (d->C / d->G + cw - 1) / cw;
         const int64_t wgs = (int64_t)blocks * d->G * d->B;
-        const int64_t want = wgs >= 256 ? 1 : std::min<int64_t>((511 + wgs) / wgs, (d->T + 127) / 128);
+        const int64_t want = wgs >= 256 ? 1 : std::min<int64_t>({(511 + wgs) / wgs, (d->T + 127) / 128, 64});
         const int64_t len = (d->T + want - 1) / want;
         seg = (int)((len + SEG - 1) / SEG * SEG);
         nseg = (int)((d->T + (int64_t)seg - 1) / seg);
@@ -1067,12 +1070,9 @@ linrec_status linrec_scan_fwd(linrec_ctx* ctx, const linrec_scan_desc* d, const 
             const Segments sg = segments(d, p, workspace);
             const In<T> a = inputs<T>(d, in);
             const unsigned wgs = (unsigned)p.blocks * d->G;
-            if (p.nseg > 1) {
-                launch_kernel(scan_sum_kernel<T, N, false>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, n_new, cact<T>(in->x),
-                              sg, d->T, d->C, d->G, p.blocks);
-                launch_kernel(scan_fold_kernel<false>, dim3((unsigned)(((int64_t)d->C * N + NT - 1) / NT), d->B), dim3(NT), s,
-                              in->A, h_in, sg, d->C, N);
-            }
+            if (p.nseg > 1)
+                launch_kernel(scan_sum_kernel<T, N, false>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, h_in, n_new,
+                              cact<T>(in->x), sg, d->T, d->C, d->G, p.blocks);
             launch_kernel(scan_fwd_kernel<T, OT, N>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, h_in, n_new, mact<OT>(y),
                           h_out, (float*)saved, sg, d->T, d->C, d->G, p.blocks);
             return hipGetLastError();
@@ -1130,19 +1130,15 @@ linrec_status linrec_scan_bwd(linrec_ctx* ctx, const linrec_scan_desc* d, const 
                                mact<OT>(out->dz), out->dh_in, params, params + params_floats(d, p)};
             const unsigned wgs = (unsigned)p.blocks * d->G;
             const int64_t cn = (int64_t)d->C * N;
-            if (p.nseg > 1) {
-                launch_kernel(scan_sum_kernel<T, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, n_new, cact<T>(dy), sg,
-                              d->T, d->C, d->G, p.blocks);
-                launch_kernel(scan_fold_kernel<true>, dim3((unsigned)((cn + NT - 1) / NT), d->B), dim3(NT), s, in->A, dh_out,
-                              sg, d->C, N);
-            }
+            if (p.nseg > 1)
+                launch_kernel(scan_sum_kernel<T, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, dh_out, n_new, cact<T>(dy),
+                              sg, d->T, d->C, d->G, p.blocks);
             launch_kernel(scan_bwd_kernel<T, OT, N>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, (const float*)saved,
                           n_new, cact<T>(dy), dh_out, gr, sg, d->T, d->C, d->G, p.blocks);
-            launch_kernel(scan_params_kernel, dim3((unsigned)((cn + 2 * d->C + 63) / 64)), dim3(1024), s, (const float*)gr.params,
-                          d->B * p.nseg, out->dA, out->dD, out->ddt_bias, cn, d->C);
-            const int64_t rounds = ((int64_t)d->T * (2 * N / 4) + NT - 1) / NT;
-            launch_kernel(scan_proj_kernel<OT, N>, dim3((unsigned)std::min<int64_t>(rounds, 4096), d->G, d->B), dim3(NT), s,
-                          (const float*)gr.proj, n_new, gr.db, gr.dc, d->B, d->T, p.blocks);
+            const int cols = (int)((cn + 2 * d->C + 63) / 64);
+            const int64_t rounds = ((int64_t)d->B * d->G * d->T * (2 * N / 4) + NT - 1) / NT;
+            launch_kernel(scan_finish_kernel<OT, N>, dim3((unsigned)std::min<int64_t>(rounds, 8192) + cols), dim3(NT), s, gr,
+                          out->dA, out->dD, out->ddt_bias, n_new, d->B, d->T, d->C, d->G, p.blocks, d->B * p.nseg, cols);
             return hipGetLastError();
         });
     }));
