@@ -104,6 +104,19 @@ __device__ __forceinline__ void steps(float (&d)[VN], const u32x4& v, const floa
             d[j] = softplus(d[j]);
 }
 
+// The steps of a token that is not there are zeros; `last`: the tile may have such
+// tokens (a branch for the workgroup, not a select for every value).
+template <int VN>
+__device__ __forceinline__ void absent(float (&d)[VN], bool last, bool gone)
+{
+    if (last) {
+        asm volatile("");
+#pragma unroll
+        for (int j = 0; j < VN; ++j)
+            d[j] = gone ? 0.f : d[j];
+    }
+}
+
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v)
 {
@@ -221,6 +234,16 @@ struct ChannelSums {
     }
 };
 
+// Waits for loads here, a walk after they were issued: the wait in front of their
+// use would be one for the stores issued in between, too.
+template <int K>
+__device__ __forceinline__ void arrived(u32x4 (&v)[K])
+{
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+        asm volatile("" : "+v"(v[i]));
+}
+
 // ---- the mapping that reads token rows ---------------------------------------
 //
 // A tile is TILE rows of CW channels; a thread takes PV of its 16-byte vectors,
@@ -231,8 +254,10 @@ struct Rows {
     static constexpr int VN = Vec<T>::N, VPR = Geo<N>::CW / VN, COUNT = TILE * VPR, PV = (COUNT + NT - 1) / NT;
     static_assert(NT % VPR == 0 && (COUNT % NT == 0 || COUNT < NT), "whole rounds of one thread's channels");
     int c, nc, row;   // first channel, channels that exist, first row
+    bool whole;       // every thread has a vector of channels that exist
     __device__ __forceinline__ Rows(const Where& w)
     {
+        whole = COUNT >= NT && w.c0 + Geo<N>::CW <= w.cend;
         const int v = threadIdx.x % VPR;
         c = w.c0 + v * VN;
         nc = (int)threadIdx.x < COUNT ? w.cend - c : 0;
@@ -256,6 +281,12 @@ struct Stream {
     // the tile's first `left` rows; the others come as zeros
     __device__ __forceinline__ void load(u32x4 (&v)[R::PV], const R& rows, int left) const
     {
+        if (rows.whole && left >= R::TILE) {
+#pragma unroll
+            for (int i = 0; i < R::PV; ++i)
+                v[i] = *reinterpret_cast<const u32x4*>(at(i));
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < R::PV; ++i)
             v[i] = rows.token(i) < left && rows.nc > 0 ? load_vec(at(i), rows.nc) : u32x4{0u, 0u, 0u, 0u};
@@ -269,16 +300,28 @@ struct Projections {
     static constexpr int TILE = Geo<N>::TILE;
     static constexpr int VN = Vec<T>::N, VPR = N / VN, ONE = TILE * VPR, COUNT = MANY * ONE, PB = (COUNT + NT - 1) / NT;
     u32x4 v[PB];
-    __device__ __forceinline__ void load(const Act<const T>& first, const Act<const T>& second, const Where& w, int t0)
+    const T* p[PB];
+    int64_t step[PB];   // elements from a tile to the next
+    __device__ __forceinline__ Projections(const Act<const T>& first, const Act<const T>& second, const Where& w, int t0, int dir)
     {
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
-            const int k = threadIdx.x + i * NT, r = k % ONE, t = t0 + r / VPR;
+            const int k = threadIdx.x + i * NT, r = k % ONE;
+            const Act<const T>& a = k < ONE ? first : second;
+            p[i] = a.head(w.b, w.g) + (int64_t)(t0 + r / VPR) * a.st + r % VPR * VN;
+            step[i] = dir * TILE * a.st;
+        }
+    }
+    // the tile's first `left` rows (the others come as zeros), and on to the next tile
+    __device__ __forceinline__ void load(int left)
+    {
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            const int k = threadIdx.x + i * NT;
             v[i] = u32x4{0u, 0u, 0u, 0u};
-            if (k < COUNT && t < w.n) {
-                const Act<const T>& a = k < ONE ? first : second;
-                v[i] = *reinterpret_cast<const u32x4*>(a.head(w.b, w.g) + (int64_t)t * a.st + r % VPR * VN);
-            }
+            if ((COUNT % NT == 0 || k < COUNT) && (left >= TILE || k % ONE / VPR < left))
+                v[i] = *reinterpret_cast<const u32x4*>(p[i]);
+            p[i] += step[i];
         }
     }
     __device__ __forceinline__ void store(float (*bc)[TILE][N]) const
@@ -379,15 +422,15 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
     float total = 0.f;
     float bias[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
-    u32x4 xv[PV], dv[PV], zv[PV];
-    Projections<T, N, 1> proj;
+    u32x4 xv[PV], dv[PV], zv[PV] = {};
+    Projections<T, N, 1> proj(REVERSE ? in.c : in.b, in.b, w, first, REVERSE ? -1 : 1);
     Stream<const T, R> xs(REVERSE ? dy : in.x, w, rows, first), ds(in.dt, w, rows, first), zs(in.z, w, rows, first);
     auto fetch = [&](int t0) {
         xs.load(xv, rows, end - t0);
         ds.load(dv, rows, end - t0);
         if (REVERSE && in.z.ptr)
             zs.load(zv, rows, end - t0);
-        proj.load(REVERSE ? in.c : in.b, in.b, w, t0);
+        proj.load(end - t0);
         xs.move(move);
         ds.move(move);
         zs.move(move);
@@ -410,10 +453,7 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
                     u[j] *= z * sigmoid(z);
                 }
             if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT) {
-                if (t0 + TILE > end && t0 + r >= end)
-#pragma unroll
-                    for (int j = 0; j < VN; ++j)
-                        d[j] = 0.f;
+                absent<VN>(d, t0 + TILE > end, t0 + r >= end);
 #pragma unroll
                 for (int j = 0; j < VN; j += 2)
                     *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) = floatx4{d[j], u[j], d[j + 1], u[j + 1]};
@@ -493,8 +533,8 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
     float bias[VN], skip[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
     load_floats<VN>(skip, in.D ? in.D + rows.c : nullptr, rows.nc);
-    u32x4 xv[PV], dv[PV], zv[PV];
-    Projections<T, N, 2> proj;
+    u32x4 xv[PV], dv[PV], zv[PV] = {};
+    Projections<T, N, 2> proj(in.b, in.c, w, begin, 1);
     Stream<const T, R> xs(in.x, w, rows, begin), ds(in.dt, w, rows, begin), zs(in.z, w, rows, begin);
     Stream<OT, R> ys(y, w, rows, begin);
     auto fetch = [&](int t0) {
@@ -502,7 +542,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
         ds.load(dv, rows, end - t0);
         if (in.z.ptr)
             zs.load(zv, rows, end - t0);
-        proj.load(in.b, in.c, w, t0);
+        proj.load(end - t0);
         xs.move(TILE);
         ds.move(TILE);
         zs.move(TILE);
@@ -519,10 +559,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
             float d[VN];
             steps<T, VN>(d, dv[i], bias, in.softplus);
             if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT) {
-                if (t0 + TILE > end && t0 + r >= end)   // a token that is not there leaves the state as it is
-#pragma unroll
-                    for (int j = 0; j < VN; ++j)
-                        d[j] = 0.f;
+                absent<VN>(d, t0 + TILE > end, t0 + r >= end);   // a token that is not there leaves the state as it is
 #pragma unroll
                 for (int j = 0; j < VN; j += 2)
                     *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) =
@@ -555,6 +592,10 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
             }
         }
         __syncthreads();
+        arrived(xv);
+        arrived(dv);
+        arrived(zv);
+        arrived(proj.v);
 #pragma unroll
         for (int i = 0; i < PV; ++i) {
             const int r = rows.token(i);
@@ -621,9 +662,9 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
 #pragma unroll
     for (int j = 0; j < VN; ++j)
         dD[j] = dbias[j] = 0.f;
-    u32x4 xv[PV], dv[PV], zv[PV], gv[PV];
-    Projections<T, N, 2> proj;
+    u32x4 xv[PV], dv[PV], zv[PV] = {}, gv[PV];
     const int last = begin + (end - 1 - begin) / TILE * TILE;
+    Projections<T, N, 2> proj(in.b, in.c, w, last, -1);
     Stream<const T, R> xs(in.x, w, rows, last), ts(in.dt, w, rows, last), zs(in.z, w, rows, last), gs(dy, w, rows, last);
     Stream<OT, R> dxs(out.dx, w, rows, last), dts(out.ddt, w, rows, last), dzs(out.dz, w, rows, last);
     auto fetch = [&](int t0) {
@@ -632,7 +673,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
         if (in.z.ptr)
             zs.load(zv, rows, end - t0);
         gs.load(gv, rows, end - t0);
-        proj.load(in.b, in.c, w, t0);
+        proj.load(end - t0);
         xs.move(-TILE);
         ts.move(-TILE);
         zs.move(-TILE);
@@ -663,10 +704,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
                     dg[i][j] *= __builtin_fmaf(y, 1.f - q, q);
                     e[j] *= y;
                 }
-            if (t0 + TILE > end && t0 + r >= end)   // a token that is not there passes the gradient on (its x and dy are zeros)
-#pragma unroll
-                for (int j = 0; j < VN; ++j)
-                    d[j] = 0.f;
+            absent<VN>(d, t0 + TILE > end, t0 + r >= end);   // a token that is not there passes the gradient on (its x and dy are zeros)
             if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT)
 #pragma unroll
                 for (int j = 0; j < VN; ++j)
@@ -722,6 +760,12 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
             }
         }
         __syncthreads();
+        arrived(xv);
+        arrived(dv);
+        arrived(zv);
+        arrived(gv);
+        arrived(proj.v);
+        asm volatile("" : "+v"(hn));
         // db, dc of this workgroup's channels
         float* pp = out.proj + (((int64_t)blockIdx.x * gridDim.z + w.b) * T_ + t0) * 2 * N;
 #pragma unroll
@@ -902,7 +946,7 @@ struct Plan {
         const int cw = channels_per_block(d->N);
         blocks = (d->C / d->G + cw - 1) / cw;
         const int64_t wgs = (int64_t)blocks * d->G * d->B;
-        const int64_t want = wgs >= 256 ? 1 : std::min<int64_t>({(511 + wgs) / wgs, (d->T + 127) / 128, 64});
+        const int64_t want = wgs >= 320 ? 1 : std::min<int64_t>({(1023 + wgs) / wgs, (d->T + 63) / 64, 64});
         const int64_t len = (d->T + want - 1) / want;
         seg = (int)((len + SEG - 1) / SEG * SEG);
         nseg = (int)((d->T + (int64_t)seg - 1) / seg);
