@@ -227,8 +227,8 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(Act<const T> x, const floa
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 acc[m][j] = 0.f;
-        // token i finishes the sum of token i - (K-1); `own`: i is of this run
-        auto token = [&](int i, const Packed<T, N>& xv, const Packed<T, N>& dv, bool own, bool live) {
+        // token i's dp into the K sums that it is part of, and (own: i is of this run) the taps' gradients
+        auto add = [&](const Packed<T, N>& xv, const Packed<T, N>& dv, bool own, bool live) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float in = xv[j];
@@ -258,6 +258,19 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(Act<const T> x, const floa
                     win[m][j] = win[m + 1][j];
                 win[K - 2][j] = in;
             }
+        };
+        auto shift_sums = [&] {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+#pragma unroll
+                for (int m = 0; m < K - 1; ++m)
+                    acc[m][j] = acc[m + 1][j];
+                acc[K - 1][j] = 0.f;
+            }
+        };
+        // token i finishes the sum of token i - (K-1), which may be of the run before, of the state, or one of the last
+        auto token = [&](int i, const Packed<T, N>& xv, const Packed<T, N>& dv, bool own, bool live) {
+            add(xv, dv, own, live);
             const int at = i - (K - 1);
             if (at < p.n && (at >= p.t0 || p.t0 == 0)) {
                 if (dstate_out && at >= p.n - (K - 1)) {
@@ -272,13 +285,7 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(Act<const T> x, const floa
                 else
                     store_floats<N>(dstate + carry + (int64_t)(at + K - 1) * C, acc[0], p.nc);
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-#pragma unroll
-                for (int m = 0; m < K - 1; ++m)
-                    acc[m][j] = acc[m + 1][j];
-                acc[K - 1][j] = 0.f;
-            }
+            shift_sums();
         };
         const int end = min(p.n, p.t0 + RUN);
         for (int t = p.t0; t < end; t += R) {
@@ -292,10 +299,20 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(Act<const T> x, const floa
                     xv[r].clear();
                     dv[r].clear();
                 }
+            if (t > p.t0 && t + R <= end) {   // inside the run: the sums of tokens t - (K-1) ..
+                static_assert(R >= K - 1, "of the run");
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (t + r < end)
-                    token(t + r, xv[r], dv[r], true, true);
+                for (int r = 0; r < R; ++r) {
+                    add(xv[r], dv[r], true, true);
+                    store_vec<OT, N>(op + (int64_t)(t + r - (K - 1)) * dx.st, acc[0], p.nc);
+                    shift_sums();
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (t + r < end)
+                        token(t + r, xv[r], dv[r], true, true);
+            }
         }
 #pragma unroll
         for (int r = 0; r < K - 1; ++r) {   // the tokens behind: of the next run, or none
@@ -432,7 +449,7 @@ struct Plan {
             ++shift;
         ncg = (vecs + (1 << shift) - 1) >> shift;
         const int64_t lanes = (int64_t)d->B * ncg << shift;
-        run = lanes * ((d->T + 31ll) / 32) >= 2048 * 64 ? 32 : 8;
+        run = lanes * ((d->T + 63ll) / 64) >= 2048 * 64 ? 64 : 8;
         const int span = run * (NT >> shift);
         ntg = (int)((d->T + (int64_t)span - 1) / span);
     }
@@ -544,7 +561,7 @@ linrec_status linrec_conv_fwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
             constexpr int K = decltype(k)::value;
             constexpr bool ACT = decltype(act)::value;
             const Plan p(d, Vec<T>::N);
-            launch_kernel(p.run == 32 ? conv_fwd_kernel<T, OT, K, ACT, 32> : conv_fwd_kernel<T, OT, K, ACT, 8>,
+            launch_kernel(p.run == 64 ? conv_fwd_kernel<T, OT, K, ACT, 64> : conv_fwd_kernel<T, OT, K, ACT, 8>,
                           dim3((unsigned)p.blocks(), d->B), dim3(NT), s, cact<T>(x), w, bias, state_in, n_new, mact<OT>(y),
                           state_out, d->T, d->C, p.ncg, p.shift);
             return hipGetLastError();
@@ -590,7 +607,7 @@ linrec_status linrec_conv_bwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
             const Plan p(d, BWD_VEC);
             float* dstate = (float*)workspace;
             float* part = dstate + round4(state_floats(d));
-            launch_kernel(p.run == 32 ? conv_bwd_kernel<T, OT, K, ACT, 32> : conv_bwd_kernel<T, OT, K, ACT, 8>,
+            launch_kernel(p.run == 64 ? conv_bwd_kernel<T, OT, K, ACT, 64> : conv_bwd_kernel<T, OT, K, ACT, 8>,
                           dim3((unsigned)p.blocks(), d->B), dim3(NT), s, cact<T>(x), w, bias, state_in, n_new, cact<T>(dy),
                           dstate_out, mact<OT>(dx), dstate, part, d->T, d->C, p.ncg, p.shift);
             const int cols = (int)(((int64_t)(K + 1) * d->C + 63) / 64);

@@ -234,6 +234,21 @@ struct ChannelSums {
     }
 };
 
+// A walk's waves drop in priority with each quarter that they have done: of two on
+// a SIMD the older issues first, and would be done long before the younger, which
+// then has the SIMD to itself and cannot fill it.
+__device__ __forceinline__ void pace(int done, int all)
+{
+    if (4 * (int64_t)done < all)
+        __builtin_amdgcn_s_setprio(3);
+    else if (2 * (int64_t)done < all)
+        __builtin_amdgcn_s_setprio(2);
+    else if (4 * (int64_t)(all - done) > all)
+        __builtin_amdgcn_s_setprio(1);
+    else
+        __builtin_amdgcn_s_setprio(0);
+}
+
 // Waits for loads here, a walk after they were issued: the wait in front of their
 // use would be one for the stores issued in between, too.
 template <int K>
@@ -438,6 +453,7 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
     if (begin < end)
         fetch(first);
     for (int t0 = first; t0 >= begin && t0 < end; t0 += move) {
+        pace(REVERSE ? first - t0 : t0 - first, end - begin);
 #pragma unroll
         for (int i = 0; i < PV; ++i) {
             const int r = rows.token(i);
@@ -550,6 +566,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
     if (begin < end)
         fetch(begin);
     for (int t0 = begin; t0 < end; t0 += TILE) {
+        pace(t0 - begin, end - begin);
         u32x4 xc[PV], zc[PV];
 #pragma unroll
         for (int i = 0; i < PV; ++i) {
@@ -686,6 +703,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
         hn = lane.load(sp);
     }
     for (int t0 = last; t0 >= begin && begin < end; t0 -= TILE) {
+        pace(last - t0, end - begin);
         u32x4 xc[PV];
         float ds[PV][VN], dg[PV][VN];   // slope of the step, dy times the slope of the gate
 #pragma unroll
