@@ -198,7 +198,7 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(Act<const T> x, const floa
 // gradient of the K-1 inputs before the piece goes to the workspace (the caller's
 // dstate_in may be its dstate_out, which other workgroups still read).
 template <typename T, typename OT, int K, bool ACT, int RUN>
-__global__ __launch_bounds__(NT) void conv_bwd_kernel(Act<const T> x, const float* w, const float* bias,
+__global__ __launch_bounds__(NT, sizeof(T) == 4 && K == 4 ? 2 : 3) void conv_bwd_kernel(Act<const T> x, const float* w, const float* bias,
                                                       const float* state_in, const int* n_new, Act<const T> dy,
                                                       const float* dstate_out, Act<OT> dx, float* dstate, float* part,
                                                       int T_, int C, int ncg, int shift)
@@ -288,17 +288,27 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(Act<const T> x, const floa
             shift_sums();
         };
         const int end = min(p.n, p.t0 + RUN);
-        for (int t = p.t0; t < end; t += R) {
-            Packed<T, N> xv[R], dv[R];
+        Packed<T, N> xn[R], dn[R];   // R tokens, loaded while those before are added
+        auto load = [&](int t) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (t + r < end) {
-                    xv[r].load(xp + (int64_t)(t + r) * x.st, p.nc);
-                    dv[r].load(dp + (int64_t)(t + r) * dy.st, p.nc);
+                    xn[r].load(xp + (int64_t)(t + r) * x.st, p.nc);
+                    dn[r].load(dp + (int64_t)(t + r) * dy.st, p.nc);
                 } else {
-                    xv[r].clear();
-                    dv[r].clear();
+                    xn[r].clear();
+                    dn[r].clear();
                 }
+        };
+        load(p.t0);
+        for (int t = p.t0; t < end; t += R) {
+            Packed<T, N> xv[R], dv[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                xv[r] = xn[r];
+                dv[r] = dn[r];
+            }
+            load(t + R);
             if (t > p.t0 && t + R <= end) {   // inside the run: the sums of tokens t - (K-1) ..
                 static_assert(R >= K - 1, "of the run");
 #pragma unroll
@@ -438,10 +448,12 @@ __global__ __launch_bounds__(64) void conv_step_kernel(Act<const T> x, const flo
 
 // ---- host ------------------------------------------------------------------
 
-// The runs of a launch: `vec` channels a lane.
+// The runs of a launch: `vec` channels a lane.  Long runs read less twice; they are
+// taken from two waves a SIMD on (4 x 4096 x 2048 bf16 forward, as many: runs of 32
+// tokens 27.5 us, of 8 30.3; 65536 x 2048 backward: of 64 199 us, of 32 215, of 16 251).
 struct Plan {
     int shift, run, ncg, ntg;
-    Plan(const linrec_conv_desc* d, int vec)
+    Plan(const linrec_conv_desc* d, int vec, int longest)
     {
         const int vecs = (d->C + vec - 1) / vec;
         shift = 0;
@@ -449,14 +461,14 @@ struct Plan {
             ++shift;
         ncg = (vecs + (1 << shift) - 1) >> shift;
         const int64_t lanes = (int64_t)d->B * ncg << shift;
-        run = lanes * ((d->T + 63ll) / 64) >= 2048 * 64 ? 64 : 8;
+        run = lanes * (((int64_t)d->T + longest - 1) / longest) >= 2048 * 64 ? longest : 8;
         const int span = run * (NT >> shift);
         ntg = (int)((d->T + (int64_t)span - 1) / span);
     }
     int64_t blocks() const { return (int64_t)ncg * ntg; }
 };
 
-constexpr int BWD_VEC = 4;
+constexpr int BWD_VEC = 4, FWD_RUN = 32, BWD_RUN = 64;
 
 linrec_status check_conv_desc(const linrec_conv_desc* d)
 {
@@ -469,7 +481,7 @@ linrec_status check_conv_desc(const linrec_conv_desc* d)
     if (d->B < 1 || d->B > 32767 || d->C < 1 || d->C > (1 << 20) || d->T < 0 || d->T > LINREC_MAX_T || d->K < 2 || d->K > 4)
         return LINREC_E_SHAPE;
     // a launch holds at most 2^32 - 1 threads along x
-    if (d->T > 0 && Plan(d, BWD_VEC).blocks() * NT > 0xffffffffll)
+    if (d->T > 0 && Plan(d, BWD_VEC, BWD_RUN).blocks() * NT > 0xffffffffll)
         return LINREC_E_SHAPE;
     if (d->act != LINREC_ACT_NONE && d->act != LINREC_ACT_SILU)
         return LINREC_E_LAYOUT;
@@ -530,7 +542,7 @@ size_t linrec_conv_bwd_workspace_bytes(const linrec_conv_desc* d)
 {
     if (check_conv_desc(d) != LINREC_OK || d->T == 0)
         return 0;
-    const Plan p(d, BWD_VEC);
+    const Plan p(d, BWD_VEC, BWD_RUN);
     return (size_t)(round4(state_floats(d)) + round4((int64_t)d->B * p.ntg * (d->K + 1) * d->C)) * sizeof(float);
 }
 
@@ -560,8 +572,8 @@ linrec_status linrec_conv_fwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
             using OT = decltype(o);
             constexpr int K = decltype(k)::value;
             constexpr bool ACT = decltype(act)::value;
-            const Plan p(d, Vec<T>::N);
-            launch_kernel(p.run == 64 ? conv_fwd_kernel<T, OT, K, ACT, 64> : conv_fwd_kernel<T, OT, K, ACT, 8>,
+            const Plan p(d, Vec<T>::N, FWD_RUN);
+            launch_kernel(p.run == FWD_RUN ? conv_fwd_kernel<T, OT, K, ACT, FWD_RUN> : conv_fwd_kernel<T, OT, K, ACT, 8>,
                           dim3((unsigned)p.blocks(), d->B), dim3(NT), s, cact<T>(x), w, bias, state_in, n_new, mact<OT>(y),
                           state_out, d->T, d->C, p.ncg, p.shift);
             return hipGetLastError();
@@ -604,10 +616,10 @@ linrec_status linrec_conv_bwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
             using OT = decltype(o);
             constexpr int K = decltype(k)::value;
             constexpr bool ACT = decltype(act)::value;
-            const Plan p(d, BWD_VEC);
+            const Plan p(d, BWD_VEC, BWD_RUN);
             float* dstate = (float*)workspace;
             float* part = dstate + round4(state_floats(d));
-            launch_kernel(p.run == 64 ? conv_bwd_kernel<T, OT, K, ACT, 64> : conv_bwd_kernel<T, OT, K, ACT, 8>,
+            launch_kernel(p.run == BWD_RUN ? conv_bwd_kernel<T, OT, K, ACT, BWD_RUN> : conv_bwd_kernel<T, OT, K, ACT, 8>,
                           dim3((unsigned)p.blocks(), d->B), dim3(NT), s, cact<T>(x), w, bias, state_in, n_new, cact<T>(dy),
                           dstate_out, mact<OT>(dx), dstate, part, d->T, d->C, p.ncg, p.shift);
             const int cols = (int)(((int64_t)(K + 1) * d->C + 63) / 64);
