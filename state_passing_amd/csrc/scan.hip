@@ -898,6 +898,9 @@ __global__ __launch_bounds__(NT) void scan_finish_kernel(Grads<OT> out, float* d
 
 // ---- token step --------------------------------------------------------------
 
+// Bound by the states' bytes, read once and written once.  What a token needs
+// beside its state is asked for before the slot is known, so that only the state's
+// own latency follows the look at the slots.
 template <typename T, typename OT, int N>
 __global__ __launch_bounds__(NT) void scan_step_kernel(In<T> in, float* S, const int* slots, int nslots, Act<OT> y, int T_,
                                                        int C, int G)
@@ -905,50 +908,59 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(In<T> in, float* S, const
     constexpr int CW = Geo<N>::CW, L = Geo<N>::L;
     const Where w{(int)blockIdx.y, 0, (int)blockIdx.x * CW, C, T_};
     const Lane<N> lane(w);
-    int slot = w.b;
+    const int c = min(lane.c, C - 1), g = c / (C / G);   // (a lane without a channel reads the last one's and writes nothing)
+    const T* xp = in.x.ptr + w.b * in.x.sb + c;
+    const T* dp = in.dt.ptr + w.b * in.dt.sb + c;
+    const T* zp = in.z.ptr ? in.z.ptr + w.b * in.z.sb + c : nullptr;
+    const T* bp = in.b.head(w.b, g) + lane.q * NS;
+    const T* cp = in.c.head(w.b, g) + lane.q * NS;
+    float x, d, z = 0.f;
+    floatx4 bv, cv;
+    auto token = [&](int64_t t) {
+        x = (float)xp[t * in.x.st];
+        d = (float)dp[t * in.dt.st];
+        if (zp)
+            z = (float)zp[t * in.z.st];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            bv[j] = (float)bp[t * in.b.st + j];
+            cv[j] = (float)cp[t * in.c.st + j];
+        }
+    };
+    token(0);
+    const floatx4 A2 = lane.load(in.A) * LOG2E;
+    const float bias = in.dt_bias ? in.dt_bias[c] : 0.f, skip = in.D ? in.D[c] : 0.f;
     OT* yp = y.ptr + w.b * y.sb + lane.c;
+    int slot = w.b;
     if (slots) {
         slot = slots[w.b];
-        int skip = slot < 0 || slot >= nslots;
+        int bad = slot < 0 || slot >= nslots;
         for (int i = threadIdx.x; i < w.b; i += NT)
-            skip |= slots[i] == slot;
-        if (__syncthreads_or(skip)) {
+            bad |= slots[i] == slot;
+        if (__syncthreads_or(bad)) {
             if (lane.ok && lane.q == 0)
                 for (int t = 0; t < T_; ++t)
                     yp[(int64_t)t * y.st] = (OT)0.f;
             return;
         }
     }
-    if (!lane.ok)
-        return;
-    const int g = lane.c / (C / G);
-    floatx4* Sp = reinterpret_cast<floatx4*>(S + ((int64_t)slot * C + lane.c) * N + lane.q * NS);
+    floatx4* Sp = reinterpret_cast<floatx4*>(S + ((int64_t)slot * C + c) * N + lane.q * NS);
     floatx4 h = *Sp;
-    const floatx4 A2 = lane.load(in.A) * LOG2E;
-    const float bias = in.dt_bias ? in.dt_bias[lane.c] : 0.f, skip = in.D ? in.D[lane.c] : 0.f;
-    const T* bp = in.b.head(w.b, g) + lane.q * NS;
-    const T* cp = in.c.head(w.b, g) + lane.q * NS;
     for (int t = 0; t < T_; ++t) {
-        const float x = (float)in.x.ptr[w.b * in.x.sb + (int64_t)t * in.x.st + lane.c];
-        float d = (float)in.dt.ptr[w.b * in.dt.sb + (int64_t)t * in.dt.st + lane.c] + bias;
+        if (t > 0)
+            token(t);
+        d += bias;
         if (in.softplus)
             d = softplus(d);
-        floatx4 bv, cv;
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            bv[j] = (float)bp[(int64_t)t * in.b.st + j];
-            cv[j] = (float)cp[(int64_t)t * in.c.st + j];
-        }
         h = exp2_4(d * A2) * h + (d * x) * bv;
         float o = __builtin_fmaf(skip, x, channel_sum<L>(dot4(cv, h)));
-        if (in.z.ptr) {
-            const float z = (float)in.z.ptr[w.b * in.z.sb + (int64_t)t * in.z.st + lane.c];
+        if (zp)
             o *= z * sigmoid(z);
-        }
-        if (lane.q == 0)
+        if (lane.ok && lane.q == 0)
             yp[(int64_t)t * y.st] = (OT)o;
     }
-    *Sp = h;
+    if (lane.ok)
+        *Sp = h;
 }
 
 // ---- host --------------------------------------------------------------------

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -135,7 +136,7 @@ def _lib():
     lib = ctypes.CDLL(LIB_PATH)
     P, T, D = ctypes.c_void_p, Tensor, ctypes.POINTER(Desc)
     I32, DD, KC = ctypes.c_int32, ctypes.POINTER(DiagDesc), ctypes.POINTER(KvCacheDesc)
-    CD, SD, SI = ctypes.POINTER(ConvDesc), ctypes.POINTER(ScanDesc), ctypes.POINTER(ScanInputs)
+    CD = SD = SI = P   # packed, or structures by reference
     sig = {
         "linrec_ctx_create": ([ctypes.POINTER(P), ctypes.c_int], ctypes.c_int),
         "linrec_ctx_destroy": ([P], ctypes.c_int),
@@ -1065,15 +1066,25 @@ def diag_bwd(g, x, states, dh, dh_out=None, *, form="plain", dg=None, dx=None, d
 
 
 # ----------------------------------------------------------------- state-space layer
+#
+# Descriptions go to the library as packed bytes (the layouts of ConvDesc,
+# ScanDesc and ScanInputs): building the structures takes a token call several
+# times as long.
+
+_CONV = struct.Struct("7i").pack
+_SCAN = struct.Struct("8i").pack
+_SCAN_INPUTS = struct.Struct("23q").pack
 
 def _out_code(dt, out_dtype, *outs):
     """The output type of a call and its code: of the given outputs, else out_dtype, else dt."""
     odt = dt if out_dtype is None else out_dtype
-    given = [t.dtype for t in outs if isinstance(t, torch.Tensor)]
-    if given:
-        odt = given[0]
-        if len(set(given)) > 1:
-            _fail(f"outputs must share one dtype, got {sorted(map(str, set(given)))}", TypeError)
+    for t in outs:
+        if t is not None:
+            given = {t.dtype for t in outs if isinstance(t, torch.Tensor)}
+            if len(given) > 1:
+                _fail(f"outputs must share one dtype, got {sorted(map(str, given))}", TypeError)
+            odt = given.pop() if given else odt
+            break
     code = _CODE.get(odt)
     if code is None:
         _fail(f"unsupported output dtype {odt}", TypeError)
@@ -1084,6 +1095,26 @@ def _new_rows_of(like, dtype, ragged):
     """A new [B,T,C] output as _new_rows; zeros where rows may not be written."""
     t = _new_rows(like, dtype)
     return t.zero_() if ragged else t
+
+
+def _view3(name, t, shape, dtype):
+    """(address, sb, sh, st) of a [B,T,C] activation of this shape and type."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype:
+        sb, st, one = t.stride()
+        if one == 1:
+            return t.data_ptr(), sb, 0, st
+    a = _arg3(name, t, shape, dtype)   # words the error
+    return a.ptr, a.sb, 0, a.st
+
+
+def _view4(name, t, shape, dtype):
+    """(address, sb, sh, st) of a [B,G,T,N] activation of this shape and type."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype:
+        sb, sh, st, one = t.stride()
+        if one == 1:
+            return t.data_ptr(), sb, sh, st
+    a = _arg4(name, t, shape, dtype)
+    return a.ptr, a.sb, a.sh, a.st
 
 
 def _conv_setup(x, w, bias, act, out_dtype, *outs):
@@ -1103,8 +1134,8 @@ def _conv_setup(x, w, bias, act, out_dtype, *outs):
     K = w.shape[1]
     if (B | T | C | K) >> 31:
         _too_large(B, T, C, K)
-    w_ptr = _state_ptr("w", w, (C, K))
-    return shape, ConvDesc(B, T, C, K, kind, code, out), odt, w_ptr, _state_ptr("bias", bias, (C,))
+    return (shape, K, _CONV(B, T, C, K, kind, code, out), odt, _state_ptr("w", w, (C, K)),
+            _state_ptr("bias", bias, (C,)))
 
 
 def conv_fwd(x, w, bias=None, state_in=None, *, act="silu", n_new=None, y=None, state_out=None,
@@ -1115,8 +1146,8 @@ def conv_fwd(x, w, bias=None, state_in=None, *, act="silu", n_new=None, y=None, 
     state_out: fp32 [B,K-1,C], the K-1 inputs before the piece and its last ones.
     n_new: int32 [B] on the device, the first n_new[b] tokens are there (rows
     behind them are left as they were, zeros in a new y).  Returns (y, state_out)."""
-    shape, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, y)
-    carry = (shape[0], d.K - 1, shape[2])
+    shape, K, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, y)
+    carry = (shape[0], K - 1, shape[2])
     xa = _arg3("x", x, shape, x.dtype)
     ya = None if y is None else _arg3("y", y, shape, odt)
     in_ptr, out_ptr = _state_ptr("state_in", state_in, carry), _state_ptr("state_out", state_out, carry)
@@ -1129,7 +1160,7 @@ def conv_fwd(x, w, bias=None, state_in=None, *, act="silu", n_new=None, y=None, 
     if state_out is None:
         state_out = torch.empty(carry, dtype=torch.float32, device=x.device)
         out_ptr = state_out.data_ptr()
-    rc = _lib().linrec_conv_fwd(context(dev), ctypes.byref(d), xa, w_ptr, b_ptr, in_ptr, n_ptr, ya, out_ptr,
+    rc = _lib().linrec_conv_fwd(context(dev), d, xa, w_ptr, b_ptr, in_ptr, n_ptr, ya, out_ptr,
                                 _raw_stream(dev))
     _check(rc, "linrec_conv_fwd")
     return y, state_out
@@ -1140,8 +1171,8 @@ def conv_bwd(x, w, bias, state_in, dy, dstate_out=None, *, act="silu", n_new=Non
     """Backward of conv_fwd over one piece (linrec_conv_bwd), for the loss
     <dy, y> + <dstate_out, state_out>.  Returns (dx, dw, dbias, dstate_in);
     dbias is None without a bias.  dw and dbias are this piece's alone."""
-    shape, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, dx)
-    C, K = shape[2], d.K
+    shape, K, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, dx)
+    C = shape[2]
     carry = (shape[0], K - 1, C)
     xa, da = _arg3("x", x, shape, x.dtype), _arg3("dy", dy, shape, x.dtype)
     dxa = None if dx is None else _arg3("dx", dx, shape, odt)
@@ -1149,7 +1180,7 @@ def conv_bwd(x, w, bias, state_in, dy, dstate_out=None, *, act="silu", n_new=Non
     din_ptr = _state_ptr("dstate_in", dstate_in, carry)
     dw_ptr, db_ptr = _state_ptr("dw", dw, (C, K)), _state_ptr("dbias", dbias, (C,))
     n_ptr = _int_ptr("n_new", n_new, (shape[0],))
-    need = int(_lib().linrec_conv_bwd_workspace_bytes(ctypes.byref(d)))
+    need = int(_lib().linrec_conv_bwd_workspace_bytes(d))
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
     dev = _same_device(x, ("w", w), ("bias", bias), ("state_in", state_in), ("n_new", n_new), ("dy", dy),
@@ -1170,7 +1201,7 @@ def conv_bwd(x, w, bias, state_in, dy, dstate_out=None, *, act="silu", n_new=Non
         din_ptr = dstate_in.data_ptr()
     if workspace is None and need:
         workspace = _bytes(need, x)
-    rc = _lib().linrec_conv_bwd(context(dev), ctypes.byref(d), xa, w_ptr, b_ptr, in_ptr, n_ptr, da, dout_ptr, dxa,
+    rc = _lib().linrec_conv_bwd(context(dev), d, xa, w_ptr, b_ptr, in_ptr, n_ptr, da, dout_ptr, dxa,
                                 dw_ptr, db_ptr, din_ptr, _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_conv_bwd")
     return dx, dw, dbias, dstate_in
@@ -1194,17 +1225,18 @@ def conv_step(x, w, bias, S, *, act="silu", slots=None, y=None, out_dtype=None):
     place.  x: [B,T,C]; S: fp32 [n,K-1,C], entry b at slots[b] (int32 [B] on the
     device) or at b.  An entry whose slot is outside the pool, or taken by an
     earlier entry, is skipped (y = 0).  Returns y."""
-    shape, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, y)
+    shape, K, d, odt, w_ptr, b_ptr = _conv_setup(x, w, bias, act, out_dtype, y)
     B, T, C = shape
     xa = _arg3("x", x, shape, x.dtype)
     ya = None if y is None else _arg3("y", y, shape, odt)
-    S_ptr, n = _pool("S", S, (d.K - 1, C), B, slots)
+    S_ptr, n = _pool("S", S, (K - 1, C), B, slots)
     slot_ptr = _int_ptr("slots", slots, (B,))
     dev = _same_device(x, ("w", w), ("bias", bias), ("S", S), ("slots", slots), ("y", y))
     if y is None:
         y = _new_rows(x, odt)
-        ya = _arg3("y", y, shape, odt)
-    rc = _lib().linrec_conv_step(context(dev), ctypes.byref(d), xa, w_ptr, b_ptr, S_ptr, slot_ptr, n, ya,
+        sb, st, _ = y.stride()
+        ya = Tensor(y.data_ptr(), sb, 0, st)
+    rc = _lib().linrec_conv_step(context(dev), d, xa, w_ptr, b_ptr, S_ptr, slot_ptr, n, ya,
                                  _raw_stream(dev))
     _check(rc, "linrec_conv_step")
     return y
@@ -1228,15 +1260,16 @@ def _scan_setup(x, dt, A, B, C, D, z, dt_bias, softplus, out_dtype, *outs):
         _too_large(n, T, ch, N, G)
     if A is None:
         _fail("A: expected a tensor", TypeError)
-    inputs = ScanInputs(_arg3("x", x, shape, t), _arg3("dt", dt, shape, t), _arg4("B", B, proj, t),
-                        _arg4("C", C, proj, t), _NONE if z is None else _arg3("z", z, shape, t),
-                        _state_ptr("A", A, (ch, N)), _state_ptr("D", D, (ch,)),
-                        _state_ptr("dt_bias", dt_bias, (ch,)))
-    return shape, proj, ScanDesc(n, T, ch, N, G, 1 if softplus else 0, code, out), inputs, odt
+    inputs = _SCAN_INPUTS(*_view3("x", x, shape, t), *_view3("dt", dt, shape, t), *_view4("B", B, proj, t),
+                          *_view4("C", C, proj, t), *((0, 0, 0, 0) if z is None else _view3("z", z, shape, t)),
+                          _state_ptr("A", A, (ch, N)), _state_ptr("D", D, (ch,)) or 0,
+                          _state_ptr("dt_bias", dt_bias, (ch,)) or 0)
+    return shape, proj, _SCAN(n, T, ch, N, G, 1 if softplus else 0, code, out), inputs, odt
 
 
-def scan_saved_bytes(d: ScanDesc) -> int:
-    return int(_lib().linrec_scan_saved_bytes(ctypes.byref(d)))
+def scan_saved_bytes(d) -> int:
+    """Bytes of `saved` for a ScanDesc (as a structure by reference, or packed)."""
+    return int(_lib().linrec_scan_saved_bytes(d))
 
 
 def scan_fwd(x, dt, A, B, C, h_in=None, *, D=None, z=None, dt_bias=None, softplus=True, n_new=None,
@@ -1255,7 +1288,7 @@ def scan_fwd(x, dt, A, B, C, h_in=None, *, D=None, z=None, dt_bias=None, softplu
     ya = None if y is None else _arg3("y", y, shape, odt)
     in_ptr, out_ptr = _state_ptr("h_in", h_in, carry), _state_ptr("h_out", h_out, carry)
     n_ptr = _int_ptr("n_new", n_new, (shape[0],))
-    need = int(_lib().linrec_scan_fwd_workspace_bytes(ctypes.byref(d)))
+    need = int(_lib().linrec_scan_fwd_workspace_bytes(d))
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
     if saved is not None:
@@ -1273,7 +1306,7 @@ def scan_fwd(x, dt, A, B, C, h_in=None, *, D=None, z=None, dt_bias=None, softplu
         saved = _bytes(max(scan_saved_bytes(d), 16), x)
     if workspace is None and need:
         workspace = _bytes(need, x)
-    rc = _lib().linrec_scan_fwd(context(dev), ctypes.byref(d), ctypes.byref(inputs), in_ptr, n_ptr, ya, out_ptr,
+    rc = _lib().linrec_scan_fwd(context(dev), d, inputs, in_ptr, n_ptr, ya, out_ptr,
                                 _ptr(saved), _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_scan_fwd")
     return y, h_out, saved
@@ -1306,7 +1339,7 @@ def scan_bwd(x, dt, A, B, C, saved, dy, dh_out=None, *, D=None, z=None, dt_bias=
     if dz is not None and z is None:
         _fail("dz: there is no z")
     n_ptr = _int_ptr("n_new", n_new, (shape[0],))
-    need = int(_lib().linrec_scan_bwd_workspace_bytes(ctypes.byref(d)))
+    need = int(_lib().linrec_scan_bwd_workspace_bytes(d))
     _check_buffer("saved", saved, scan_saved_bytes(d))
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
@@ -1340,7 +1373,7 @@ def scan_bwd(x, dt, A, B, C, saved, dy, dh_out=None, *, D=None, z=None, dt_bias=
                         deep["dB"] or _arg4("dB", dB, proj, odt), deep["dC"] or _arg4("dC", dC, proj, odt),
                         _NONE if dz is None else rows["dz"] or _arg3("dz", dz, shape, odt),
                         _ptr(dA), _ptr(dD), _ptr(ddt_bias), _ptr(dh_in))
-    rc = _lib().linrec_scan_bwd(context(dev), ctypes.byref(d), ctypes.byref(inputs), _ptr(saved), n_ptr, da, dout_ptr,
+    rc = _lib().linrec_scan_bwd(context(dev), d, inputs, _ptr(saved), n_ptr, da, dout_ptr,
                                 ctypes.byref(out), _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_scan_bwd")
     return ScanGrads(dx, ddt, dA, dB, dC, dh_in, dD, dz, ddt_bias)
@@ -1359,8 +1392,9 @@ def scan_step(x, dt, A, B, C, S, *, D=None, z=None, dt_bias=None, softplus=True,
                        ("S", S), ("slots", slots), ("y", y))
     if y is None:
         y = _new_rows(x, odt)
-        ya = _arg3("y", y, shape, odt)
-    rc = _lib().linrec_scan_step(context(dev), ctypes.byref(d), ctypes.byref(inputs), S_ptr, slot_ptr, n, ya,
+        sb, st, _ = y.stride()
+        ya = Tensor(y.data_ptr(), sb, 0, st)
+    rc = _lib().linrec_scan_step(context(dev), d, inputs, S_ptr, slot_ptr, n, ya,
                                  _raw_stream(dev))
     _check(rc, "linrec_scan_step")
     return y
