@@ -362,7 +362,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 4 && K == 4 ? 2 : 3) void conv_bwd
 // The taps' and the bias's gradients from the workgroups' sums, 64 columns and
 // 16 slices of the sums a workgroup; the last workgroups copy dstate_in.
 template <int K>
-__global__ __launch_bounds__(1024) void conv_finish_kernel(const float* part, int parts, float* dw, float* dbias,
+__global__ __launch_bounds__(1024) void conv_finish_kernel(const float* part, int64_t parts, float* dw, float* dbias,
                                                            const float* dstate, float* dstate_in, int64_t nstate, int C,
                                                            int cols)
 {
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(1024) void conv_finish_kernel(const float* part, in
     float s = 0.f;
     if (i < ld)
 #pragma unroll 8
-        for (int q = slice; q < parts; q += 16)
+        for (int64_t q = slice; q < parts; q += 16)
             s += part[q * ld + i];
     sums[slice][col] = s;
     __syncthreads();
@@ -624,7 +624,7 @@ linrec_status linrec_conv_bwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
                           dstate_out, mact<OT>(dx), dstate, part, d->T, d->C, p.ncg, p.shift);
             const int cols = (int)(((int64_t)(K + 1) * d->C + 63) / 64);
             const int copies = (int)std::min<int64_t>((state_floats(d) + 1023) / 1024, 1024);
-            launch_kernel(conv_finish_kernel<K>, dim3(cols + copies), dim3(1024), s, part, d->B * p.ntg, dw, dbias, dstate,
+            launch_kernel(conv_finish_kernel<K>, dim3(cols + copies), dim3(1024), s, part, (int64_t)d->B * p.ntg, dw, dbias, dstate,
                           dstate_in, state_floats(d), d->C, cols);
             return hipGetLastError();
         });
