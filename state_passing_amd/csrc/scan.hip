@@ -279,6 +279,11 @@ struct Rows {
         row = threadIdx.x / VPR;
     }
     __device__ __forceinline__ int token(int i) const { return row + i * (NT / VPR); }
+    // The places of a row's channels in LDS, 16 bytes each: a thread's channels lie VN places behind those of the
+    // thread beside it, so threads that write their channel j together would meet in 16 / VN groups of banks; xor-ed
+    // by the thread's number among those that meet, they spread.  first(): channel 0's place, channel j's: first() ^ j.
+    static __device__ __forceinline__ int place(int c) { return c ^ (c / 16 & (VN - 1)); }
+    __device__ __forceinline__ int first() const { return place(col()); }
     __device__ __forceinline__ int col() const { return (threadIdx.x % VPR) * VN; }
 };
 
@@ -653,10 +658,10 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
 {
     typedef Rows<T, N> R;
     constexpr int CW = Geo<N>::CW, L = Geo<N>::L, TILE = Geo<N>::TILE, VN = R::VN, PV = R::PV;
-    // a row: d, d x, e, c . h of the channels (G . b in d x's place after the walk), then the sums of q A;
-    // rows are 4 banks apart
-    constexpr int PITCH = 4 * (CW + 1) + CW;
-    __shared__ __attribute__((aligned(16))) float slot[TILE][PITCH];
+    // a row: d, d x, e, c . h of the channels (G . b in d x's place after the walk; in the order of R::place),
+    // then the sums of q A
+    constexpr int PITCH = (5 * CW + 31) / 32 * 32, SUMS = 4 * CW;
+    __shared__ __attribute__((aligned(128))) float slot[TILE][PITCH];
     __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
     __shared__ __attribute__((aligned(16))) float part[NT / 64][TILE][2 * N];
     const Where w = where<N>(n_new, T_, C, G, blocks);
@@ -670,8 +675,9 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
     floatx4 dA = zero4();
     typedef WaveSums<L> Sums;
     // where this lane's sums lie in the rows of its channel and of the tokens
-    float* const own_at = lane.q & 3 ? &slot[0][4 * lane.col + (lane.q & 2 ? 3 : 1)] : &slot[0][4 * (CW + 1) + lane.col];
-    const int own_o = (int)(&slot[0][4 * lane.col + 3] - own_at);   // (L == 2 writes c . h apart)
+    const float* const mine = &slot[0][4 * R::place(lane.col)];
+    float* const own_at = &slot[0][lane.q & 3 ? 4 * R::place(lane.col) + (lane.q & 2 ? 3 : 1) : SUMS + lane.col];
+    const int own_o = (int)(mine + 3 - own_at);   // (L == 2 writes c . h apart)
     float* const part_at = &part[threadIdx.x >> 6][Sums::token()][Sums::set() * N + lane.q * NS + Sums::of()];
     float bias[VN], skip[VN], dD[VN], dbias[VN];
     load_floats<VN>(bias, in.dt_bias ? in.dt_bias + rows.c : nullptr, rows.nc);
@@ -726,7 +732,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
             if (R::COUNT >= NT || (int)threadIdx.x < R::COUNT)
 #pragma unroll
                 for (int j = 0; j < VN; ++j)
-                    *reinterpret_cast<floatx4*>(&slot[r][4 * (rows.col() + j)]) =
+                    *reinterpret_cast<floatx4*>(&slot[0][0] + ((r * PITCH + 4 * rows.first()) ^ 4 * j)) =
                         floatx4{d[j], d[j] * vec_get<T>(xc[i], j), e[j], 0.f};
         }
         proj.store(bc);
@@ -743,7 +749,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
             floatx4 h = h0, hs[BLOCK], as[BLOCK];
 #pragma unroll
             for (int t = 0; t < BLOCK; ++t) {
-                const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
+                const floatx4 s = *reinterpret_cast<const floatx4*>(mine + (tk + t) * PITCH);
                 const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
                 as[t] = exp2_4(s[0] * A2);
                 hs[t] = h = as[t] * h + s[1] * bv;
@@ -751,7 +757,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
             float sb[Sums::TOKENS], sc[Sums::TOKENS];
 #pragma unroll
             for (int t = BLOCK - 1; t >= 0; --t) {
-                const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[tk + t][4 * lane.col]);
+                const floatx4 s = *reinterpret_cast<const floatx4*>(mine + (tk + t) * PITCH);
                 const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][tk + t][lane.q * NS]);
                 const floatx4 cv = *reinterpret_cast<const floatx4*>(&bc[1][tk + t][lane.q * NS]);
                 const floatx4 Gt = g + s[2] * cv;
@@ -802,8 +808,9 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
                 float dx[VN], ddt[VN], dz[VN];
 #pragma unroll
                 for (int j = 0; j < VN; ++j) {
-                    const floatx4 s = *reinterpret_cast<const floatx4*>(&slot[r][4 * (rows.col() + j)]);   // d, G . b, e, c . h
-                    const float x = vec_get<T>(xc[i], j), da = slot[r][4 * (CW + 1) + rows.col() + j];
+                    const floatx4 s =   // d, G . b, e, c . h
+                        *reinterpret_cast<const floatx4*>(&slot[0][0] + ((r * PITCH + 4 * rows.first()) ^ 4 * j));
+                    const float x = vec_get<T>(xc[i], j), da = slot[r][SUMS + rows.col() + j];
                     dx[j] = __builtin_fmaf(s[2], skip[j], s[1] * s[0]);
                     ddt[j] = __builtin_fmaf(s[1], x, da * LN2) * ds[i][j];   // (the walk sums q A in base 2)
                     dz[j] = dg[i][j] * __builtin_fmaf(skip[j], x, s[3]);
