@@ -182,7 +182,7 @@ def _lib():
         "linrec_scan_fwd_workspace_bytes": ([SD], ctypes.c_size_t),
         "linrec_scan_bwd_workspace_bytes": ([SD], ctypes.c_size_t),
         "linrec_scan_fwd": ([P, SD, SI, P, P, T, P, P, P, P], ctypes.c_int),
-        "linrec_scan_bwd": ([P, SD, SI, P, P, T, P, ctypes.POINTER(ScanGradsDesc), P, P], ctypes.c_int),
+        "linrec_scan_bwd": ([P, SD, SI, P, P, T, P, P, P, P], ctypes.c_int),
         "linrec_scan_step": ([P, SD, SI, P, P, I32, T, P], ctypes.c_int),
         "linrec_status_str": ([ctypes.c_int], ctypes.c_char_p),
         "linrec_last_hip_error": ([], ctypes.c_int),
@@ -1068,12 +1068,22 @@ def diag_bwd(g, x, states, dh, dh_out=None, *, form="plain", dg=None, dx=None, d
 # ----------------------------------------------------------------- state-space layer
 #
 # Descriptions go to the library as packed bytes (the layouts of ConvDesc,
-# ScanDesc and ScanInputs): building the structures takes a token call several
+# ScanDesc, ScanInputs and ScanGradsDesc): building the structures takes a token call several
 # times as long.
 
 _CONV = struct.Struct("7i").pack
 _SCAN = struct.Struct("8i").pack
 _SCAN_INPUTS = struct.Struct("23q").pack
+_SCAN_GRADS = struct.Struct("24q").pack
+# The tensors of a call beside x, in the order their devices are compared.
+_CONV_FWD_NAMES = ("w", "bias", "state_in", "n_new", "y", "state_out")
+_CONV_BWD_NAMES = ("w", "bias", "state_in", "n_new", "dy", "dstate_out", "dx", "dw", "dbias", "dstate_in", "workspace")
+_CONV_STEP_NAMES = ("w", "bias", "S", "slots", "y")
+_SCAN_NAMES = ("dt", "A", "B", "C", "D", "z", "dt_bias")
+_SCAN_FWD_NAMES = (*_SCAN_NAMES, "h_in", "n_new", "y", "h_out", "saved", "workspace")
+_SCAN_BWD_NAMES = (*_SCAN_NAMES, "saved", "n_new", "dy", "dh_out", "dx", "ddt", "dB", "dC", "dz", "workspace", "dA", "dD",
+                   "ddt_bias", "dh_in")
+_SCAN_STEP_NAMES = (*_SCAN_NAMES, "S", "slots", "y")
 
 def _out_code(dt, out_dtype, *outs):
     """The output type of a call and its code: of the given outputs, else out_dtype, else dt."""
@@ -1093,8 +1103,20 @@ def _out_code(dt, out_dtype, *outs):
 
 def _new_rows_of(like, dtype, ragged):
     """A new [B,T,C] output as _new_rows; zeros where rows may not be written."""
-    t = _new_rows(like, dtype)
+    t = torch.empty_like(like) if dtype is like.dtype and not like.shape[2] & 7 else _new_rows(like, dtype)
     return t.zero_() if ragged else t
+
+
+def _device_of(first, names, *tensors) -> int:
+    """_same_device with the names apart, paired with the tensors only if it fails."""
+    index = first.get_device()
+    if index >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return index
+    return _same_device(first, *zip(names, tensors))
 
 
 def _view3(name, t, shape, dtype):
@@ -1152,8 +1174,7 @@ def conv_fwd(x, w, bias=None, state_in=None, *, act="silu", n_new=None, y=None, 
     ya = None if y is None else _arg3("y", y, shape, odt)
     in_ptr, out_ptr = _state_ptr("state_in", state_in, carry), _state_ptr("state_out", state_out, carry)
     n_ptr = _int_ptr("n_new", n_new, (shape[0],))
-    dev = _same_device(x, ("w", w), ("bias", bias), ("state_in", state_in), ("n_new", n_new), ("y", y),
-                       ("state_out", state_out))
+    dev = _device_of(x, _CONV_FWD_NAMES, w, bias, state_in, n_new, y, state_out)
     if y is None:
         y = _new_rows_of(x, odt, n_new is not None)
         ya = _arg3("y", y, shape, odt)
@@ -1183,21 +1204,18 @@ def conv_bwd(x, w, bias, state_in, dy, dstate_out=None, *, act="silu", n_new=Non
     need = int(_lib().linrec_conv_bwd_workspace_bytes(d))
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
-    dev = _same_device(x, ("w", w), ("bias", bias), ("state_in", state_in), ("n_new", n_new), ("dy", dy),
-                       ("dstate_out", dstate_out), ("dx", dx), ("dw", dw), ("dbias", dbias),
-                       ("dstate_in", dstate_in), ("workspace", workspace))
+    dev = _device_of(x, _CONV_BWD_NAMES, w, bias, state_in, n_new, dy, dstate_out, dx, dw, dbias, dstate_in, workspace)
     if dx is None:
         dx = _new_rows_of(x, odt, n_new is not None)
         dxa = _arg3("dx", dx, shape, odt)
-    f32 = dict(dtype=torch.float32, device=x.device)
     if dw is None:
-        dw = torch.empty(C, K, **f32)
+        dw = torch.empty_like(w)
         dw_ptr = dw.data_ptr()
     if dbias is None and bias is not None:
-        dbias = torch.empty(C, **f32)
+        dbias = torch.empty_like(bias)
         db_ptr = dbias.data_ptr()
     if dstate_in is None:
-        dstate_in = torch.empty(carry, **f32)
+        dstate_in = torch.empty(carry, dtype=torch.float32, device=x.device)
         din_ptr = dstate_in.data_ptr()
     if workspace is None and need:
         workspace = _bytes(need, x)
@@ -1231,7 +1249,7 @@ def conv_step(x, w, bias, S, *, act="silu", slots=None, y=None, out_dtype=None):
     ya = None if y is None else _arg3("y", y, shape, odt)
     S_ptr, n = _pool("S", S, (K - 1, C), B, slots)
     slot_ptr = _int_ptr("slots", slots, (B,))
-    dev = _same_device(x, ("w", w), ("bias", bias), ("S", S), ("slots", slots), ("y", y))
+    dev = _device_of(x, _CONV_STEP_NAMES, w, bias, S, slots, y)
     if y is None:
         y = _new_rows(x, odt)
         sb, st, _ = y.stride()
@@ -1293,9 +1311,7 @@ def scan_fwd(x, dt, A, B, C, h_in=None, *, D=None, z=None, dt_bias=None, softplu
         _check_buffer("workspace", workspace, need)
     if saved is not None:
         _check_buffer("saved", saved, scan_saved_bytes(d))
-    dev = _same_device(x, ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
-                       ("h_in", h_in), ("n_new", n_new), ("y", y), ("h_out", h_out), ("saved", saved),
-                       ("workspace", workspace))
+    dev = _device_of(x, _SCAN_FWD_NAMES, dt, A, B, C, D, z, dt_bias, h_in, n_new, y, h_out, saved, workspace)
     if y is None:
         y = _new_rows_of(x, odt, n_new is not None)
         ya = _arg3("y", y, shape, odt)
@@ -1343,38 +1359,36 @@ def scan_bwd(x, dt, A, B, C, saved, dy, dh_out=None, *, D=None, z=None, dt_bias=
     _check_buffer("saved", saved, scan_saved_bytes(d))
     if workspace is not None:
         _check_buffer("workspace", workspace, need)
-    rows = {k: t if t is None else _arg3(k, t, shape, odt) for k, t in (("dx", dx), ("ddt", ddt), ("dz", dz))}
-    deep = {k: t if t is None else _arg4(k, t, proj, odt) for k, t in (("dB", dB), ("dC", dC))}
-    flat = {"dA": (dA, (ch, proj[3])), "dD": (dD, (ch,)), "ddt_bias": (ddt_bias, (ch,)), "dh_in": (dh_in, carry)}
-    for k, (t, s) in flat.items():
-        _state_ptr(k, t, s)
-    dev = _same_device(x, ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
-                       ("saved", saved), ("n_new", n_new), ("dy", dy), ("dh_out", dh_out), ("dx", dx), ("ddt", ddt),
-                       ("dB", dB), ("dC", dC), ("dz", dz), ("workspace", workspace),
-                       *((k, t) for k, (t, _) in flat.items()))
-    f32 = dict(dtype=torch.float32, device=x.device)
-    ragged = n_new is not None
-    dx = _new_rows_of(x, odt, ragged) if dx is None else dx
-    ddt = _new_rows_of(x, odt, ragged) if ddt is None else ddt
+    # outputs that are not given are made before the devices are compared: all are described in one go
+    ragged, f32 = n_new is not None, torch.float32
+    if dx is None:
+        dx = _new_rows_of(x, odt, ragged)
+    if ddt is None:
+        ddt = _new_rows_of(x, odt, ragged)
     if z is not None and dz is None:
         dz = _new_rows_of(x, odt, ragged)
     new = torch.zeros if ragged else torch.empty
-    dB = new(proj, dtype=odt, device=x.device) if dB is None else dB
-    dC = new(proj, dtype=odt, device=x.device) if dC is None else dC
-    dA = torch.empty(ch, proj[3], **f32) if dA is None else dA
-    dh_in = torch.empty(carry, **f32) if dh_in is None else dh_in
+    if dB is None:
+        dB = new(proj, dtype=odt, device=x.device)
+    if dC is None:
+        dC = new(proj, dtype=odt, device=x.device)
+    if dA is None:
+        dA = torch.empty_like(A)
     if dD is None and D is not None:
-        dD = torch.empty(ch, **f32)
+        dD = torch.empty_like(D)
     if ddt_bias is None and dt_bias is not None:
-        ddt_bias = torch.empty(ch, **f32)
+        ddt_bias = torch.empty_like(dt_bias)
+    if dh_in is None:
+        dh_in = torch.empty(carry, dtype=f32, device=x.device)
+    out = _SCAN_GRADS(*_view3("dx", dx, shape, odt), *_view3("ddt", ddt, shape, odt), *_view4("dB", dB, proj, odt),
+                      *_view4("dC", dC, proj, odt), *((0, 0, 0, 0) if dz is None else _view3("dz", dz, shape, odt)),
+                      _state_ptr("dA", dA, (ch, proj[3])), _state_ptr("dD", dD, (ch,)) or 0,
+                      _state_ptr("ddt_bias", ddt_bias, (ch,)) or 0, _state_ptr("dh_in", dh_in, carry))
+    dev = _device_of(x, _SCAN_BWD_NAMES, dt, A, B, C, D, z, dt_bias, saved, n_new, dy, dh_out, dx, ddt, dB, dC, dz, workspace,
+                     dA, dD, ddt_bias, dh_in)
     if workspace is None and need:
         workspace = _bytes(need, x)
-    out = ScanGradsDesc(rows["dx"] or _arg3("dx", dx, shape, odt), rows["ddt"] or _arg3("ddt", ddt, shape, odt),
-                        deep["dB"] or _arg4("dB", dB, proj, odt), deep["dC"] or _arg4("dC", dC, proj, odt),
-                        _NONE if dz is None else rows["dz"] or _arg3("dz", dz, shape, odt),
-                        _ptr(dA), _ptr(dD), _ptr(ddt_bias), _ptr(dh_in))
-    rc = _lib().linrec_scan_bwd(context(dev), d, inputs, _ptr(saved), n_ptr, da, dout_ptr,
-                                ctypes.byref(out), _ptr(workspace), _raw_stream(dev))
+    rc = _lib().linrec_scan_bwd(context(dev), d, inputs, _ptr(saved), n_ptr, da, dout_ptr, out, _ptr(workspace), _raw_stream(dev))
     _check(rc, "linrec_scan_bwd")
     return ScanGrads(dx, ddt, dA, dB, dC, dh_in, dD, dz, ddt_bias)
 
@@ -1388,8 +1402,7 @@ def scan_step(x, dt, A, B, C, S, *, D=None, z=None, dt_bias=None, softplus=True,
     ya = None if y is None else _arg3("y", y, shape, odt)
     S_ptr, n = _pool("S", S, (shape[2], proj[3]), shape[0], slots)
     slot_ptr = _int_ptr("slots", slots, (shape[0],))
-    dev = _same_device(x, ("dt", dt), ("A", A), ("B", B), ("C", C), ("D", D), ("z", z), ("dt_bias", dt_bias),
-                       ("S", S), ("slots", slots), ("y", y))
+    dev = _device_of(x, _SCAN_STEP_NAMES, dt, A, B, C, D, z, dt_bias, S, slots, y)
     if y is None:
         y = _new_rows(x, odt)
         sb, st, _ = y.stride()

@@ -267,3 +267,4 @@ def test_packed_descriptions_are_the_structures():
     assert linrec._CONV(*v[:7]) == bytes(linrec.ConvDesc(*v[:7])) and linrec._SCAN(*v) == bytes(linrec.ScanDesc(*v))
     t = [linrec.Tensor(4 * i + 1, 4 * i + 2, 4 * i + 3, 4 * i + 4) for i in range(5)]
     assert linrec._SCAN_INPUTS(*range(1, 24)) == bytes(linrec.ScanInputs(*t, 21, 22, 23))
+    assert linrec._SCAN_GRADS(*range(1, 25)) == bytes(linrec.ScanGradsDesc(*t, 21, 22, 23, 24))
