@@ -30,7 +30,8 @@ Flags: --gpus N (only 1 is supported: one GPU), --steps K, --warmup W,
 for calibrating rocprofv3 byte counters), --profile (run only the
 serialized pass, so a profiler sees undisturbed dispatches), --profile-delta
 and --profile-generation [NAME] (likewise the delta rule's drivers; the calls of
-the elementwise recurrence and the generation operators whose names hold NAME).
+the elementwise recurrence, the generation operators and the state-space layer's
+whose names hold NAME).
 """
 from __future__ import annotations
 
@@ -107,7 +108,8 @@ def parse():
     p.add_argument("--profile-delta", action="store_true",
                    help="run one forward and one backward of the delta-rule workload's sequence drivers only")
     p.add_argument("--profile-generation", nargs="?", const="", default=None, metavar="NAME",
-                   help="run the elementwise recurrence's and the generation operators' workloads only")
+                   help="run the elementwise recurrence's, the generation operators' and the state-space layer's "
+                        "workloads only")
     return p.parse_args()
 
 
@@ -292,7 +294,7 @@ def delta_bench(linrec, dev, args):
 
 def generation_calls(linrec, dev):
     """(name, function that makes three sets of inputs' calls) of the elementwise
-    recurrence and the generation operators."""
+    recurrence, the generation operators and the state-space layer's."""
     import torch
     bf, f32 = torch.bfloat16, torch.float32
     gen = torch.Generator(device=dev).manual_seed(0)
@@ -337,6 +339,32 @@ def generation_calls(linrec, dev):
         at = past - torch.arange(B, device=dev, dtype=torch.int32) * spread // max(B - 1, 1)
         return lambda: linrec.kv_attn(c, q, at, window=window)
 
+    def conv(B, T, C, K, dtype, train):
+        x, dy, S = rand(B, T, C, dtype=dtype), rand(B, T, C, dtype=dtype), rand(B, K - 1, C, dtype=f32)
+        w, bias = rand(C, K, dtype=f32), rand(C, dtype=f32)
+        if T == 1:
+            return lambda: linrec.conv_step(x, w, bias, S)
+
+        def call():
+            linrec.conv_fwd(x, w, bias, S)
+            if train:
+                linrec.conv_bwd(x, w, bias, S, dy)
+        return call
+
+    def scan(B, T, C, N, dtype, train):
+        x, dt, z, dy = (rand(B, T, C, dtype=dtype) for _ in range(4))
+        b, c = rand(B, 1, T, N, dtype=dtype), rand(B, 1, T, N, dtype=dtype)
+        A, S = -torch.rand(C, N, device=dev, generator=gen) * N, rand(B, C, N, dtype=f32)
+        rest = dict(D=rand(C, dtype=f32), z=z, dt_bias=rand(C, dtype=f32) - 4.0)
+        if T == 1:
+            return lambda: linrec.scan_step(x, dt, A, b, c, S, **rest)
+
+        def call():
+            saved = linrec.scan_fwd(x, dt, A, b, c, S, save=train, **rest)[2]
+            if train:
+                linrec.scan_bwd(x, dt, A, b, c, saved, dy, **rest)
+        return call
+
     cases = [
         ("recurrence, 1 token, 64 x 2048, bf16 mix", diag, (64, 1, 2048, bf, "mix", False)),
         ("recurrence, 2 x 4096 x 1024 fp32, forward", diag, (2, 4096, 1024, f32, "plain", False)),
@@ -350,6 +378,13 @@ def generation_calls(linrec, dev):
         ("attention, 1 token, 32 sequences of 12K to 16K, 32 / 8 heads", attn, (32, 1, 32, 8, 128, 64, 16384, 0, 4096)),
         ("attention, 5 tokens, 16 sequences, window 2048, d = 64, pages of 16", attn, (16, 5, 16, 2, 64, 16, 6001, 2048)),
         ("attention, 4096 tokens behind 12K, 16 / 4 heads", attn, (1, 4096, 16, 4, 128, 64, 12288)),
+        ("convolution, 1 token, 64 x 4096, 4 taps", conv, (64, 1, 4096, 4, bf, False)),
+        ("convolution, 4 x 4096 x 2048, forward", conv, (4, 4096, 2048, 4, bf, False)),
+        ("convolution, 65536 x 2048, forward + backward", conv, (1, 65536, 2048, 4, bf, True)),
+        ("scan, 1 token, 128 x 4096 x 16 states", scan, (128, 1, 4096, 16, bf, False)),
+        ("scan, 4 x 4096 x 2048 x 16 states, forward", scan, (4, 4096, 2048, 16, bf, False)),
+        ("scan, 16384 x 2048 x 16 states, forward + backward", scan, (1, 16384, 2048, 16, bf, True)),
+        ("scan, 8 x 2048 x 4096 x 16 states, forward + backward", scan, (8, 2048, 4096, 16, bf, True)),
     ]
     for name, make, args in cases:
         yield name, lambda make=make, args=args: [make(*args) for _ in range(3)]

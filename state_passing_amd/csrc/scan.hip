@@ -62,11 +62,12 @@ __device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf
 
 // log(1 + e^v) = max(v, 0) + log(w), w = 1 + e, e = exp(-|v|).  What w loses of e
 // is added back, which keeps the relative precision of small steps (log(w) is c / w
-// short, and w = 1 up to rounding where c counts).  slope: the derivative.
+// short, and w = 1 up to rounding where c counts).  v = -inf gives 0: a token whose
+// step is hidden so leaves the state as it is.  slope: the derivative.
 __device__ __forceinline__ float softplus(float v)
 {
     const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(v)), w = 1.f + e, c = e - (w - 1.f);
-    return __builtin_fmaf(0.5f, v + fabsf(v), __builtin_fmaf(__builtin_amdgcn_logf(w), LN2, c));
+    return fmaxf(v, 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(w), LN2, c);
 }
 
 __device__ __forceinline__ float softplus(float v, float& slope)
@@ -74,7 +75,7 @@ __device__ __forceinline__ float softplus(float v, float& slope)
     const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(v)), w = 1.f + e, c = e - (w - 1.f);
     const float r = __builtin_amdgcn_rcpf(w);
     slope = v >= 0.f ? r : e * r;
-    return __builtin_fmaf(0.5f, v + fabsf(v), __builtin_fmaf(__builtin_amdgcn_logf(w), LN2, c));
+    return fmaxf(v, 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(w), LN2, c);
 }
 
 // The steps of a vector of channels (and their slopes).
@@ -508,7 +509,7 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
 template <int N, bool REVERSE>
 __device__ __forceinline__ floatx4 enter(const Segments& sg, const Lane<N>& lane, const floatx4& A2, int b, int seg, int C)
 {
-    constexpr int W = 8;   // segments read together
+    constexpr int W = 16;   // segments read together
     const int order = REVERSE ? sg.nseg - 1 - seg : seg;
     const int64_t at = (int64_t)b * sg.nseg + (REVERSE ? sg.nseg - 1 : 0);   // of the first in order
     const int64_t step = REVERSE ? -1 : 1;
@@ -975,7 +976,16 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(In<T> in, float* S, const
 int channels_per_block(int N) { return NT / 64 * 64 / (N / NS); }
 
 // How a piece is split: `blocks` workgroups over the channels of a group, nseg
-// segments of seg tokens.
+// segments of seg tokens.  Segments cost a pass that forms what they make of zeros
+// (0.7 of the forward, 0.25 of the backward), so they are taken where the channels
+// alone leave the GPU short of workgroups: at 256 of them (4 x 2048 x 4096, 16 states)
+// a training step takes as long either way (877 us in one, 871 in four segments), at
+// 512 splitting loses, at 128 (4 x 4096 x 2048) it wins.  Then 1024 workgroups, four a
+// CU: 512 leave the forward 17% slower (16384 x 2048: 188 against 161 us).  At least 64
+// tokens a segment (3 x 1023 x 1000: 60 + 21 us for the two walks, 64 + 26 with 128
+// tokens).  Every segment's workgroup reads what those before it make, so there are at
+// most 128 (65536 x 256: 436 us a step; 64 segments 587, 256 463), or 256 where a
+// segment is one workgroup (32768 x 64: 151 us, with 128 185).
 struct Plan {
     int blocks, nseg, seg;
     Plan(const linrec_scan_desc* d)
@@ -983,7 +993,7 @@ struct Plan {
         const int cw = channels_per_block(d->N);
         blocks = (d->C / d->G + cw - 1) / cw;
         const int64_t wgs = (int64_t)blocks * d->G * d->B;
-        const int64_t want = wgs >= 320 ? 1 : std::min<int64_t>({(1023 + wgs) / wgs, (d->T + 63) / 64, 64});
+        const int64_t want = wgs >= 320 ? 1 : std::min<int64_t>({(1023 + wgs) / wgs, (d->T + 63) / 64, wgs == 1 ? 256 : 128});
         const int64_t len = (d->T + want - 1) / want;
         seg = (int)((len + SEG - 1) / SEG * SEG);
         nseg = (int)((d->T + (int64_t)seg - 1) / seg);

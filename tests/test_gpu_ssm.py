@@ -335,6 +335,54 @@ def test_empty_pieces():
     assert torch.equal(st, c["state"]) and torch.equal(ds, c["dstate"]) and (dw == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_hidden_steps_leave_the_state(dtype):
+    """A raw step of -inf, or of the type's lowest value, is a step of 0: the token changes
+    no state and gets no gradient through its step; its output is that of the state before."""
+    B, T, C, N = 2, 45, 24, 16
+    s, grad = scan_inputs(B, T, C, N, 1, dtype, seed=14)
+    hidden = torch.zeros(T, dtype=torch.bool)
+    hidden[[0, 7, 8, 31, 32, 44]] = True
+    s["dt"][0, hidden.to(DEV)] = float("-inf")
+    s["dt"][1, hidden.to(DEV)] = torch.finfo(dtype).min
+    got = run(s, grad)
+    check(s, grad, got, B, T, C)
+    assert (got["ddt"][:, hidden.to(DEV)] == 0).all()
+    few = dict(s, **{k: s[k][:, ~hidden.to(DEV)] for k in ("x", "dt", "z")}, **{k: s[k][:, :, ~hidden.to(DEV)] for k in ("B", "C")})
+    few_y, few_h, _ = linrec.scan_fwd(*(few[k] for k in ("x", "dt", "A", "B", "C")), few["h_in"],
+                                      **{k: few[k] for k in ("D", "z", "dt_bias")})
+    assert torch.equal(few_y, got["y"][:, ~hidden.to(DEV)]) and torch.equal(few_h, got["h_out"])
+
+
+def test_values_that_are_not_finite_stay_with_their_channel():
+    """An infinite or NaN input spoils its own channel from its token on, and the gradients
+    that sum over it; other channels and sequences, and the tokens before, keep their values."""
+    B, T, C, N = 2, 70, 24, 16
+    s, grad = scan_inputs(B, T, C, N, 1, BF, seed=15)
+    clean = run(s, grad)
+    c = conv_inputs(B, T, C, 4, BF, seed=15)
+    cy, cs = linrec.conv_fwd(c["x"], c["w"], c["bias"], c["state"])
+    cg = linrec.conv_bwd(c["x"], c["w"], c["bias"], c["state"], c["dy"], c["dstate"])
+    for bad in (float("inf"), float("nan")):
+        x = s["x"].clone()
+        x[0, 40, 5] = bad
+        got = run(dict(s, x=x), grad)
+        rest = [k for k in range(C) if k != 5]
+        for k in ("y", "dx", "ddt", "dz"):
+            assert torch.equal(got[k][1], clean[k][1]) and torch.equal(got[k][0][:, rest], clean[k][0][:, rest]), k
+        assert torch.equal(got["y"][0, :40], clean["y"][0, :40]) and not torch.isfinite(got["y"][0, 41:, 5]).any()
+        for k in ("dA", "dD", "ddt_bias"):
+            assert torch.equal(got[k][rest], clean[k][rest]), k
+        assert torch.equal(got["dB"][1], clean["dB"][1]) and torch.equal(got["h_out"][0][rest], clean["h_out"][0][rest])
+        x = c["x"].clone()
+        x[0, T - 1, 5] = bad          # the last one: nothing behind it
+        y, st = linrec.conv_fwd(x, c["w"], c["bias"], c["state"])
+        dx, dw, db, ds = linrec.conv_bwd(x, c["w"], c["bias"], c["state"], c["dy"], c["dstate"])
+        assert torch.equal(y[0, :T - 1], cy[0, :T - 1]) and torch.equal(y[1], cy[1]) and torch.equal(y[0][:, rest], cy[0][:, rest])
+        assert torch.equal(dx[0, :T - 4], cg[0][0, :T - 4]) and torch.equal(dx[0][:, rest], cg[0][0][:, rest])
+        assert torch.equal(dx[1], cg[0][1]) and torch.equal(dw[rest], cg[1][rest]) and torch.equal(ds, cg[3])
+
+
 def test_broadcast_inputs():
     """One sequence's inputs for the whole batch, one projection for all groups: their gradients come entry by entry."""
     B, T, C, N, G = 3, 40, 32, 16, 2
