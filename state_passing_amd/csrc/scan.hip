@@ -284,6 +284,7 @@ struct Rows {
     // thread beside it, so threads that write their channel j together would meet in 16 / VN groups of banks; xor-ed
     // by the thread's number among those that meet, they spread.  first(): channel 0's place, channel j's: first() ^ j.
     static __device__ __forceinline__ int place(int c) { return c ^ (c / 16 & (VN - 1)); }
+    static __device__ __forceinline__ int pair(int p) { return p ^ (p / 16 & (VN / 2 - 1)); }   // likewise 2 channels in 16 bytes
     __device__ __forceinline__ int first() const { return place(col()); }
     __device__ __forceinline__ int col() const { return (threadIdx.x % VPR) * VN; }
 };
@@ -431,6 +432,7 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
     const Where w = where<N>(n_new, T_, C, G, blocks);
     const R rows(w);
     const Lane<N> lane(w);
+    const int at = 2 * R::pair(lane.col / 2) + lane.col % 2;   // where this channel's step lies
     const int seg = REVERSE ? sg.nseg - 1 - blockIdx.y : blockIdx.y;
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
     const int first = REVERSE ? begin + (end - 1 - begin) / TILE * TILE : begin, move = REVERSE ? -TILE : TILE;
@@ -478,7 +480,7 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
                 absent<VN>(d, t0 + TILE > end, t0 + r >= end);
 #pragma unroll
                 for (int j = 0; j < VN; j += 2)
-                    *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) = floatx4{d[j], u[j], d[j + 1], u[j + 1]};
+                    *reinterpret_cast<floatx4*>(&step[r][2 * (R::pair(rows.col() / 2) ^ j / 2)]) = floatx4{d[j], u[j], d[j + 1], u[j + 1]};
             }
         }
         proj.store(bc);
@@ -488,7 +490,7 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
 #pragma unroll 8
         for (int k = 0; k < TILE; ++k) {
             const int t = REVERSE ? TILE - 1 - k : k;
-            const float2 s = step[t][lane.col];
+            const float2 s = step[t][at];
             const floatx4 v = *reinterpret_cast<const floatx4*>(&bc[0][t][lane.q * NS]);
             if constexpr (REVERSE)
                 h = exp2_4(s.x * A2) * (h + s.y * v);
@@ -498,10 +500,10 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
         }
         __syncthreads();
     }
-    const int64_t at = (int64_t)w.b * sg.nseg + seg;
-    lane.store(sg.state + at * C * N, h);
+    const int64_t own = (int64_t)w.b * sg.nseg + seg;
+    lane.store(sg.state + own * C * N, h);
     if (lane.ok && lane.q == 0)
-        sg.total[at * C + lane.c] = total;
+        sg.total[own * C + lane.c] = total;
 }
 
 // The state that enters segment `seg` (REVERSE: the gradient that enters it from
@@ -547,6 +549,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
     const Where w = where<N>(n_new, T_, C, G, blocks);
     const R rows(w);
     const Lane<N> lane(w);
+    const int at = 2 * R::pair(lane.col / 2) + lane.col % 2;   // where this channel's step lies
     const int seg = blockIdx.y;
     const int begin = seg * sg.seg, end = begin + min(max(w.n - begin, 0), sg.seg);
     floatx4 A2 = lane.load(in.A), h = zero4();
@@ -585,7 +588,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
                 absent<VN>(d, t0 + TILE > end, t0 + r >= end);   // a token that is not there leaves the state as it is
 #pragma unroll
                 for (int j = 0; j < VN; j += 2)
-                    *reinterpret_cast<floatx4*>(&step[r][rows.col() + j]) =
+                    *reinterpret_cast<floatx4*>(&step[r][2 * (R::pair(rows.col() / 2) ^ j / 2)]) =
                         floatx4{d[j], d[j] * vec_get<T>(xv[i], j), d[j + 1], d[j + 1] * vec_get<T>(xv[i], j + 1)};
             }
         }
@@ -600,7 +603,7 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
             float o[BLOCK];
 #pragma unroll
             for (int t = 0; t < BLOCK; ++t) {
-                const float2 s = step[k + t][lane.col];
+                const float2 s = step[k + t][at];
                 const floatx4 bv = *reinterpret_cast<const floatx4*>(&bc[0][k + t][lane.q * NS]);
                 h = exp2_4(s.x * A2) * h + s.y * bv;
                 o[t] = dot4(*reinterpret_cast<const floatx4*>(&bc[1][k + t][lane.q * NS]), h);
