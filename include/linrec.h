@@ -635,7 +635,9 @@ linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int3
  * formed in fp32.
  *   n_new: int32 [B] in device memory, the first n_new[b] of the T tokens
  *   (clamped to [0, T]) are there, or NULL: all.  Rows behind them are neither
- *   read nor written; the state that leaves is that of the last token there. */
+ *   read nor written; the state that leaves is that of the last token there.
+ * An input that is not finite reaches its channel's next K outputs, and in the
+ * backward the gradients that those are part of. */
 typedef enum { LINREC_ACT_NONE = 0, LINREC_ACT_SILU = 1 } linrec_act;
 
 typedef struct {
@@ -697,7 +699,12 @@ linrec_status linrec_conv_step(linrec_ctx* ctx, const linrec_conv_desc* d, linre
  * fill whole 16-byte vectors of x and of y; 1 <= B <= 32767, 1 <= C <= 2^20,
  * 0 <= T <= LINREC_MAX_T.  Inputs share `dtype`, outputs `out_dtype` (LINREC_F32
  * when dtype is); states, sums and parameters are fp32.  n_new as for the
- * convolution. */
+ * convolution.
+ * A: finite.  A raw step of -inf (with softplus) is a step of 0: the token, with
+ * finite inputs, leaves the state as it is.  An input that is not finite spoils
+ * its channel from its token on, and the gradients that sum over it.  The result
+ * does not depend on what else is in the batch beyond the split of the piece (a
+ * function of the description). */
 typedef struct {
     int32_t B, T, C, N, G;
     int32_t softplus;         /* 0 or 1 */
