@@ -654,7 +654,8 @@ linrec_status linrec_conv_fwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
                               const int32_t* n_new, linrec_tensor y, float* state_out, void* stream);
 
 /* Bytes of workspace linrec_conv_bwd needs (0 if `d` is invalid or T == 0):
- * the taps' gradients of every workgroup, and dstate_in. */
+ * the taps' gradients of every workgroup, and dstate_in.  16-byte aligned, contents
+ * without meaning before and after; calls that may run at once need their own. */
 size_t linrec_conv_bwd_workspace_bytes(const linrec_conv_desc* d);
 
 /* Backward, for L = <dy, y> + <dstate_out, state_out>, with dp = dy y'(p):
@@ -721,8 +722,10 @@ typedef struct {
 } linrec_scan_inputs;
 
 /* Bytes linrec_scan_fwd writes to `saved` for the backward: the states that
- * enter every block of tokens, fp32.  Bytes of workspace of the two calls.  0 if
- * `d` is invalid or T == 0, or none is needed. */
+ * enter every block of tokens, fp32.  Bytes of workspace of the two calls, 16-byte
+ * aligned, contents without meaning before and after; calls that may run at once
+ * need their own.  0 if `d` is invalid or T == 0, or none is needed (then workspace
+ * may be NULL). */
 size_t linrec_scan_saved_bytes(const linrec_scan_desc* d);
 size_t linrec_scan_fwd_workspace_bytes(const linrec_scan_desc* d);
 size_t linrec_scan_bwd_workspace_bytes(const linrec_scan_desc* d);

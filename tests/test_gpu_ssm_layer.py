@@ -251,3 +251,52 @@ def test_many_segments(C_, t):
             assert (getattr(part, k) - whole[:, sl]).abs().max() <= 5 * t * 2.0 ** -24 * whole.abs().max(), k
     assert (grad - full.dh_in).abs().max() <= 5 * t * 2.0 ** -24 * full.dh_in.abs().max()
     assert (dA - full.dA).abs().max() <= 6 * t * 2.0 ** -24 * full.dA.abs().max()
+
+
+def test_a_large_batch_is_its_sequences():
+    """The variants of large calls (long runs of the convolution, walks that are not
+    split) against the same sequences one call each."""
+    g = torch.Generator(device=DEV).manual_seed(31)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    n_, t, c_ = 17, 1040, 2056
+    x, dy = r(n_, t, c_).bfloat16(), r(n_, t, c_).bfloat16()
+    w, bias, st, dst = r(c_, 4), r(c_), r(n_, 3, c_), r(n_, 3, c_)
+    n = torch.randint(t // 2, t + 1, (n_,), generator=g, device=DEV, dtype=torch.int32)
+    n[3], n[4] = 0, 2
+    y, end = linrec.conv_fwd(x, w, bias, st, n_new=n)
+    dx, dw, db, ds = linrec.conv_bwd(x, w, bias, st, dy, dst, n_new=n)
+    dw1, db1 = torch.zeros_like(dw, dtype=torch.float64), torch.zeros_like(db, dtype=torch.float64)
+    for b in range(n_):
+        at = slice(b, b + 1)
+        y1, end1 = linrec.conv_fwd(x[at], w, bias, st[at], n_new=n[at])
+        dx1, *sums, ds1 = linrec.conv_bwd(x[at], w, bias, st[at], dy[at], dst[at], n_new=n[at])
+        assert torch.equal(y[at], y1) and torch.equal(end[at], end1) and torch.equal(dx[at], dx1) and torch.equal(ds[at], ds1), b
+        dw1 += sums[0]
+        db1 += sums[1]
+    # at most 100 additions follow each other (a run, a workgroup, the workgroups), on terms whose absolute values add
+    # up to about 30 times the largest sum: 3000 2^-24 of it, below n_ t
+    for got, want in ((dw, dw1), (db, db1)):
+        assert (got - want).abs().max() <= n_ * t * 2.0 ** -24 * want.abs().max()
+    n_, t, c_ = 21, 150, 1016                      # 16 workgroups a sequence
+    x, dt, z, dy = (r(n_, t, c_) for _ in range(4))
+    b, c = r(n_, 1, t, N), r(n_, 1, t, N)
+    A, dt_bias, D, h0, e = -r(c_, N).abs() * 8, r(c_) - 4, r(c_), r(n_, c_, N), r(n_, c_, N)
+    n = torch.randint(1, t + 1, (n_,), generator=g, device=DEV, dtype=torch.int32)
+    rest = dict(D=D, dt_bias=dt_bias)
+    y, h, saved = linrec.scan_fwd(x, dt, A, b, c, h0, z=z, n_new=n, save=True, **rest)
+    full = linrec.scan_bwd(x, dt, A, b, c, saved, dy, e, z=z, n_new=n, **rest)
+    sums = {k: 0 for k in ("dA", "dD", "ddt_bias")}
+    # paths of gates joined at other places: a few roundings a token
+    near_ = lambda a, b, k: (a - b).abs().max() <= 6 * t * 2.0 ** -24 * b.abs().max() or pytest.fail(k)  # noqa: E731
+    for i in range(n_):
+        at = slice(i, i + 1)
+        first = (x[at], dt[at], A, b[at], c[at])
+        y1, h1, saved1 = linrec.scan_fwd(*first, h0[at], z=z[at], n_new=n[at], save=True, **rest)
+        part = linrec.scan_bwd(*first, saved1, dy[at], e[at], z=z[at], n_new=n[at], **rest)
+        near_(y[at], y1, "y")
+        near_(h[at], h1, "h_out")
+        for k in ("dx", "ddt", "dz", "dB", "dC", "dh_in"):
+            near_(getattr(full, k)[at], getattr(part, k), k)
+        sums = {k: v + getattr(part, k).double() for k, v in sums.items()}
+    for k, v in sums.items():
+        near_(getattr(full, k), v, k)
