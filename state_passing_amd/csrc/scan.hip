@@ -224,16 +224,18 @@ struct ChannelSums {
     {
         return dpp_add<0xb1>(a);
     }
-    // 4 values, or 3: value 2 is value 3 too
-    static __device__ __forceinline__ void sum(float (&r)[COUNT], const float (&v)[4], bool three = false)
+    // MANY == 3: value 2 is value 3 too; 2: only values 0 and 1 are asked for
+    template <int MANY = 4>
+    static __device__ __forceinline__ void sum(float (&r)[COUNT], const float (&v)[4])
     {
         const bool one = threadIdx.x & 1, two = threadIdx.x & 2;
-        const float a = pick<0xb1>(v[0], v[1], one), b = three ? both(v[3]) : pick<0xb1>(v[2], v[3], one);
+        const float a = pick<0xb1>(v[0], v[1], one);
+        const float b = MANY == 2 ? 0.f : MANY == 3 ? both(v[3]) : pick<0xb1>(v[2], v[3], one);
         if constexpr (L == 2) {
             r[0] = a;
             r[1] = b;
         } else {
-            float s = pick<0x4e>(a, b, two);
+            float s = MANY == 2 ? dpp_add<0x4e>(a) : pick<0x4e>(a, b, two);
             // the 4 (12) lanes beside hold other parts of the same values
             if constexpr (L == 8) {
                 unsigned o = __builtin_amdgcn_update_dpp(0u, __float_as_uint(s), 0x124, 0xf, 0xa, false);   // 4 lanes before
@@ -674,6 +676,10 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(In<T> in, const float* h_i
 // 8 x 2048 x 4096 bf16: 904 us; the same with sums over channels by single shuffles
 // 2250, with the loader's values in the order of the channels in LDS 973, with the
 // saved states read when they are needed 1060.
+// GATE: there is a z.  Without one nothing takes c . h, and its product and sum are
+// left out (4 x 2048 x 2048 x 16 bf16, a training step: 343 us, with them 358).  With
+// one the pointer is asked for all the same: the branches keep the compiler from
+// mixing the vectors' chains, which takes 12 registers more than there are.
 
 template <typename OT>
 struct Grads {
@@ -683,7 +689,7 @@ struct Grads {
     float* proj;     // [G * blocks][B][T][2 N]: db, dc of a workgroup's channels
 };
 
-template <typename T, typename OT, int N>
+template <typename T, typename OT, int N, bool GATE>
 __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* saved, const int* n_new, Act<const T> dy,
                                                       const float* dh_out, Grads<OT> out, Segments sg, int T_, int C, int G,
                                                       int blocks)
@@ -693,6 +699,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
     // a row: d, d x, e, c . h of the channels (G . b in d x's place after the walk; in the order of R::place),
     // then the sums of q A
     constexpr int PITCH = (5 * CW + 31) / 32 * 32, SUMS = 4 * CW;
+    constexpr int MANY = !GATE ? 2 : (L > 2) ? 3 : 4;   // sums over the states of a channel
     __shared__ __attribute__((aligned(128))) float slot[TILE][PITCH];
     __shared__ __attribute__((aligned(16))) float bc[2][TILE][N];
     __shared__ __attribute__((aligned(16))) float part[NT / 64][TILE][2 * N];
@@ -725,7 +732,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
     auto fetch = [&](int t0) {
         xs.load(xv, rows, end - t0);
         ts.load(dv, rows, end - t0);
-        if (in.z.ptr)
+        if (GATE && in.z.ptr)
             zs.load(zv, rows, end - t0);
         gs.load(gv, rows, end - t0);
         proj.load(end - t0);
@@ -753,7 +760,7 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
 #pragma unroll
             for (int j = 0; j < VN; ++j)
                 e[j] = dg[i][j] = vec_get<T>(gv[i], j);
-            if (in.z.ptr)
+            if (GATE && in.z.ptr)
 #pragma unroll
                 for (int j = 0; j < VN; ++j) {
                     const float z = vec_get<T>(zv[i], j), q = sigmoid(z), y = z * q;
@@ -799,10 +806,10 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
                 dA += s[0] * qv;
                 // the channel's lanes write its sums together, and no lane branches
                 float own[ChannelSums<L>::COUNT];
-                const float o = dot4(cv, hs[t]);
-                ChannelSums<L>::sum(own, {dot4(qv, A2), dot4(Gt, bv), o, o}, L > 2);
+                const float o = GATE ? dot4(cv, hs[t]) : 0.f;   // (only dz takes it)
+                ChannelSums<L>::template sum<MANY>(own, {dot4(qv, A2), dot4(Gt, bv), o, o});
 #pragma unroll
-                for (int i = 0; i < ChannelSums<L>::COUNT; ++i)
+                for (int i = 0; i < (GATE ? ChannelSums<L>::COUNT : 1); ++i)
                     own_at[(tk + t) * PITCH + (i ? own_o : 0)] = own[i];
                 sb[t % Sums::TOKENS] = Sums::sum(pb);
                 sc[t % Sums::TOKENS] = Sums::sum(pc);
@@ -845,13 +852,14 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
                     const float x = vec_get<T>(xc[i], j), da = slot[r][SUMS + rows.col() + j];
                     dx[j] = __builtin_fmaf(s[2], skip[j], s[1] * s[0]);
                     ddt[j] = __builtin_fmaf(s[1], x, da * LN2) * ds[i][j];   // (the walk sums q A in base 2)
-                    dz[j] = dg[i][j] * __builtin_fmaf(skip[j], x, s[3]);
+                    if (GATE)
+                        dz[j] = dg[i][j] * __builtin_fmaf(skip[j], x, s[3]);
                     dD[j] = __builtin_fmaf(s[2], x, dD[j]);
                     dbias[j] += ddt[j];
                 }
                 store_vec<OT, VN>(dxs.at(i), dx, rows.nc);
                 store_vec<OT, VN>(dts.at(i), ddt, rows.nc);
-                if (in.z.ptr)
+                if (GATE && in.z.ptr)
                     store_vec<OT, VN>(dzs.at(i), dz, rows.nc);
             }
         }
@@ -1256,8 +1264,9 @@ linrec_status linrec_scan_bwd(linrec_ctx* ctx, const linrec_scan_desc* d, const 
             if (p.nseg > 1)
                 launch_kernel(scan_sum_kernel<T, N, true>, dim3(wgs, p.nseg - 1, d->B), dim3(NT), s, a, dh_out, n_new, cact<T>(dy),
                               sg, d->T, d->C, d->G, p.blocks);
-            launch_kernel(scan_bwd_kernel<T, OT, N>, dim3(wgs, p.nseg, d->B), dim3(NT), s, a, (const float*)saved,
-                          n_new, cact<T>(dy), dh_out, gr, sg, d->T, d->C, d->G, p.blocks);
+            launch_kernel(in->z.ptr ? scan_bwd_kernel<T, OT, N, true> : scan_bwd_kernel<T, OT, N, false>,
+                          dim3(wgs, p.nseg, d->B), dim3(NT), s, a, (const float*)saved, n_new, cact<T>(dy), dh_out, gr, sg,
+                          d->T, d->C, d->G, p.blocks);
             const int cols = (int)((cn + 2 * d->C + 63) / 64);
             const int64_t rounds = ((int64_t)d->B * d->G * d->T * (2 * N / 4) + NT - 1) / NT;
             launch_kernel(scan_finish_kernel<OT, N>, dim3((unsigned)std::min<int64_t>(rounds, 8192) + cols), dim3(NT), s, gr,

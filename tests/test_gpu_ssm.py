@@ -220,6 +220,18 @@ def test_scan_forward_and_backward(B, T, C, N, G, dtype, out, n, options):
     check(s, grad, got, B, T, C, n)
 
 
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype,out", [(BF, None), (BF, F32), (F32, None)])
+def test_scan_without_a_gate(N, dtype, out):
+    """Its backward is a kernel of its own, of every number of states and type; a segmented piece, a group's end."""
+    B, T, C, n = 2, 170, 520 // N + 11, [170, 97]
+    s, grad = scan_inputs(B, T, C, N, dtype=dtype, seed=N, z=False)
+    got = run(s, grad, torch.tensor(n, dtype=torch.int32, device=DEV), out)
+    torch.cuda.synchronize()
+    assert got["dz"] is None
+    check(s, grad, got, B, T, C, n)
+
+
 @pytest.mark.parametrize("N,dtype", [(16, BF), (64, F32), (8, BF), (32, F32)])
 def test_scan_pieces_are_the_whole(N, dtype):
     B, T, C = 2, 330, 24
