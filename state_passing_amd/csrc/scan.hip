@@ -520,6 +520,20 @@ __global__ __launch_bounds__(NT) void scan_sum_kernel(In<T> in, const float* car
         sg.total[own * C + lane.c] = total;
 }
 
+// exp2(2 x) h, a segment's part in what it passes on of h: the product is finite
+// wherever its value is, although exp2(2 x) may not be (a state that grows token by
+// token from a small value, or one that is still zero, which the walk keeps zero).
+// From 2^127 on the half's factor is held there: its square takes every h but zero past
+// the largest number, as the factor itself.
+__device__ __forceinline__ floatx4 across(floatx4 x, const floatx4& h)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        x[j] = fminf(x[j], 127.f);
+    x = exp2_4(x);
+    return x * (x * h);
+}
+
 // The state that enters segment `seg` (REVERSE: the gradient that enters it from
 // behind), from what those before it in order make.
 template <int N, bool REVERSE>
@@ -531,6 +545,8 @@ __device__ __forceinline__ floatx4 enter(const Segments& sg, const Lane<N>& lane
     const int64_t step = REVERSE ? -1 : 1;
     if (order == 0)
         return lane.load(sg.state + ((int64_t)b * sg.nseg + (REVERSE ? 0 : sg.nseg - 1)) * C * N);
+    // (half of A2, not of the sums: a product formed where they are loaded would wait for each)
+    const floatx4 half = 0.5f * A2;
     floatx4 h = lane.load(sg.state + at * C * N);
     for (int k = 1; k < order; k += W) {
         floatx4 own[W];
@@ -544,7 +560,7 @@ __device__ __forceinline__ floatx4 enter(const Segments& sg, const Lane<N>& lane
 #pragma unroll
         for (int u = 0; u < W; ++u)
             if (k + u < order)
-                h = exp2_4(d[u] * A2) * h + own[u];
+                h = across(d[u] * half, h) + own[u];
     }
     return h;
 }
