@@ -630,7 +630,9 @@ linrec_status linrec_kv_attn(linrec_ctx* ctx, const linrec_kv_cache* cache, int3
  * Layouts: x, y, dy, dx are [B, T, C] as for the elementwise recurrence (rows
  * 16-byte aligned, channels contiguous); w: fp32 [C, K], bias: fp32 [C] or NULL
  * (zeros); states: fp32 [B, K-1, C], the oldest input first; all contiguous.
- * K in {2, 3, 4}; 1 <= B <= 32767, 1 <= C <= 2^20, 0 <= T <= LINREC_MAX_T.
+ * K in {2, 3, 4}; 1 <= B <= 32767, 1 <= C <= 2^20, 0 <= T <= LINREC_MAX_T.  A
+ * launch of more than 2^32 - 1 threads a sequence (C T past about 2^40; 2^39 for the
+ * forward of fp32) is refused: LINREC_E_SHAPE.
  * Inputs share `dtype`, outputs `out_dtype` (LINREC_F32 when dtype is); sums are
  * formed in fp32.
  *   n_new: int32 [B] in device memory, the first n_new[b] of the T tokens

@@ -473,6 +473,8 @@ struct Plan {
         ntg = (int)((d->T + (int64_t)span - 1) / span);
     }
     int64_t blocks() const { return (int64_t)ncg * ntg; }
+    // a launch holds at most 2^32 - 1 threads along x
+    bool fits() const { return blocks() * NT <= 0xffffffffll; }
 };
 
 constexpr int BWD_VEC = 4, FWD_RUN = 32, BWD_RUN = 64;
@@ -487,12 +489,20 @@ linrec_status check_conv_desc(const linrec_conv_desc* d)
         return LINREC_E_DTYPE;
     if (d->B < 1 || d->B > 32767 || d->C < 1 || d->C > (1 << 20) || d->T < 0 || d->T > LINREC_MAX_T || d->K < 2 || d->K > 4)
         return LINREC_E_SHAPE;
-    // a launch holds at most 2^32 - 1 threads along x
-    if (d->T > 0 && Plan(d, BWD_VEC, BWD_RUN).blocks() * NT > 0xffffffffll)
+    if (d->T > 0 && !Plan(d, BWD_VEC, BWD_RUN).fits())
         return LINREC_E_SHAPE;
     if (d->act != LINREC_ACT_NONE && d->act != LINREC_ACT_SILU)
         return LINREC_E_LAYOUT;
     return LINREC_OK;
+}
+
+// The forward's own launch: of fp32 it has twice the backward's workgroups (runs half as long).
+linrec_status check_fwd_desc(const linrec_conv_desc* d)
+{
+    const linrec_status st = check_conv_desc(d);
+    if (st != LINREC_OK || d->T == 0)
+        return st;
+    return Plan(d, d->dtype == LINREC_F32 ? Vec<float>::N : Vec<bf16>::N, FWD_RUN).fits() ? LINREC_OK : LINREC_E_SHAPE;
 }
 
 linrec_status check_rows(const linrec_conv_desc* d, const linrec_tensor& t, int dtype, bool out)
@@ -558,7 +568,7 @@ linrec_status linrec_conv_fwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
                               float* state_out, void* stream)
 {
     linrec_status st;
-    if ((st = check_conv_desc(d)) != LINREC_OK || (st = check_state_ptr(state_in, false)) != LINREC_OK ||
+    if ((st = check_fwd_desc(d)) != LINREC_OK || (st = check_state_ptr(state_in, false)) != LINREC_OK ||
         (st = check_state_ptr(state_out, true)) != LINREC_OK)
         return st;
     if (d->T > 0) {

@@ -83,6 +83,24 @@ def test_conv_step_statuses(kw, name):
     status(conv_step(**kw), name)
 
 
+def test_conv_launches_fit():
+    """Every direction's own grid: the fp32 forward has 128 tokens and 256 channels a workgroup, 256 threads
+    each (4096 times 4095 workgroups are the most below 2^32 threads), the others 256 tokens."""
+    wide = 1 << 20
+
+    def fwd(T, dtype):
+        at = rows(sb=T * wide, st=wide)
+        return conv_fwd(d=cd(B=1, T=T, C=wide, dtype=dtype, out=F32), x=at, y=at)
+
+    def bwd(T, dtype):
+        at = rows(sb=T * wide, st=wide)
+        return conv_bwd(d=cd(B=1, T=T, C=wide, dtype=dtype, out=F32), x=at, dy=at, dx=at)
+
+    for call, dtype, most in ((fwd, F32, 4095 * 128), (fwd, BF, 4095 * 256), (bwd, F32, 4095 * 256), (bwd, BF, 4095 * 256)):
+        status(call(most, dtype), "LINREC_E_NULL")      # the context
+        status(call(most + 1, dtype), "LINREC_E_SHAPE")
+
+
 def test_conv_sizes():
     size = lambda d: linrec._lib().linrec_conv_bwd_workspace_bytes(ctypes.byref(d))  # noqa: E731
     assert size(cd(T=0)) == 0 and size(cd(K=7)) == 0 and size(cd(C=0)) == 0
