@@ -12,8 +12,10 @@
 // reads too and nothing else twice.  The backward slides the K-1 unfinished sums
 //   dx_t = sum_k w_k dp_{t+K-1-k},  dp = dy act'(p)
 // the same way, with p formed again from x, and adds dp_t x_{t-K+1+k} into the
-// taps' gradients, summed over a run in registers, over a workgroup through LDS
-// and over workgroups by a second kernel, in a fixed order.
+// taps' gradients, summed over a run in registers (at most 64 tokens), over a workgroup
+// through LDS and over workgroups by a second kernel, in a fixed order.  The last two
+// add in 64 bits, which costs nothing there (both wait for memory); a run's sums would
+// take 40 registers more.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -358,10 +360,10 @@ __global__ __launch_bounds__(NT, sizeof(T) == 4 && K == 4 ? 2 : 3) void conv_bwd
     for (int i = threadIdx.x; i < lanes * (K + 1) * N; i += NT) {
         const int k = i / (lanes * N), col = i % (lanes * N), c = ((int)(blockIdx.x % ncg) << shift) * N + col;
         if (c < C) {
-            float s = 0.f;
+            double s = 0.0;
             for (int r = 0; r < NT >> shift; ++r)
                 s += sums[(r << shift) + col / N][k * N + col % N];
-            out[(int64_t)k * C + c] = s;
+            out[(int64_t)k * C + c] = (float)s;
         }
     }
 }
@@ -373,7 +375,7 @@ __global__ __launch_bounds__(1024) void conv_finish_kernel(const float* part, in
                                                            const float* dstate, float* dstate_in, int64_t nstate, int C,
                                                            int cols)
 {
-    __shared__ float sums[16][64];
+    __shared__ double sums[16][64];
     if ((int)blockIdx.x >= cols) {
         for (int64_t i = (blockIdx.x - cols) * 1024ll + threadIdx.x; i < nstate; i += (gridDim.x - cols) * 1024ll)
             dstate_in[i] = dstate[i];
@@ -381,7 +383,7 @@ __global__ __launch_bounds__(1024) void conv_finish_kernel(const float* part, in
     }
     const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
     const int64_t i = blockIdx.x * 64ll + col, ld = (int64_t)(K + 1) * C;
-    float s = 0.f;
+    double s = 0.0;
     if (i < ld)
 #pragma unroll 8
         for (int64_t q = slice; q < parts; q += 16)
@@ -393,9 +395,9 @@ __global__ __launch_bounds__(1024) void conv_finish_kernel(const float* part, in
             s += sums[q][col];
         const int k = (int)(i / C), c = (int)(i % C);
         if (k < K)
-            dw[(int64_t)c * K + k] = s;
+            dw[(int64_t)c * K + k] = (float)s;
         else if (dbias)
-            dbias[c] = s;
+            dbias[c] = (float)s;
     }
 }
 

@@ -902,21 +902,23 @@ __global__ __launch_bounds__(NT, 2) void scan_bwd_kernel(In<T> in, const float* 
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * CW; i += NT)
         if (w.c0 + i % CW < w.cend) {
-            float s = 0.f;
+            double s = 0.0;
             for (int r = 0; r < ROWS; ++r)
                 s += red[((i / CW) * ROWS + r) * CW + i % CW];
-            pp[(int64_t)C * N + (i / CW) * C + w.c0 + i % CW] = s;
+            pp[(int64_t)C * N + (i / CW) * C + w.c0 + i % CW] = (float)s;
         }
 }
 
 // The sums over workgroups, in order: db and dc over those of a group's channels, 4
 // values a thread, then (the last `cols` workgroups) dA, dD and ddt_bias over the
-// sequences and segments, 64 columns and 4 slices of the sums a workgroup.
+// sequences and segments, 64 columns and 4 slices of the sums a workgroup, in 64 bits:
+// there are up to 32767 sums, and the kernel waits for memory either way.  Within a
+// segment they are added in 32: the walk has no registers for more.
 template <typename OT, int N>
 __global__ __launch_bounds__(NT) void scan_finish_kernel(Grads<OT> out, float* dA, float* dD, float* dbias, const int* n_new,
                                                          int B, int T_, int C, int G, int blocks, int parts, int cols)
 {
-    __shared__ float sums[NT / 64][64];
+    __shared__ double sums[NT / 64][64];
     const int rows = gridDim.x - cols;
     if ((int)blockIdx.x < rows) {
         const int64_t ld = (int64_t)B * T_ * 2 * N, per = (int64_t)T_ * (2 * N / 4), count = per * B * G;
@@ -938,7 +940,7 @@ __global__ __launch_bounds__(NT) void scan_finish_kernel(Grads<OT> out, float* d
     }
     const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
     const int64_t i = (blockIdx.x - rows) * 64ll + col, cn = (int64_t)C * N, ld = cn + 2 * C;
-    float s = 0.f;
+    double s = 0.0;
     if (i < ld)
 #pragma unroll 8
         for (int q = slice; q < parts; q += NT / 64)
@@ -949,12 +951,12 @@ __global__ __launch_bounds__(NT) void scan_finish_kernel(Grads<OT> out, float* d
         for (int q = 1; q < NT / 64; ++q)
             s += sums[q][col];
         if (i < cn)
-            dA[i] = s;
+            dA[i] = (float)s;
         else if (i < cn + C) {
             if (dD)
-                dD[i - cn] = s;
+                dD[i - cn] = (float)s;
         } else if (dbias) {
-            dbias[i - cn - C] = s;
+            dbias[i - cn - C] = (float)s;
         }
     }
 }
