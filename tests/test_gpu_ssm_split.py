@@ -156,3 +156,16 @@ def test_a_small_state_grows_across_a_segment():
     assert (got["h_out"].abs() > 1e3).any()
     want, err = walk(*args, zero, dy, h0, S)
     check(run(*args, None, dy, h0), want, err)
+
+
+@pytest.mark.parametrize("C,N,T,S,count", [(8, 8, 16377, 64, 256), (136, 8, 12279, 96, 128), (70, 16, 8190, 64, 128), (16, 64, 5000, 64, 79)])
+def test_the_most_segments(C, N, T, S, count):
+    """As many segments as a call makes (a workgroup each, and two), with states that live for one to ten or
+    more segments, so that every segment counts in those behind it."""
+    assert segments(1, T, C, N) == count and -(-T // S) == count
+    r, rate = inputs(T, C, N, T)
+    A = (-2 * 10.0 ** (-1.3 * rate)).float().to(F64)                 # -1.1 to -0.1, a hundredth of it a token
+    d = (0.02 * torch.rand(T, C, generator=torch.Generator().manual_seed(3))).to(F64)
+    args = (r(T, C), d, A, r(T, N), r(T, N), r(C, N), r(T, C), r(C, N))
+    want, err = walk(*args, S)
+    check(run(*args), want, err)
