@@ -192,3 +192,80 @@ def test_scan_walks_that_are_not_split(N):
         one = lambda v: {k: t[b:b + 1] if isinstance(t, torch.Tensor) and t.shape[0] == B else t for k, t in v.items()}  # noqa: E731
         mine = {k: t for k, t in one(got).items() if k not in ("dA", "dD", "ddt_bias")}
         check(one(s), one(grad), mine, 1, T, C, n[b:b + 1])
+
+
+# ----------------------------------------------------------------- ends of the ranges
+
+def first_of(s):
+    return [s[k] for k in ("x", "dt", "A", "B", "C")]
+
+
+def test_the_most_sequences():
+    """32767 of them: three equal the calls of their own, forward, backward and as tokens of a pool."""
+    B, T, C, N = 32767, 3, 8, 8
+    at = torch.tensor([0, 12345, B - 1], device=DEV)
+    s, grad = scan_inputs(B, T, C, N, seed=1)
+    some = lambda v: {k: t[at].contiguous() if isinstance(t, torch.Tensor) and t.shape[0] == B else t for k, t in v.items()}  # noqa: E731
+    n = torch.randint(0, T + 1, (B,), generator=gen(4), dtype=torch.int32).to(DEV)
+    got, want = scan_run(s, grad, n), scan_run(some(s), some(grad), n[at])
+    for k, t in want.items():
+        if k not in ("dA", "dD", "ddt_bias"):
+            assert torch.equal(got[k][at], t), k
+    rest = {k: s[k] for k in ("D", "dt_bias")}
+    S, slots = torch.randn(B, C, N, generator=gen(5)).to(DEV), torch.randperm(B, generator=gen(6)).to(torch.int32).to(DEV)
+    mine = S[slots[at].long()].clone()
+    y = linrec.scan_step(*first_of(s), S, z=s["z"], slots=slots, **rest)
+    few = some(s)
+    assert torch.equal(y[at], linrec.scan_step(*first_of(few), mine, z=few["z"], **rest)) and torch.equal(S[slots[at].long()], mine)
+    c = conv_inputs(B, T, C, 4, BF, seed=2)
+    few = some(c)
+    for a, b in zip(linrec.conv_fwd(c["x"], c["w"], c["bias"], c["state"], n_new=n),
+                    linrec.conv_fwd(few["x"], c["w"], c["bias"], few["state"], n_new=n[at])):
+        assert torch.equal(a[at], b)
+    a = linrec.conv_bwd(c["x"], c["w"], c["bias"], c["state"], c["dy"], c["dstate"], n_new=n)
+    b = linrec.conv_bwd(few["x"], c["w"], c["bias"], few["state"], few["dy"], few["dstate"], n_new=n[at])
+    assert torch.equal(a[0][at], b[0]) and torch.equal(a[3][at], b[3])
+    W = torch.randn(B, 3, C, generator=gen(7)).to(DEV)
+    mine = W[slots[at].long()].clone()
+    y = linrec.conv_step(c["x"], c["w"], c["bias"], W, slots=slots)
+    assert torch.equal(y[at], linrec.conv_step(few["x"], c["w"], c["bias"], mine)) and torch.equal(W[slots[at].long()], mine)
+
+
+@pytest.mark.parametrize("C,G,N", [(1 << 20, 1, 8), (65535 * 8, 65535, 8), (1 << 20, 2, 64)])
+def test_the_most_channels_and_groups(C, G, N):
+    """The last channels (of the last group) equal a call of their own."""
+    T, few = 2, 8
+    s, grad = scan_inputs(1, T, C, N, G, seed=1)
+
+    def last(v):
+        out = {}
+        for k, t in v.items():
+            if k in ("B", "C"):
+                t = t[:, -1:]
+            elif k in ("A", "D", "dt_bias"):
+                t = t[-few:]
+            elif k in ("h_in", "dh_out"):
+                t = t[:, -few:].contiguous()
+            elif isinstance(t, torch.Tensor):
+                t = t[..., -few:]
+            out[k] = t
+        return out
+
+    got, want = scan_run(s, grad), scan_run(last(s), last(grad))
+    for k in ("y", "dx", "ddt", "dz"):
+        assert torch.equal(got[k][..., -few:], want[k]), k
+    for k in ("h_out", "dh_in"):
+        assert torch.equal(got[k][:, -few:], want[k]), k
+    for k in ("dA", "dD", "ddt_bias"):
+        assert torch.equal(got[k][-few:], want[k]), k
+    if C // G == few:
+        assert torch.equal(got["dB"][:, -1:], want["dB"]) and torch.equal(got["dC"][:, -1:], want["dC"])
+    if G > 2:
+        return
+    c = conv_inputs(1, T, C, 4, BF, seed=2)
+    part = {k: t[-few:] if k in ("w", "bias") else t[..., -few:].contiguous() for k, t in c.items()}
+    order = ("x", "w", "bias", "state")
+    assert torch.equal(linrec.conv_fwd(*(c[k] for k in order))[0][..., -few:], linrec.conv_fwd(*(part[k] for k in order))[0])
+    order += ("dy", "dstate")
+    a, b = linrec.conv_bwd(*(c[k] for k in order)), linrec.conv_bwd(*(part[k] for k in order))
+    assert torch.equal(a[0][..., -few:], b[0]) and torch.equal(a[1][-few:], b[1]) and torch.equal(a[2][-few:], b[2])
