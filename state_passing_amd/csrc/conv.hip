@@ -69,13 +69,6 @@ struct Packed {
     }
 };
 
-__device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf(1.f + __expf(-p)); }
-
-__device__ __forceinline__ int tokens_of(const int* n_new, int b, int T_)
-{
-    return n_new ? min(max(n_new[b], 0), T_) : T_;
-}
-
 // Taps and bias of N channels.
 template <int N, int K>
 __device__ __forceinline__ void load_taps(float (&w)[K][N], float (&bias)[N], const float* wp, const float* bp, int c0, int nc)
@@ -507,11 +500,6 @@ linrec_status check_fwd_desc(const linrec_conv_desc* d)
     return Plan(d, d->dtype == LINREC_F32 ? Vec<float>::N : Vec<bf16>::N, FWD_RUN).fits() ? LINREC_OK : LINREC_E_SHAPE;
 }
 
-linrec_status check_rows(const linrec_conv_desc* d, const linrec_tensor& t, int dtype, bool out)
-{
-    return check_view(linrec_tensor{t.ptr, t.sb, 0, t.st}, d->B, 1, d->T, d->C, elem_size(dtype), out);
-}
-
 linrec_status check_taps(const float* w, const float* bias)
 {
     if (!w)
@@ -539,16 +527,6 @@ hipError_t dispatch(const linrec_conv_desc* d, F&& f)
 }
 
 int64_t state_floats(const linrec_conv_desc* d) { return (int64_t)d->B * (d->K - 1) * d->C; }
-
-int64_t round4(int64_t n) { return (n + 3) / 4 * 4; }
-
-linrec_status pass(const linrec_conv_desc* d, const float* in, float* out, hipStream_t s)
-{
-    if (in == out)
-        return LINREC_OK;
-    LAUNCH(launch_carry_copy(in, out, state_floats(d), s));
-    return LINREC_OK;
-}
 
 }  // namespace
 }  // namespace linrec
@@ -584,7 +562,7 @@ linrec_status linrec_conv_fwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
         return st;
     hipStream_t s = (hipStream_t)stream;
     if (d->T == 0)
-        return pass(d, state_in, state_out, s);
+        return pass_carry(state_in, state_out, state_floats(d), s);
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_CONV_FWD, s, [&] {
         return dispatch(d, [&](auto t, auto o, auto k, auto act) {
             using T = decltype(t);
@@ -627,7 +605,7 @@ linrec_status linrec_conv_bwd(linrec_ctx* ctx, const linrec_conv_desc* d, linrec
         LAUNCH(launch_carry_copy(nullptr, dw, (int64_t)d->C * d->K, s));
         if (dbias)
             LAUNCH(launch_carry_copy(nullptr, dbias, d->C, s));
-        return pass(d, dstate_out, dstate_in, s);
+        return pass_carry(dstate_out, dstate_in, state_floats(d), s);
     }
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_CONV_BWD, s, [&] {
         return dispatch(d, [&](auto t, auto o, auto k, auto act) {

@@ -525,11 +525,6 @@ linrec_status check_diag_desc(const linrec_diag_desc* d)
     return LINREC_OK;
 }
 
-linrec_status check_diag_rows(const linrec_diag_desc* d, const linrec_tensor& t, int dtype, bool out)
-{
-    return check_view(linrec_tensor{t.ptr, t.sb, 0, t.st}, d->B, 1, d->T, d->C, elem_size(dtype), out);
-}
-
 // Calls f with (input type, output type, mix) of the description.
 template <typename F>
 hipError_t dispatch(const linrec_diag_desc* d, F&& f)
@@ -648,9 +643,9 @@ linrec_status linrec_diag_fwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec
         (st = check_state_ptr(h_out, true)) != LINREC_OK)
         return st;
     if (d->T > 0) {
-        if ((st = check_diag_rows(d, g, d->dtype, false)) != LINREC_OK ||
-            (st = check_diag_rows(d, x, d->dtype, false)) != LINREC_OK ||
-            (st = check_diag_rows(d, h, d->out_dtype, true)) != LINREC_OK ||
+        if ((st = check_rows(d, g, d->dtype, false)) != LINREC_OK ||
+            (st = check_rows(d, x, d->dtype, false)) != LINREC_OK ||
+            (st = check_rows(d, h, d->out_dtype, true)) != LINREC_OK ||
             (st = check_buffer(states)) != LINREC_OK)
             return st;
         if (d->T > SEG && (st = check_buffer(workspace)) != LINREC_OK)
@@ -676,11 +671,11 @@ linrec_status linrec_diag_bwd(linrec_ctx* ctx, const linrec_diag_desc* d, linrec
         (st = check_state_ptr(dh_in, true)) != LINREC_OK)
         return st;
     if (d->T > 0) {
-        if ((st = check_diag_rows(d, g, d->dtype, false)) != LINREC_OK ||
-            (st = check_diag_rows(d, x, d->dtype, false)) != LINREC_OK ||
-            (st = check_diag_rows(d, dh, d->dtype, false)) != LINREC_OK ||
-            (st = check_diag_rows(d, dg, d->out_dtype, true)) != LINREC_OK ||
-            (st = check_diag_rows(d, dx, d->out_dtype, true)) != LINREC_OK ||
+        if ((st = check_rows(d, g, d->dtype, false)) != LINREC_OK ||
+            (st = check_rows(d, x, d->dtype, false)) != LINREC_OK ||
+            (st = check_rows(d, dh, d->dtype, false)) != LINREC_OK ||
+            (st = check_rows(d, dg, d->out_dtype, true)) != LINREC_OK ||
+            (st = check_rows(d, dx, d->out_dtype, true)) != LINREC_OK ||
             (st = check_buffer(states)) != LINREC_OK)
             return st;
         if (d->T > SEG && (st = check_buffer(workspace)) != LINREC_OK)

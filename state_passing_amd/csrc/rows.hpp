@@ -1,5 +1,6 @@
 // rows.hpp -- token rows [B, T, C] with the channel index contiguous, read and
-// written 16 bytes at a time, and carried fp32 states beside them.
+// written 16 bytes at a time, and carried fp32 states beside them; what the calls on
+// such rows check and share.
 #pragma once
 
 #include "ctx.hpp"
@@ -98,6 +99,31 @@ __device__ __forceinline__ void store_floats(float* p, const float (&y)[N], int 
             if (j < n)
                 p[j] = y[j];
     }
+}
+
+__device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf(1.f + __expf(-p)); }
+
+// Tokens of sequence b that are there.
+__device__ __forceinline__ int tokens_of(const int* n_new, int b, int T_)
+{
+    return n_new ? min(max(n_new[b], 0), T_) : T_;
+}
+
+template <typename D>
+inline linrec_status check_rows(const D* d, const linrec_tensor& t, int dtype, bool out)
+{
+    return check_view(linrec_tensor{t.ptr, t.sb, 0, t.st}, d->B, 1, d->T, d->C, elem_size(dtype), out);
+}
+
+inline int64_t round4(int64_t n) { return (n + 3) / 4 * 4; }
+
+// What an empty piece does: n floats of carry from `in` (NULL: zeros) to `out`.
+inline linrec_status pass_carry(const float* in, float* out, int64_t n, hipStream_t s)
+{
+    if (in == out)
+        return LINREC_OK;
+    LAUNCH(launch_carry_copy(in, out, n, s));
+    return LINREC_OK;
 }
 
 template <typename T>

@@ -66,11 +66,9 @@ __device__ __forceinline__ Where where(const int* n_new, int T_, int C, int G, i
     w.g = blockIdx.x / blocks;
     w.c0 = w.g * cg + (int)(blockIdx.x % blocks) * Geo<N>::CW;
     w.cend = (w.g + 1) * cg;
-    w.n = n_new ? min(max(n_new[w.b], 0), T_) : T_;
+    w.n = tokens_of(n_new, w.b, T_);
     return w;
 }
-
-__device__ __forceinline__ float sigmoid(float p) { return __builtin_amdgcn_rcpf(1.f + __expf(-p)); }
 
 // log(1 + e^v) = max(v, 0) + log(w), w = 1 + e, e = exp(-|v|).  What w loses of e
 // is added back, which keeps the relative precision of small steps (log(w) is c / w
@@ -925,7 +923,7 @@ __global__ __launch_bounds__(NT) void scan_finish_kernel(Grads<OT> out, float* d
         for (int64_t i = blockIdx.x * (int64_t)NT + threadIdx.x; i < count; i += (int64_t)rows * NT) {
             const int64_t r = i % per, t = r / (2 * N / 4);
             const int b = (int)(i / per % B), g = (int)(i / per / B), at = (int)(r % (2 * N / 4)) * 4;
-            if (n_new && t >= min(max(n_new[b], 0), T_))
+            if (t >= tokens_of(n_new, b, T_))
                 continue;
             const float* p = out.proj + ((int64_t)g * blocks * B + b) * T_ * 2 * N + r * 4;
             floatx4 s = zero4();
@@ -1077,11 +1075,6 @@ linrec_status check_scan_desc(const linrec_scan_desc* d)
     return LINREC_OK;
 }
 
-linrec_status check_rows(const linrec_scan_desc* d, const linrec_tensor& t, int dtype, bool out)
-{
-    return check_view(linrec_tensor{t.ptr, t.sb, 0, t.st}, d->B, 1, d->T, d->C, elem_size(dtype), out);
-}
-
 linrec_status check_proj(const linrec_scan_desc* d, const linrec_tensor& t, int dtype, bool out)
 {
     return check_view(t, d->B, d->G, d->T, d->N, elem_size(dtype), out);
@@ -1130,8 +1123,6 @@ hipError_t dispatch(const linrec_scan_desc* d, F&& f)
     return d->out_dtype == LINREC_F32 ? states(bf16{}, float{}) : states(bf16{}, bf16{});
 }
 
-int64_t round4(int64_t n) { return (n + 3) / 4 * 4; }
-
 int64_t state_floats(const linrec_scan_desc* d) { return (int64_t)d->B * d->C * d->N; }
 
 // The segments' part of a workspace.
@@ -1149,14 +1140,6 @@ Segments segments(const linrec_scan_desc* d, const Plan& p, void* workspace)
 int64_t params_floats(const linrec_scan_desc* d, const Plan& p)
 {
     return round4((int64_t)d->B * p.nseg * ((int64_t)d->C * d->N + 2 * d->C));
-}
-
-linrec_status pass(const linrec_scan_desc* d, const float* in, float* out, hipStream_t s)
-{
-    if (in == out)
-        return LINREC_OK;
-    LAUNCH(launch_carry_copy(in, out, state_floats(d), s));
-    return LINREC_OK;
 }
 
 }  // namespace
@@ -1209,7 +1192,7 @@ linrec_status linrec_scan_fwd(linrec_ctx* ctx, const linrec_scan_desc* d, const 
         return st;
     hipStream_t s = (hipStream_t)stream;
     if (d->T == 0)
-        return pass(d, h_in, h_out, s);
+        return pass_carry(h_in, h_out, state_floats(d), s);
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_SCAN_FWD, s, [&] {
         return dispatch(d, [&](auto t, auto o, auto n) {
             using T = decltype(t);
@@ -1264,7 +1247,7 @@ linrec_status linrec_scan_bwd(linrec_ctx* ctx, const linrec_scan_desc* d, const 
             LAUNCH(launch_carry_copy(nullptr, out->dD, d->C, s));
         if (out->ddt_bias)
             LAUNCH(launch_carry_copy(nullptr, out->ddt_bias, d->C, s));
-        return pass(d, dh_out, out->dh_in, s);
+        return pass_carry(dh_out, out->dh_in, state_floats(d), s);
     }
     LAUNCH(timed_launch(ctx, LINREC_KERNEL_SCAN_BWD, s, [&] {
         return dispatch(d, [&](auto t, auto o, auto n) {
