@@ -385,6 +385,7 @@ def generation_calls(linrec, dev):
         ("scan, 4 x 4096 x 2048 x 16 states, forward", scan, (4, 4096, 2048, 16, bf, False)),
         ("scan, 16384 x 2048 x 16 states, forward + backward", scan, (1, 16384, 2048, 16, bf, True)),
         ("scan, 8 x 2048 x 4096 x 16 states, forward + backward", scan, (8, 2048, 4096, 16, bf, True)),
+        ("scan, 4 x 2048 x 512 x 64 states, forward + backward", scan, (4, 2048, 512, 64, bf, True)),
     ]
     for name, make, args in cases:
         yield name, lambda make=make, args=args: [make(*args) for _ in range(3)]

@@ -5,7 +5,7 @@
 // Bound by HBM: 2 elements a token and channel forward, 3 backward.  65536 x 2048
 // bf16, 4 taps, silu: 98-101 us forward (5.4 TB/s: a part comes from the last-level
 // cache), 188 us backward (4.3 TB/s; its 34 vector instructions a token and channel
-// are issued in 68% of the cycles, three waves a SIMD); 3 x 4099 x 1000 fp32, 3 taps,
+// are issued in 70% of the cycles, three waves a SIMD); 3 x 4099 x 1000 fp32, 3 taps,
 // 19 and 34 us (5.2 and 4.3 TB/s).
 // A lane owns a vector of channels and a run of consecutive tokens, and slides the
 // last K-1 inputs through registers, so a run reads K-1 tokens that its neighbour

@@ -8,9 +8,10 @@
 // and no two channels share a gate, so nothing of it is a matrix product.  Per token
 // and wave of 16 channels x 16 states the forward issues 30 vector instructions, the
 // backward 91 (78 of them in the walk: 16 to form the states again, 36 to go back,
-// 26 to add over states and channels); 8 x 2048 x 4096 bf16 runs at 76% and 92% of
+// 26 to add over states and channels); 8 x 2048 x 4096 bf16 runs at 79% and 93% of
 // the cycles that issue them, 344 and 904 us, with 1.07 and 1.5 GB to move (3.1 and
-// 1.7 TB/s, where a copy reaches 4.9).
+// 1.7 TB/s, where a copy reaches 4.9).  Where a piece is split, the segments' pass
+// issues 22 (from behind 24), in 83 to 92% of the cycles at 16 states.
 //
 // A lane owns 4 states of a channel, N / 4 lanes a channel, so a workgroup of
 // four waves walks 4 * 64 / (N / 4) channels token by token with their states in
@@ -1040,8 +1041,8 @@ int channels_per_block(int N) { return NT / 64 * 64 / (N / NS); }
 // CU: 512 leave the forward 17% slower (16384 x 2048: 188 against 161 us).  At least 64
 // tokens a segment (3 x 1023 x 1000: 60 + 21 us for the two walks, 64 + 26 with 128
 // tokens).  Every segment's workgroup reads what those before it make, so there are at
-// most 128 (65536 x 256: 436 us a step; 64 segments 587, 256 463), or 256 where a
-// segment is one workgroup (32768 x 64: 151 us, with 128 185).
+// most 128 (65536 x 256: 417 us a step; 64 segments 584, 256 454), or 256 where a
+// segment is one workgroup (32768 x 64: 158 us, with 128 188).
 struct Plan {
     int blocks, nseg, seg;
     Plan(const linrec_scan_desc* d)
